@@ -17,7 +17,7 @@ __all__ = [
     "workspace_bytes", "new_workspace", "topk", "expand", "prune", "tree_mask", "build_tree",
     "verify", "read_status", "clear_status", "Round", "EXPORTS", "heap_build", "HeapRound",
     "verify_sample", "adaptive_budget", "lm_head_topk", "tree_attention", "AttnParams", "HostRounds",
-    "HostInputs", "HostOutputs",
+    "HostInputs", "HostOutputs", "PagedCache",
 ]
 
 F32, BF16 = 0, 1
@@ -31,7 +31,9 @@ EXPORTS = ("dartree_head_init", "dartree_workspace_bytes", "dartree_topk", "dart
            "dartree_timing_read", "dartree_kernel_name", "dartree_heap_workspace_bytes", "dartree_heap_build",
            "dartree_verify_sample", "dartree_adaptive_budget", "dartree_lm_head_workspace_bytes",
            "dartree_lm_head_topk", "dartree_tree_attention_workspace_bytes", "dartree_tree_attention", "dartree_host_session_create",
-           "dartree_host_session_destroy", "dartree_host_stage", "dartree_host_round", "dartree_host_input_bytes")
+           "dartree_host_session_destroy", "dartree_host_stage", "dartree_host_round", "dartree_host_input_bytes",
+           "dartree_paged_workspace_bytes", "dartree_paged_append", "dartree_paged_attention",
+           "dartree_paged_weights", "dartree_paged_evict", "dartree_paged_commit")
 
 
 class DartreeError(RuntimeError):
@@ -62,6 +64,20 @@ class Supertree(ctypes.Structure):
 class AttnParams(ctypes.Structure):
     _fields_ = [("C", ctypes.c_int), ("S", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int),
                 ("D", ctypes.c_int), ("N", ctypes.c_int), ("theta", ctypes.c_float)]
+
+
+class PagedParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("C", "T", "S", "Hq", "Hkv", "D", "page", "n_pages", "max_pages", "dtype")]
+
+
+class PagedCacheDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "table", "n_ctx", "q_start")]
+
+
+class PagedTokens(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("ldq", ctypes.c_int64),
+                ("ldk", ctypes.c_int64), ("ldv", ctypes.c_int64), ("gq", ctypes.c_void_p), ("gk", ctypes.c_void_p),
+                ("pos_base", ctypes.c_void_p), ("eps", ctypes.c_float), ("theta", ctypes.c_float)]
 
 
 class Tree(ctypes.Structure):
@@ -123,6 +139,14 @@ def lib() -> ctypes.CDLL:
         "dartree_host_stage": (i, [vp, P(HostInputs)]),
         "dartree_host_round": (i, [vp, P(HostOutputs), vp]),
         "dartree_host_input_bytes": (sz, [vp, i]),
+        "dartree_paged_workspace_bytes": (sz, [P(PagedParams)]),
+        "dartree_paged_append": (i, [P(PagedParams), P(PagedTokens), P(PagedCacheDesc), P(Tree), vp, vp, sz, vp]),
+        "dartree_paged_attention": (i, [P(PagedParams), vp, P(PagedCacheDesc), P(Tree), ctypes.c_float, vp, vp, vp, sz,
+                                        vp]),
+        "dartree_paged_weights": (i, [P(PagedParams), vp, vp, P(PagedCacheDesc), P(Tree), ctypes.c_float,
+                                      ctypes.c_float, vp, vp, sz, vp]),
+        "dartree_paged_evict": (i, [P(PagedParams), P(PagedCacheDesc), vp, i, i, i, vp, i, vp, vp, vp, vp, sz, vp]),
+        "dartree_paged_commit": (i, [P(PagedParams), P(PagedCacheDesc), vp, vp, i, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -653,3 +677,182 @@ def heap_build(E, Wq, base, hidden, anchor, K, B, beta, stream=None):
     _keep(stream, h.ws, h.wqt)
     out["_keep"] = (h.ws, h.wqt)
     return out
+
+
+class PagedCache:
+    """One layer's key/value cache kept in pages and the calls on it (dartree_paged_*):
+    append, attention and weights for a step's new tokens, evict, commit.
+
+      k_pages, v_pages  [n_pages, Hkv, page, D], bf16 or float32 (keys rotated)
+      table             [C, max_pages] int32, the page of each run of `page` rows
+      n_ctx             [C] int32, rows cached before the step's new tokens
+      Hq, S             query heads; most new tokens of a request
+      q_start           [C + 1] int32 first rows of q (T rows in all); None: S tokens of
+                        every request, or a tree's S slots
+      ws                a workspace to use (shared by calls that follow one another on
+                        the device); allocated when None
+
+    The tensors are read at every call: a serving loop changes table, n_ctx and q_start
+    in place. Nothing is allocated by a call that is given its outputs, so it can be
+    captured into a CUDA graph. read_status(cache.ws) tells what the kernels found wrong
+    in lengths and tables. Calls run on `stream` (default: the current stream of the
+    pages' device) and outputs they allocate belong to it; the workspace is made on the
+    stream that is current when the object is.
+    """
+
+    def __init__(self, k_pages, v_pages, table, n_ctx, Hq, S, T=None, q_start=None, ws=None):
+        _need(k_pages, "k_pages")
+        if k_pages.dim() != 4:
+            raise ValueError("k_pages must be [n_pages, Hkv, page, D]")
+        self.n_pages, self.Hkv, self.page, self.D = k_pages.shape
+        self.device, self.dtype = k_pages.device, k_pages.dtype
+        self.Hq, self.S = int(Hq), int(S)
+        if not isinstance(table, torch.Tensor) or table.dim() != 2:
+            raise ValueError("table must be [C, max_pages]")
+        self.C, self.max_pages = table.shape
+        if T is None:
+            if q_start is not None:
+                raise ValueError("T (rows of q) is needed with q_start")
+            T = self.C * self.S
+        self.T = int(T)
+        self._need(v_pages, "v_pages", self.dtype, k_pages.shape)
+        self._need(table, "table", torch.int32)
+        self._need(n_ctx, "n_ctx", torch.int32, (self.C,))
+        if q_start is not None:
+            self._need(q_start, "q_start", torch.int32, (self.C + 1,))
+        self.k_pages, self.v_pages, self.table, self.n_ctx, self.q_start = k_pages, v_pages, table, n_ctx, q_start
+        self.p = PagedParams(self.C, self.T, self.S, self.Hq, self.Hkv, self.D, self.page, self.n_pages,
+                             self.max_pages, _dtype_code(k_pages))
+        self._m = PagedCacheDesc(k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(), n_ctx.data_ptr(),
+                                 q_start.data_ptr() if q_start is not None else None)
+        n = lib().dartree_paged_workspace_bytes(ctypes.byref(self.p))
+        if n == 0:
+            raise DartreeError(EUNSUPPORTED, "dartree_paged_workspace_bytes")
+        if ws is None:
+            ws = new_workspace(n, self.device)
+        else:
+            self._need(ws, "ws", torch.uint8)
+        self.ws = ws
+        self._wsp = (ctypes.c_void_p(ws.data_ptr()), ws.numel())
+        self.rows = self.max_pages * self.page
+
+    def _need(self, t, name, dtype=None, shape=None) -> int:
+        ptr = _need(t, name, dtype, shape)
+        if t.device != self.device:
+            raise ValueError(f"{name} must be on {self.device}, got {t.device}")
+        return ptr
+
+    def _run(self, name, stream, *args):
+        s = stream if stream is not None else torch.cuda.current_stream(self.device)
+        if torch.cuda.current_device() == self.device.index:
+            return _call(name, *args, *self._wsp, ctypes.c_void_p(s.cuda_stream))
+        with torch.cuda.device(self.device):
+            _call(name, *args, *self._wsp, ctypes.c_void_p(s.cuda_stream))
+
+    def _new(self, make, shape, dtype, stream):
+        """An output tensor that belongs to the stream of the call that fills it."""
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(self.device)):
+            return make(shape, dtype=dtype, device=self.device)
+
+    def _tree(self, tree, *keys):
+        if tree is None:
+            return None
+        shapes = dict(mask=(self.C, self.S, self.S), pos=(self.C, self.S), n_nodes=(self.C,))
+        for k in keys:
+            self._need(tree[k], f"tree[{k!r}]", torch.uint8 if k == "mask" else torch.int32, shapes[k])
+        return ctypes.byref(_tree_struct({k: tree[k] for k in keys}))
+
+    def _heads(self, t, name, heads):
+        """A [T, heads, D] tensor whose tokens may lie further apart: (address, elements between tokens)."""
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch tensor")
+        if t.device != self.device or t.dtype != self.dtype or tuple(t.shape) != (self.T, heads, self.D):
+            raise ValueError(f"{name} must be {self.dtype} {(self.T, heads, self.D)} on {self.device}, got {t.dtype} "
+                             f"{tuple(t.shape)} on {t.device}")
+        ld, h, one = t.stride()
+        if (one != 1 and self.D > 1) or (h != self.D and heads > 1):
+            raise ValueError(f"{name}: the heads of a token must be contiguous")
+        return t.data_ptr(), (ld if self.T > 1 else heads * self.D)
+
+    def append(self, q, k, v, q_gain=None, k_gain=None, eps=1e-6, theta=1.0e6, tree=None, pos_base=None, out=None,
+               stream=None):
+        """Head norms (with gains [D]), rotation and store of the new tokens (dartree_paged_append):
+        q [T, Hq, D], k and v [T, Hkv, D], parts of one tensor or not -> rotated queries [T, Hq, D]."""
+        qp, ldq = self._heads(q, "q", self.Hq)
+        kp, ldk = self._heads(k, "k", self.Hkv)
+        vp, ldv = self._heads(v, "v", self.Hkv)
+        gains = [None if g is None else self._need(g, n, self.dtype, (self.D,))
+                 for g, n in ((q_gain, "q_gain"), (k_gain, "k_gain"))]
+        base = None if pos_base is None else self._need(pos_base, "pos_base", torch.int32, (self.C,))
+        if out is None:
+            out = self._new(torch.empty, (self.T, self.Hq, self.D), self.dtype, stream)
+        op = self._need(out, "out", self.dtype, (self.T, self.Hq, self.D))
+        x = PagedTokens(qp, kp, vp, ldq, ldk, ldv, gains[0], gains[1], base, float(eps), float(theta))
+        self._run("dartree_paged_append", stream, ctypes.byref(self.p), ctypes.byref(x), ctypes.byref(self._m),
+                  self._tree(tree, "pos", "n_nodes"), ctypes.c_void_p(op))
+        return out
+
+    def attention(self, q, tree=None, scale=None, out=None, lse=None, stream=None):
+        """Attention of the new tokens, already appended, over the pages (dartree_paged_attention):
+        q [T, Hq, D] rotated -> out [T, Hq, D]; lse [T, Hq] float32 is filled when given."""
+        qp = self._need(q, "q", self.dtype, (self.T, self.Hq, self.D))
+        if out is None:
+            out = self._new(torch.empty, (self.T, self.Hq, self.D), self.dtype, stream)
+        op = self._need(out, "out", self.dtype, (self.T, self.Hq, self.D))
+        lp = None if lse is None else ctypes.c_void_p(self._need(lse, "lse", torch.float32, (self.T, self.Hq)))
+        self._run("dartree_paged_attention", stream, ctypes.byref(self.p), ctypes.c_void_p(qp), ctypes.byref(self._m),
+                  self._tree(tree, "mask", "n_nodes"), float(scale or 0.0), ctypes.c_void_p(op), lp)
+        return out
+
+    def weights(self, q, lse, weights, tree=None, scale=None, decay=1.0, stream=None):
+        """weights [C, Hkv, max_pages * page] float32 decayed and increased by the attention weight each
+        cached row receives from the new tokens (dartree_paged_weights)."""
+        qp = self._need(q, "q", self.dtype, (self.T, self.Hq, self.D))
+        lp = self._need(lse, "lse", torch.float32, (self.T, self.Hq))
+        wp = self._need(weights, "weights", torch.float32, (self.C, self.Hkv, self.rows))
+        self._run("dartree_paged_weights", stream, ctypes.byref(self.p), ctypes.c_void_p(qp), ctypes.c_void_p(lp),
+                  ctypes.byref(self._m), self._tree(tree, "mask", "n_nodes"), float(scale or 0.0), float(decay),
+                  ctypes.c_void_p(wp))
+        return weights
+
+    def evict(self, weights, budget, dst_table, sink=0, recent=0, keep=None, n_out=None, weights_out=None,
+              stream=None):
+        """The first `sink`, the last `recent` and the heaviest other rows of every request and key/value
+        head, `budget` in all, copied into the pages of dst_table [C, dst_pages] (dartree_paged_evict) ->
+        dict(keep [C, Hkv, budget], n [C], weights [C, Hkv, dst_pages * page])."""
+        budget = int(budget)
+        wp = self._need(weights, "weights", torch.float32, (self.C, self.Hkv, self.rows))
+        if not isinstance(dst_table, torch.Tensor) or dst_table.dim() != 2:
+            raise ValueError("dst_table must be [C, dst_pages]")
+        pages = dst_table.shape[1]
+        dp = self._need(dst_table, "dst_table", torch.int32, (self.C, pages))
+
+        def output(t, name, dtype, shape, new):
+            if t is None:
+                t = self._new(new, shape, dtype, stream)
+            self._need(t, name, dtype, shape)
+            return t
+
+        keep = output(keep, "keep", torch.int32, (self.C, self.Hkv, max(budget, 0)), torch.empty)
+        n_out = output(n_out, "n_out", torch.int32, (self.C,), torch.empty)
+        weights_out = output(weights_out, "weights_out", torch.float32, (self.C, self.Hkv, pages * self.page),
+                             torch.zeros)
+        self._run("dartree_paged_evict", stream, ctypes.byref(self.p), ctypes.byref(self._m), ctypes.c_void_p(wp),
+                  budget, int(sink), int(recent), ctypes.c_void_p(dp), pages, ctypes.c_void_p(keep.data_ptr()),
+                  ctypes.c_void_p(n_out.data_ptr()), ctypes.c_void_p(weights_out.data_ptr()))
+        return dict(keep=keep, n=n_out, weights=weights_out)
+
+    def commit(self, path, accepted_len, n_out=None, stream=None):
+        """The accepted path [C, L] of each request's tree moved behind the root's row
+        (dartree_paged_commit) -> rows cached then [C] (n_out may be the cache's n_ctx)."""
+        if not isinstance(path, torch.Tensor) or path.dim() != 2:
+            raise ValueError("path must be [C, L]")
+        L = path.shape[1]
+        pp = self._need(path, "path", torch.int32, (self.C, L))
+        ap = self._need(accepted_len, "accepted_len", torch.int32, (self.C,))
+        if n_out is None:
+            n_out = self._new(torch.empty, (self.C,), torch.int32, stream)
+        np_ = self._need(n_out, "n_out", torch.int32, (self.C,))
+        self._run("dartree_paged_commit", stream, ctypes.byref(self.p), ctypes.byref(self._m), ctypes.c_void_p(pp),
+                  ctypes.c_void_p(ap), int(L), ctypes.c_void_p(np_))
+        return n_out

@@ -555,6 +555,178 @@ int dartree_tree_attention(const dartree_attn_params* p, const void* q, const vo
                                  as_stream(stream));
 }
 
+// --------------------------------------------------------------------------- paged cache
+
+}  // extern "C"
+
+namespace {
+
+bool al16(const void* x) { return x && reinterpret_cast<uintptr_t>(x) % 16 == 0; }
+
+// Workspace of the paged calls: status word, the counts of an eviction, the partial
+// results of an attention.
+struct PagedLayout {
+    size_t counts, part, total;
+};
+PagedLayout paged_layout(const PagedArgs& a) {
+    PagedLayout l{};
+    l.counts = kAlign;
+    l.part = l.counts + up(size_t(a.C) * 4);
+    l.total = l.part + up(paged_attention_part_bytes(a));
+    return l;
+}
+
+int check_paged(const dartree_paged_params* p, PagedArgs* a) {
+    if (!p || p->C < 0 || p->T < 0 || p->S < 1 || p->Hq < 1 || p->Hkv < 1 || p->Hq % p->Hkv != 0 || p->n_pages < 0 ||
+        p->max_pages < 0)
+        return DARTREE_EINVAL;
+    if (!dtype_ok(p->dtype)) return DARTREE_EDTYPE;
+    if ((p->D != 64 && p->D != 128) || p->Hq / p->Hkv > 128 || p->page < 16 || p->page > 256 ||
+        (p->page & (p->page - 1)) != 0)
+        return DARTREE_EUNSUPPORTED;
+    int lg = 4;
+    while ((1 << lg) < p->page) ++lg;
+    // row numbers, the rows of q and the launches' CTA counts stay below 2^31
+    const int64_t most = int64_t(1) << 31, rows = int64_t(p->max_pages) << lg;
+    const int64_t heads = int64_t(p->C) * p->Hkv;
+    if (rows + p->S >= most || int64_t(p->C) * p->S >= most || heads >= most ||
+        int64_t(p->C) * p->S * p->Hq >= most || heads * (rows / 128 + 1) >= most)
+        return DARTREE_EUNSUPPORTED;
+    *a = PagedArgs{};
+    a->C = p->C, a->T = p->T, a->S = p->S, a->Hq = p->Hq, a->Hkv = p->Hkv, a->D = p->D, a->page = p->page;
+    a->log2_page = lg, a->n_pages = p->n_pages, a->max_pages = p->max_pages, a->dtype = p->dtype;
+    return DARTREE_OK;
+}
+
+// Pools, table and lengths; `tokens`: the call has new tokens in T rows of q.
+int check_paged_cache(const dartree_paged_cache* m, const dartree_tree* tree, bool tokens, PagedArgs* a) {
+    if (!m || !m->n_ctx || a->n_pages < 1 || a->max_pages < 1 || !m->table || !al16(m->k) || !al16(m->v))
+        return DARTREE_EINVAL;
+    a->k = m->k, a->v = m->v, a->table = m->table, a->n_ctx = m->n_ctx;
+    if (!tokens) return DARTREE_OK;
+    if (m->q_start ? tree != nullptr : int64_t(a->C) * a->S != a->T) return DARTREE_EINVAL;
+    a->q_start = m->q_start;
+    if (tree) {
+        if (!tree->n_nodes) return DARTREE_EINVAL;
+        a->n_nodes = tree->n_nodes, a->mask = tree->mask, a->pos = tree->pos;
+    }
+    return DARTREE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t dartree_paged_workspace_bytes(const dartree_paged_params* p) {
+    PagedArgs a;
+    if (check_paged(p, &a) != DARTREE_OK) return 0;
+    return paged_layout(a).total;
+}
+
+int dartree_paged_append(const dartree_paged_params* p, const dartree_paged_tokens* x, const dartree_paged_cache* cache,
+                         const dartree_tree* tree, void* q_out, void* ws, size_t ws_bytes, void* stream) {
+    PagedArgs a;
+    if (int e = check_paged(p, &a)) return e;
+    if (!x || !(x->theta > 0.f) || !isfinite(x->theta)) return DARTREE_EINVAL;
+    if ((x->gq || x->gk) && !(x->eps > 0.f && isfinite(x->eps))) return DARTREE_EINVAL;
+    if (a.C == 0 || a.T == 0) return DARTREE_OK;
+    if (int e = check_paged_cache(cache, tree, true, &a)) return e;
+    if (tree && !tree->pos) return DARTREE_EINVAL;
+    const int64_t vec = a.dtype == DARTREE_BF16 ? 8 : 4;
+    if (!al16(x->q) || !al16(x->k) || !al16(x->v) || !al16(q_out) || (x->gq && !al16(x->gq)) ||
+        (x->gk && !al16(x->gk)) || x->ldq % vec != 0 || x->ldk % vec != 0 || x->ldv % vec != 0 ||
+        x->ldq < int64_t(a.Hq) * a.D || x->ldk < int64_t(a.Hkv) * a.D || x->ldv < int64_t(a.Hkv) * a.D)
+        return DARTREE_EINVAL;
+    if (x->q == q_out && x->ldq != int64_t(a.Hq) * a.D) return DARTREE_EINVAL;
+    if (int e = check_ws(ws, ws_bytes, paged_layout(a).total)) return e;
+    a.status = at<int>(ws, 0);
+    return launch_paged_append(a, x->q, x->k, x->v, x->ldq, x->ldk, x->ldv, x->gq, x->gk, x->pos_base, x->eps,
+                               double(x->theta), q_out, as_stream(stream));
+}
+
+static int check_paged_scores(const dartree_paged_params* p, const dartree_tree* tree, const void* q,
+                              const dartree_paged_cache* cache, float* scale, PagedArgs* a, bool* empty) {
+    *empty = false;
+    if (int e = check_paged(p, a)) return e;
+    if (a->dtype != DARTREE_BF16) return DARTREE_EUNSUPPORTED;  // bf16 tensor-core operands
+    if (!(*scale >= 0.f) || !isfinite(*scale)) return DARTREE_EINVAL;
+    if (*scale == 0.f) *scale = float(1.0 / sqrt(double(a->D)));
+    if (a->C == 0 || a->T == 0) {
+        *empty = true;
+        return DARTREE_OK;
+    }
+    if (int e = check_paged_cache(cache, tree, true, a)) return e;
+    if ((tree && !tree->mask) || !al16(q)) return DARTREE_EINVAL;
+    return DARTREE_OK;
+}
+
+int dartree_paged_attention(const dartree_paged_params* p, const void* q, const dartree_paged_cache* cache,
+                            const dartree_tree* tree, float scale, void* out, float* lse, void* ws, size_t ws_bytes,
+                            void* stream) {
+    PagedArgs a;
+    bool empty;
+    if (int e = check_paged_scores(p, tree, q, cache, &scale, &a, &empty)) return e;
+    if (empty) return DARTREE_OK;
+    if (!al16(out) || (lse && reinterpret_cast<uintptr_t>(lse) % 4 != 0)) return DARTREE_EINVAL;
+    const PagedLayout l = paged_layout(a);
+    if (int e = check_ws(ws, ws_bytes, l.total)) return e;
+    a.status = at<int>(ws, 0);
+    return launch_paged_attention(a, q, scale, out, lse, at<void>(ws, l.part), as_stream(stream));
+}
+
+int dartree_paged_weights(const dartree_paged_params* p, const void* q, const float* lse,
+                          const dartree_paged_cache* cache, const dartree_tree* tree, float scale, float decay,
+                          float* weights, void* ws, size_t ws_bytes, void* stream) {
+    PagedArgs a;
+    bool empty;
+    if (!(decay >= 0.f && decay <= 1.f)) return DARTREE_EINVAL;
+    if (int e = check_paged_scores(p, tree, q, cache, &scale, &a, &empty)) return e;
+    if (a.C == 0) return DARTREE_OK;
+    if (empty) {  // no new token anywhere: the cached rows' weights still decay
+        if (int e = check_paged_cache(cache, nullptr, false, &a)) return e;
+        if (!weights || !cache->q_start) return DARTREE_EINVAL;
+        a.q_start = cache->q_start;
+    }
+    if (!weights || (!empty && !lse)) return DARTREE_EINVAL;
+    if (int e = check_ws(ws, ws_bytes, paged_layout(a).total)) return e;
+    a.status = at<int>(ws, 0);
+    return launch_paged_weights(a, q, lse, scale, decay, weights, as_stream(stream));
+}
+
+int dartree_paged_evict(const dartree_paged_params* p, const dartree_paged_cache* cache, const float* weights,
+                        int budget, int sink, int recent, const int32_t* dst_table, int dst_pages, int32_t* keep,
+                        int32_t* n_out, float* weights_out, void* ws, size_t ws_bytes, void* stream) {
+    PagedArgs a;
+    if (int e = check_paged(p, &a)) return e;
+    if (budget < 1 || sink < 0 || recent < 0 || int64_t(sink) + recent > budget || dst_pages < 1 ||
+        (int64_t(dst_pages) << a.log2_page) < budget)
+        return DARTREE_EINVAL;
+    if (int64_t(a.C) * a.Hkv * budget >= (int64_t(1) << 31) || (int64_t(dst_pages) << a.log2_page) >= (int64_t(1) << 31))
+        return DARTREE_EUNSUPPORTED;
+    if (a.C == 0) return DARTREE_OK;
+    if (int e = check_paged_cache(cache, nullptr, false, &a)) return e;
+    if (!weights || !dst_table || !keep || !n_out) return DARTREE_EINVAL;
+    const PagedLayout l = paged_layout(a);
+    if (int e = check_ws(ws, ws_bytes, l.total)) return e;
+    a.status = at<int>(ws, 0);
+    return launch_paged_evict(a, weights, budget, sink, recent, dst_table, dst_pages, keep, n_out, weights_out,
+                              at<int32_t>(ws, l.counts), as_stream(stream));
+}
+
+int dartree_paged_commit(const dartree_paged_params* p, const dartree_paged_cache* cache, const int32_t* path,
+                         const int32_t* accepted_len, int L, int32_t* n_out, void* ws, size_t ws_bytes, void* stream) {
+    PagedArgs a;
+    if (int e = check_paged(p, &a)) return e;
+    if (L < 1) return DARTREE_EINVAL;
+    if (L > DARTREE_MAX_L) return DARTREE_EUNSUPPORTED;
+    if (a.C == 0) return DARTREE_OK;
+    if (int e = check_paged_cache(cache, nullptr, false, &a)) return e;
+    if (!path || !accepted_len || !n_out) return DARTREE_EINVAL;
+    if (int e = check_ws(ws, ws_bytes, paged_layout(a).total)) return e;
+    a.status = at<int>(ws, 0);
+    return launch_paged_commit(a, path, accepted_len, L, n_out, as_stream(stream));
+}
+
 int dartree_adaptive_budget(int C, int* B, int* W) {
     if (C < 1 || !B || !W) return DARTREE_EINVAL;
     const bool reduced = C >= DARTREE_REDUCED_BUDGET_FROM_C;

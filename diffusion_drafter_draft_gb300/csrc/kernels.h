@@ -30,7 +30,8 @@ std::recursive_mutex& side_mutex();
 enum KernelId {
     KID_TOPK_ROWS = 0, KID_TOPK_STREAM, KID_GEMM, KID_CONTRACT, KID_EXPAND_G, KID_GATHER, KID_SELECT,
     KID_STATE, KID_HEAP, KID_FINISH, KID_PRUNE, KID_MASK, KID_ROWMAX, KID_WALK, KID_ROWSAMPLE, KID_LMHEAD,
-    KID_LMMERGE, KID_ATTN_PREP, KID_ATTN, KID_ATTN_COMBINE, KID_OTHER,
+    KID_LMMERGE, KID_ATTN_PREP, KID_ATTN, KID_ATTN_COMBINE, KID_PAGED_APPEND, KID_PAGED_ATTN,
+    KID_PAGED_COMBINE, KID_PAGED_WEIGHTS, KID_PAGED_SELECT, KID_PAGED_MOVE, KID_PAGED_COMMIT, KID_OTHER,
     KID_COUNT
 };
 // Brackets the launches of its scope with timing events when timing is enabled.
@@ -246,6 +247,34 @@ int launch_tree_attention(int C, int S, int Hq, int Hkv, int N, double theta, co
                           const void* v_tree, const void* k_cache, const void* vt_cache, const int32_t* n_ctx,
                           const uint8_t* mask, const int32_t* pos, const int32_t* n_nodes, void* out, void* ws,
                           const AttnPlan& pl, cudaStream_t stream);
+
+// Paged cache: what every kernel gets of the call (checked by the caller).
+struct PagedArgs {
+    int C, T, S, Hq, Hkv, D, page, log2_page, n_pages, max_pages, dtype;
+    void* k;
+    void* v;
+    const int32_t* table;
+    const int32_t* n_ctx;
+    const int32_t* q_start;
+    // tree of the new tokens (null: causal)
+    const uint8_t* mask;
+    const int32_t* pos;
+    const int32_t* n_nodes;
+    int* status;
+};
+int launch_paged_append(const PagedArgs& a, const void* q, const void* k, const void* v, int64_t ldq, int64_t ldk,
+                        int64_t ldv, const void* gq, const void* gk, const int32_t* pos_base, float eps, double theta,
+                        void* q_out, cudaStream_t stream);
+size_t paged_attention_part_bytes(const PagedArgs& a);
+int launch_paged_attention(const PagedArgs& a, const void* q, float scale, void* out, float* lse, void* part,
+                           cudaStream_t stream);
+int launch_paged_weights(const PagedArgs& a, const void* q, const float* lse, float scale, float decay,
+                         float* weights, cudaStream_t stream);
+int launch_paged_evict(const PagedArgs& a, const float* weights, int budget, int sink, int recent,
+                       const int32_t* dst_table, int dst_pages, int32_t* keep, int32_t* n_out, float* weights_out,
+                       int32_t* counts, cudaStream_t stream);
+int launch_paged_commit(const PagedArgs& a, const int32_t* path, const int32_t* accepted_len, int L, int32_t* n_out,
+                        cudaStream_t stream);
 
 // Bounded-wait self-test (which = 0: mbarrier, 1: grid barrier on ctr).
 int launch_selftest_wait(int which, unsigned* ctr, int* status, uint64_t limit_ns, cudaStream_t stream);

@@ -288,6 +288,140 @@ DARTREE_API int dartree_tree_attention(const dartree_attn_params* p, const void*
                                        const int32_t* n_ctx, const dartree_tree* tree, void* out, void* ws,
                                        size_t ws_bytes, void* stream);
 
+/* One layer of the target model over a key/value cache kept in pages: the calls a
+ * serving loop makes around the trees built above. A pool of pages holds the rows of
+ * all requests, pages [n_pages, Hkv, page, D] for keys and for values; row j of request
+ * c is row j % page of page table[c, j / page]. Keys are stored rotated. New tokens of
+ * request c take the rows behind its n_ctx[c] cached ones:
+ *   q_start NULL  every request has S new tokens (T = C * S), token i of request c in
+ *                 row c * S + i of q
+ *   q_start       [C + 1], ascending: request c has q_start[c+1] - q_start[c] <= S new
+ *                 tokens, in rows q_start[c] .. q_start[c+1] - 1 of q; rows outside
+ *                 [q_start[0], q_start[C]) are neither read nor written
+ *   tree          (q_start NULL only) the new tokens are the S slots of a verification
+ *                 tree; slots from tree->n_nodes[c] on are not stored, and their output
+ *                 rows are zero
+ * A new token sees all n_ctx cached rows and, of the new ones, those up to its own
+ * (causal), or the slots tree->mask [C, S, S] marks.
+ * Checked on the device, with DARTREE_EINTERNAL in the status word of ws: lengths below
+ * zero, more than S new tokens (the ones behind the S-th are left out), q_start outside
+ * [0, T], rows past the block table's capacity max_pages * page (not stored and not
+ * seen), and table entries outside [0, n_pages) (nothing is read from or written to
+ * such a page; results that needed it are finite but unspecified). Two rows of the
+ * batch's new tokens never share a page row: pages that requests share hold cached rows
+ * only.
+ * Workspace of all calls: dartree_paged_workspace_bytes. */
+typedef struct {
+    int C;          /* requests */
+    int T;          /* rows of q (C * S without q_start) */
+    int S;          /* most new tokens of one request, >= 1 */
+    int Hq, Hkv;    /* query heads (a multiple of Hkv, at most 128 per key/value head), key/value heads */
+    int D;          /* head dimension, 64 or 128 */
+    int page;       /* rows of a page: a power of two, 16..256 */
+    int n_pages;    /* pages of the pool */
+    int max_pages;  /* entries of one row of the block table */
+    int dtype;      /* dartree_dtype of q, k, v and the pages */
+} dartree_paged_params;
+
+typedef struct {
+    void* k;                /* [n_pages, Hkv, page, D] keys, rotated */
+    void* v;                /* [n_pages, Hkv, page, D] values */
+    const int32_t* table;   /* [C, max_pages] page of each run of `page` rows */
+    const int32_t* n_ctx;   /* [C] rows cached before the new tokens */
+    const int32_t* q_start; /* [C + 1] or NULL */
+} dartree_paged_cache;
+
+DARTREE_API size_t dartree_paged_workspace_bytes(const dartree_paged_params* p);
+
+/* Head norms, position rotation and store of a layer's new tokens in one pass.
+ *   q, k, v     rows of Hq, Hkv and Hkv heads of D values; consecutive tokens lie ldq,
+ *               ldk, ldv elements apart (16-byte multiples, at least the row), so the
+ *               three may be parts of one projection's output
+ *   gq, gk      [D] gains of the norms x * g / sqrt(mean(x^2) + eps) over each query
+ *               and key head, or NULL: no norm. Values are stored as they are.
+ *   pos_base    [C] rotary position of each request's first new token (of a tree's
+ *               root), or NULL: n_ctx[c]. Token i sits at position base + i, slot j of a
+ *               tree at base + tree->pos[c, j]; pairs (i, i + D/2) turn by position *
+ *               theta^(-2i/D) as in dartree_tree_attention.
+ *   q_out       [T, Hq, D]
+ * Norm and rotation in fp32 (angles reduced in double), rounded once to dtype. All
+ * pointers 16-byte aligned. q_out may be q itself when ldq = Hq * D. */
+typedef struct {
+    const void* q;
+    const void* k;
+    const void* v;
+    int64_t ldq, ldk, ldv;
+    const void* gq;
+    const void* gk;
+    const int32_t* pos_base;
+    float eps;    /* > 0 (unused without gains) */
+    float theta;  /* > 0 */
+} dartree_paged_tokens;
+DARTREE_API int dartree_paged_append(const dartree_paged_params* p, const dartree_paged_tokens* x,
+                                     const dartree_paged_cache* cache, const dartree_tree* tree, void* q_out,
+                                     void* ws, size_t ws_bytes, void* stream);
+
+/* Attention of the new tokens (their keys and values already stored) over the pages.
+ *   q     [T, Hq, D] rotated queries; query head h reads key/value head h / (Hq / Hkv)
+ *   scale factor of the scores, > 0 and finite (0: 1 / sqrt(D))
+ *   out   [T, Hq, D]; a token that sees no row (a tree slot with an empty mask row and
+ *         no context) gives zeros
+ *   lse   [T, Hq] float, natural logarithm of the sum of exponentials of a row's scaled
+ *         scores (-inf for a row that sees nothing), or NULL
+ * bf16 only (DARTREE_EUNSUPPORTED otherwise). Scores and sums in fp32; probabilities
+ * are rounded to bf16 for the product with the values. Page rows behind a request's
+ * last one (n_ctx + its new tokens) may hold anything, infinities and NaN included; the
+ * rows it holds are finite. */
+DARTREE_API int dartree_paged_attention(const dartree_paged_params* p, const void* q,
+                                        const dartree_paged_cache* cache, const dartree_tree* tree, float scale,
+                                        void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* Attention weight each cached row receives, summed over the new tokens and the query
+ * heads of its key/value head: with N = max_pages * page, for every row j that request
+ * c holds (new ones included)
+ *   weights[c, g, j] = decay * weights[c, g, j] + sum exp(scale <q, k_j> - lse)
+ * over the tokens that see j; a new row starts from 0 instead of weights[c, g, j].
+ * Rows past the new ones are not touched.
+ *   lse     [T, Hq] from dartree_paged_attention with the same arguments
+ *   weights [C, Hkv, N] float, in and out; decay in [0, 1]
+ * The sums are taken in a fixed order: equal inputs give equal results. bf16 only. */
+DARTREE_API int dartree_paged_weights(const dartree_paged_params* p, const void* q, const float* lse,
+                                      const dartree_paged_cache* cache, const dartree_tree* tree, float scale,
+                                      float decay, float* weights, void* ws, size_t ws_bytes, void* stream);
+
+/* Eviction: per request and key/value head, of the n_ctx[c] cached rows the first
+ * `sink`, the last `recent` and, up to `budget` in all, those of the largest weights are
+ * kept (equal weights: the lowest row; NaN counts below every number); all of them when
+ * n_ctx[c] <= budget. The kept rows are copied in their order into rows 0.. of the
+ * pages of a second block table, whose pages are none of the first's (the first's are
+ * left as they were, for requests that share them); rotated keys keep their angle,
+ * so later tokens go on at their old positions (pos_base).
+ *   weights      [C, Hkv, max_pages * page] float
+ *   budget       >= 1, at most dst_pages * page; sink, recent >= 0, sink + recent <= budget
+ *   dst_table    [C, dst_pages]
+ *   keep         [C, Hkv, budget] output: the kept rows, ascending, -1 behind them
+ *   n_out        [C] output: min(n_ctx, budget) (may be cache->n_ctx itself)
+ *   weights_out  [C, Hkv, dst_pages * page] output: the kept rows' weights (others not
+ *                touched), or NULL
+ * T, S, Hq and q_start are not used. Pages of either dtype. */
+DARTREE_API int dartree_paged_evict(const dartree_paged_params* p, const dartree_paged_cache* cache,
+                                    const float* weights, int budget, int sink, int recent,
+                                    const int32_t* dst_table, int dst_pages, int32_t* keep, int32_t* n_out,
+                                    float* weights_out, void* ws, size_t ws_bytes, void* stream);
+
+/* After dartree_verify: the accepted path of each request's tree moves behind the
+ * root's row, rows n_ctx + path[c, i] -> n_ctx + 1 + i for i < accepted_len[c], and
+ * n_out[c] = n_ctx[c] + 1 + accepted_len[c] rows are cached.
+ *   path          [C, L] slot ids as dartree_verify writes them, each in 1..S-1
+ *                 (else DARTREE_EINTERNAL in the status word; that row is not moved)
+ *   accepted_len  [C], 0..L (clamped to it, and to S - 1)
+ *   L             1..DARTREE_MAX_L
+ *   n_out         [C] (may be cache->n_ctx itself)
+ * T, Hq and q_start are not used. Pages of either dtype. */
+DARTREE_API int dartree_paged_commit(const dartree_paged_params* p, const dartree_paged_cache* cache,
+                                     const int32_t* path, const int32_t* accepted_len, int L, int32_t* n_out,
+                                     void* ws, size_t ws_bytes, void* stream);
+
 /* Node budget and width for a batch of C concurrent requests (DARTree blog post,
  * section 4.4: at concurrency 4 the budget B shrinks from 64 to 32 and the width W
  * from 12 to 3; at concurrency 1 and 2 the defaults run). Reading: the reduced pair
@@ -424,7 +558,7 @@ DARTREE_API int dartree_selftest_wait(void* ws, size_t ws_bytes, int which, unsi
  * device time. Kernel ids 0..DARTREE_NUM_KERNEL_IDS-1, named by
  * dartree_kernel_name. Not for launches captured into a CUDA graph; adds two
  * event records per launch while on. */
-#define DARTREE_NUM_KERNEL_IDS 15
+#define DARTREE_NUM_KERNEL_IDS 28
 DARTREE_API int dartree_timing(int enable);
 DARTREE_API int dartree_timing_read(int kernel_id, int* launches, double* total_ms);
 DARTREE_API const char* dartree_kernel_name(int kernel_id);

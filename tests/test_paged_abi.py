@@ -1,0 +1,148 @@
+"""The paged-cache entry points reject bad arguments on the host, before any CUDA call
+(no GPU needed; the fake pointers are never dereferenced)."""
+import ctypes
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def dd():
+    from diffusion_drafter_draft_gb300 import _build
+    _build.build()
+    import diffusion_drafter_draft_gb300 as m
+    m.lib()
+    return m
+
+
+FAKE, WS = ctypes.c_void_p(256), ctypes.c_void_p(1 << 20)
+GOOD = dict(C=2, T=6, S=3, Hq=8, Hkv=2, D=128, page=64, n_pages=8, max_pages=4, dtype=1)
+
+
+def _p(dd, **kw):
+    return dd.PagedParams(**{**GOOD, **kw})
+
+
+def _m(dd, k=256, v=256, table=256, n_ctx=256, q_start=None):
+    return dd.PagedCacheDesc(k, v, table, n_ctx, q_start)
+
+
+def _x(dd, **kw):
+    d = dict(q=256, k=256, v=256, ldq=1024, ldk=256, ldv=256, gq=256, gk=256, pos_base=None, eps=1e-6, theta=1e6)
+    return dd.PagedTokens(**{**d, **kw})
+
+
+def _tree(dd, mask=256, pos=256, n_nodes=256):
+    return ctypes.byref(dd.Tree(None, None, None, None, n_nodes, mask, pos))
+
+
+BAD = [(dict(C=-1), "EINVAL"), (dict(S=0), "EINVAL"), (dict(T=-1), "EINVAL"), (dict(Hq=7), "EINVAL"),
+       (dict(Hkv=0), "EINVAL"), (dict(dtype=5), "EDTYPE"), (dict(D=96), "EUNSUPPORTED"),
+       (dict(D=256), "EUNSUPPORTED"), (dict(page=8), "EUNSUPPORTED"), (dict(page=48), "EUNSUPPORTED"),
+       (dict(page=512), "EUNSUPPORTED"), (dict(Hq=258, Hkv=2), "EUNSUPPORTED"),
+       (dict(page=256, max_pages=1 << 23), "EUNSUPPORTED"),   # 2^31 rows
+       (dict(C=1 << 15, S=1 << 16, T=1 << 30), "EUNSUPPORTED")]
+
+
+@pytest.mark.parametrize("kw,err", BAD)
+def test_sizes(dd, kw, err):
+    L, code, p = dd.lib(), getattr(dd, err), _p(dd, **kw)
+    b, m, x = ctypes.byref(p), _m(dd), _x(dd)
+    assert L.dartree_paged_workspace_bytes(b) == 0
+    assert L.dartree_paged_append(b, ctypes.byref(x), ctypes.byref(m), None, FAKE, WS, 1 << 30, None) == code
+    assert L.dartree_paged_attention(b, FAKE, ctypes.byref(m), None, 0.0, FAKE, None, WS, 1 << 30, None) == code
+    assert L.dartree_paged_weights(b, FAKE, FAKE, ctypes.byref(m), None, 0.0, 1.0, FAKE, WS, 1 << 30, None) == code
+    assert L.dartree_paged_evict(b, ctypes.byref(m), FAKE, 4, 0, 0, FAKE, 9, FAKE, FAKE, None, WS, 1 << 30,
+                                 None) == code
+    assert L.dartree_paged_commit(b, ctypes.byref(m), FAKE, FAKE, 4, FAKE, WS, 1 << 30, None) == code
+
+
+def test_append_arguments(dd):
+    L = dd.lib()
+    need = L.dartree_paged_workspace_bytes(ctypes.byref(_p(dd)))
+    assert need > 256
+
+    def call(p=None, x=None, m=None, tree=None, out=FAKE, ws=WS, n=None):
+        return L.dartree_paged_append(ctypes.byref(p or _p(dd)), ctypes.byref(x or _x(dd)), ctypes.byref(m or _m(dd)),
+                                      tree, out, ws, need if n is None else n, None)
+
+    for kw in (dict(q=None), dict(k=260), dict(v=264), dict(gq=258), dict(ldq=1020), dict(ldq=1016), dict(ldk=248),
+               dict(ldv=0), dict(theta=0.0), dict(theta=float("inf")), dict(eps=0.0), dict(eps=float("nan"))):
+        assert call(x=_x(dd, **kw)) == dd.EINVAL, kw
+    assert call(x=_x(dd, ldq=1032), out=FAKE) == dd.EINVAL     # in place needs packed queries
+    for kw in (dict(k=None), dict(v=264), dict(table=None), dict(n_ctx=None)):
+        assert call(m=_m(dd, **kw)) == dd.EINVAL, kw
+    assert call(p=_p(dd, n_pages=0)) == dd.EINVAL
+    assert call(p=_p(dd, max_pages=0)) == dd.EINVAL
+    assert call(p=_p(dd, T=5)) == dd.EINVAL                    # T = C * S without q_start
+    assert call(m=_m(dd, q_start=256), tree=_tree(dd)) == dd.EINVAL
+    assert call(tree=_tree(dd, pos=None)) == dd.EINVAL
+    assert call(tree=_tree(dd, n_nodes=None)) == dd.EINVAL
+    assert call(out=None) == dd.EINVAL
+    assert call(ws=None) == dd.EWORKSPACE
+    assert call(n=need - 1) == dd.EWORKSPACE
+    assert call(p=_p(dd, C=0, T=0)) == dd.OK
+
+
+def test_attention_and_weights_arguments(dd):
+    L = dd.lib()
+    need = L.dartree_paged_workspace_bytes(ctypes.byref(_p(dd)))
+
+    def att(p=None, q=FAKE, m=None, tree=None, scale=0.0, out=FAKE, lse=None, n=None):
+        return L.dartree_paged_attention(ctypes.byref(p or _p(dd)), q, ctypes.byref(m or _m(dd)), tree, scale, out, lse,
+                                         WS, need if n is None else n, None)
+
+    def wts(p=None, q=FAKE, lse=FAKE, m=None, tree=None, scale=0.0, decay=0.5, w=FAKE, n=None):
+        return L.dartree_paged_weights(ctypes.byref(p or _p(dd)), q, lse, ctypes.byref(m or _m(dd)), tree, scale, decay,
+                                       w, WS, need if n is None else n, None)
+
+    for f in (att, wts):
+        assert f(p=_p(dd, dtype=0)) == dd.EUNSUPPORTED         # bf16 only
+        assert f(q=ctypes.c_void_p(264)) == dd.EINVAL
+        assert f(q=None) == dd.EINVAL
+        assert f(scale=-1.0) == dd.EINVAL
+        assert f(scale=float("nan")) == dd.EINVAL
+        assert f(tree=_tree(dd, mask=None)) == dd.EINVAL
+        assert f(m=_m(dd, q_start=256), tree=_tree(dd)) == dd.EINVAL
+        assert f(p=_p(dd, T=7)) == dd.EINVAL
+        assert f(n=need - 1) == dd.EWORKSPACE
+        assert f(p=_p(dd, C=0, T=0)) == dd.OK
+    assert att(out=None) == dd.EINVAL
+    assert att(lse=ctypes.c_void_p(258)) == dd.EINVAL
+    assert att(p=_p(dd, T=0), m=_m(dd, q_start=256)) == dd.OK  # no new token
+    for d in (-0.1, 1.5, float("nan")):
+        assert wts(decay=d) == dd.EINVAL
+    assert wts(lse=None) == dd.EINVAL
+    assert wts(w=None) == dd.EINVAL
+
+
+def test_evict_and_commit_arguments(dd):
+    L = dd.lib()
+    need = L.dartree_paged_workspace_bytes(ctypes.byref(_p(dd)))
+
+    def ev(p=None, m=None, w=FAKE, budget=64, sink=4, recent=8, dst=FAKE, pages=1, keep=FAKE, n_out=FAKE, n=None):
+        return L.dartree_paged_evict(ctypes.byref(p or _p(dd)), ctypes.byref(m or _m(dd)), w, budget, sink, recent,
+                                     dst, pages, keep, n_out, None, WS, need if n is None else n, None)
+
+    for kw in (dict(budget=0), dict(budget=65), dict(sink=-1), dict(recent=-1), dict(sink=60, recent=5),
+               dict(sink=2 ** 31 - 1, recent=2 ** 31 - 1), dict(pages=0), dict(w=None), dict(dst=None),
+               dict(keep=None), dict(n_out=None), dict(m=_m(dd, k=None))):
+        assert ev(**kw) == dd.EINVAL, kw
+    assert ev(p=_p(dd, C=1 << 12, T=3 << 12, Hq=4096, Hkv=4096), budget=128, pages=2) == dd.EUNSUPPORTED
+    assert ev(n=need - 1) == dd.EWORKSPACE
+    assert ev(p=_p(dd, C=0, T=0)) == dd.OK
+
+    def cm(p=None, m=None, path=FAKE, acc=FAKE, Lp=16, n_out=FAKE, n=None):
+        return L.dartree_paged_commit(ctypes.byref(p or _p(dd)), ctypes.byref(m or _m(dd)), path, acc, Lp, n_out, WS,
+                                      need if n is None else n, None)
+
+    for kw in (dict(path=None), dict(acc=None), dict(Lp=0), dict(n_out=None), dict(m=_m(dd, table=None))):
+        assert cm(**kw) == dd.EINVAL, kw
+    assert cm(Lp=65) == dd.EUNSUPPORTED
+    assert cm(n=need - 1) == dd.EWORKSPACE
+    assert cm(p=_p(dd, C=0, T=0)) == dd.OK
+
+
+def test_kernel_families_are_named(dd):
+    names = [dd.lib().dartree_kernel_name(i).decode() for i in range(dd.num_kernel_ids())]
+    for n in ("append", "attn", "weights", "select", "move", "commit"):
+        assert f"paged_{n}_kernel" in names
