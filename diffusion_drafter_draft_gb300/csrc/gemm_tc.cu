@@ -298,6 +298,21 @@ bool make_tensor_map_bf16(CUtensorMap* map, const void* base, int rows, int cols
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_tensor_map_bf16_nd(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                             const uint64_t* stride_bytes, const uint32_t* box) {
+    auto fn = encode_fn();
+    if (!fn || rank < 2 || rank > 5) return false;
+    cuuint64_t d[5], st[4];
+    cuuint32_t b[5], es[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i], b[i] = box[i], es[i] = 1;
+        if (i + 1 < rank) st[i] = stride_bytes[i];
+    }
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cuuint32_t(rank), const_cast<void*>(base), d, st, b, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Operand tiles of the GEMM: box = 64 columns x box_rows rows, 128-byte swizzle.
 static bool make_map(CUtensorMap* map, const void* base, int rows, int cols, int box_rows) {
     return make_tensor_map_bf16(map, base, rows, cols, GT_BK, box_rows, 128);

@@ -148,6 +148,10 @@ struct ExpandArgs {
 // swizzle 0 (none), 32, 64 or 128 bytes. False when the driver refuses it.
 bool make_tensor_map_bf16(CUtensorMap* map, const void* base, int rows, int cols, int box_cols, int box_rows,
                           int swizzle_bytes);
+// TMA descriptor of a bf16 tensor of 2..5 dimensions (innermost first; stride_bytes[i]
+// belongs to dimension i + 1), 128-byte swizzle: box[0] = 64.
+bool make_tensor_map_bf16_nd(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
+                             const uint64_t* stride_bytes, const uint32_t* box);
 // out[m] = E[idx[m]] for m < M (rows of H bf16, H / 8 <= 768).
 int launch_gather_rows(const uint16_t* E, const int32_t* idx, int H, int M, uint16_t* out, cudaStream_t stream);
 

@@ -1,172 +1,580 @@
-// Attention of new tokens over the paged cache and the attention weight each cached row
-// receives: the plain kernels (CUDA cores, fp32).
+// Attention of new tokens over the paged key/value cache.
+//
+//   out_i = sum_j softmax_j(scale <q_i, k_j>) v_j,   lse_i = log sum_j exp(scale <q_i, k_j>)
+//
+// over the cached rows j < n_old and the new rows up to token i's own (or those a tree
+// mask marks). The query heads of a key/value head are stacked: a tile holds TT = 128 / grp
+// tokens, row (token, head) at token * grp + head, so that one TMA box brings it and a
+// tile's rows end at nearly the same key. One pass over 128-key blocks with the running
+// maximum and sum of the softmax.
+//
+// CTA = (chunk of a tile's key blocks, NT tiles, (request, key/value head)):
+//   warp 0      producer: a block's keys, then its values, page by page (TMA, 128-byte
+//               swizzle) through a ring of ST stages; a row past the request's last is
+//               fetched from beyond the pool, which TMA fills with zeros
+//   warp 1      issues S = Q K^T (both operands in shared memory) and O += P V (P in
+//               tensor memory over S's columns, V as an MN-major operand straight from
+//               its pages: nothing is transposed)
+//   warps 2..   softmax, one thread per row: the row's 128 scores in registers, P in bf16
+//               back to tensor memory; O is rescaled only when the maximum grows by more
+//               than 2^8
+// With NT = 2 the tensor cores work on one tile while the other tile's softmax runs.
+// Rows of a partly used page may hold anything: the last block's value rows past the end
+// are zeroed in shared memory (0 * NaN is NaN), its scores are masked.
+//
+// A second launch (several chunks only) merges the chunks' partial rows.
+// Every mbarrier wait is bounded; one that runs out records DARTREE_ETIMEOUT.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <math.h>
 
 #include "paged.cuh"
+#include "tc.cuh"
 
 namespace dartree {
 
-// Whether new token i of request c sees row j of it (j < n_keys).
-__device__ __forceinline__ bool paged_sees(const PagedArgs& a, const PagedRequest& r, int c, int i, int j) {
-    if (j < r.n_old) return true;
-    const int s = j - r.n_old;
-    return a.mask ? a.mask[(size_t(c) * a.S + i) * a.S + s] != 0 : s <= i;
+constexpr int PG_BM = 128;            // rows of a tile
+constexpr int PG_BN = 128;            // keys of a block
+constexpr float PG_RESCALE = 8.0f;    // log2 growth of the maximum that forces a rescale
+constexpr float LOG2E = 1.4426950408889634f;
+
+template <int D, int NT, int ST>
+struct PgSmem {
+    static constexpr int PANELS = D / 64;                       // 64 values of D per 128-byte row
+    static constexpr size_t PANEL = size_t(PG_BN) * 128;
+    static constexpr size_t TILE = PANELS * PANEL;              // a query tile, or a block's keys or values
+    static constexpr size_t RING_OFF = NT * TILE;
+    static constexpr size_t BAR_OFF = RING_OFF + ST * TILE;
+    // qfull, full[ST], empty[ST], sfull[NT], pfull[NT], ofull[NT]
+    static constexpr size_t SLOT_OFF = BAR_OFF + 8 * (1 + 2 * ST + 3 * NT);
+    static constexpr size_t TOTAL = SLOT_OFF + 16 + 1024;       // (+ alignment of the base to 1024)
+    static_assert(TOTAL <= 227 * 1024, "tiles and ring fit in shared memory");
+};
+
+struct PgPlan {
+    int tt, tiles, nt, nchunk, rows;  // tokens per tile, tiles, tiles per CTA, chunks, rows kept per partial tile
+    size_t part_o, part_ml, total;    // workspace (partials): offsets and bytes
+};
+
+struct PgArgs {
+    PagedArgs a;
+    int grp, tt, tiles, nchunk, rows;
+    float sl2;                        // scale * log2(e)
+    bf16_t* out;
+    float* lse;
+    float* part_o;
+    float2* part_ml;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// ----------------------------------------------------------------------------- attention
-//
-// One warp per (row of q, query head): 32 keys a step, one score per lane, the running
-// maximum and sum of the softmax across the warp; each lane holds D / 32 values of the
-// output.
-
-constexpr int PG_NT = 256;
-
-template <int D>
-__global__ void __launch_bounds__(PG_NT) paged_attn_kernel(PagedArgs a, const bf16_t* __restrict__ q, float scale,
-                                                           bf16_t* __restrict__ out, float* __restrict__ lse) {
-    __shared__ float sq[PG_NT / 32][D];
+template <int D, int NT, int ST>
+__global__ void __launch_bounds__(64 + 128 * NT, NT == 1 ? 2 : 1)
+    paged_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PgArgs x) {
+    using L = PgSmem<D, NT, ST>;
+    constexpr uint32_t OCOL = NT * PG_BN;                    // TMEM: S/P of tile t at 128 t, O at OCOL + D t
+    constexpr uint32_t TCOLS = NT == 2 ? 512 : 256;
+    const PagedArgs& a = x.a;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* qfull = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
+    uint64_t* full = qfull + 1;       // [ST] stage landed
+    uint64_t* empty = full + ST;      // [ST] the MMAs that read it are done
+    uint64_t* sfull = empty + ST;     // [NT] scores written (and every earlier MMA done)
+    uint64_t* pfull = sfull + NT;     // [NT] P written
+    uint64_t* ofull = pfull + NT;     // [NT] the last product with V done
+    uint32_t* slot = reinterpret_cast<uint32_t*>(smem + L::SLOT_OFF);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const size_t id = size_t(blockIdx.x) * (PG_NT / 32) + warp;  // (request, token, head)
-    if (id >= size_t(a.C) * a.S * a.Hq) return;
-    const int h = int(id % a.Hq), i = int(id / a.Hq % a.S), c = int(id / a.Hq / a.S);
+
+    if (threadIdx.x == 0) {
+        mbar_init(qfull, 1);
+        for (int s = 0; s < ST; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int t = 0; t < NT; ++t) {
+            mbar_init(&sfull[t], 1);
+            mbar_init(&pfull[t], 4);
+            mbar_init(&ofull[t], 1);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 1) tc::tmem_alloc(slot, TCOLS);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *slot;
+    griddep_launch_dependents();
+    griddep_wait();
+
+    // the last tiles (the most keys of a causal batch) first
+    const int ntile = (x.tiles + NT - 1) / NT;
+    const int chunk = int(blockIdx.x % x.nchunk);
+    const unsigned rest = blockIdx.x / x.nchunk;
+    const int heads = a.C * a.Hkv, cg = int(rest % heads), tp = ntile - 1 - int(rest / heads);
+    const int c = cg / a.Hkv, g = cg - c * a.Hkv;
     bool bad;
     const PagedRequest r = paged_request(a, c, bad);
-    if (bad && h == 0 && i == 0 && lane == 0) set_status(a.status, DARTREE_EINTERNAL);
-    if (i >= r.n_new) {
-        if (!a.q_start) {  // a slot without a node
-            const size_t row = size_t(c) * a.S + i;
-            for (int d = lane; d < D; d += 32) out[(row * a.Hq + h) * D + d] = bf16_t{0};
-            if (lse && lane == 0) lse[row * a.Hq + h] = -INFINITY;
-        }
-        return;
-    }
-    const size_t row = size_t(r.q0) + i;
-    const int g = h / (a.Hq / a.Hkv);
-    for (int d = lane; d < D; d += 32) sq[warp][d] = to_float(q[(row * a.Hq + h) * D + d]);
-    __syncwarp();
-    const bf16_t* kp = static_cast<const bf16_t*>(a.k);
-    const bf16_t* vp = static_cast<const bf16_t*>(a.v);
-    float m = -INFINITY, l = 0.f, acc[D / 32];
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
-    for (int j0 = 0; j0 < r.n_keys; j0 += 32) {
-        const int j = j0 + lane;
-        long long off = -1;
-        float s = -INFINITY;
-        if (j < r.n_keys && paged_sees(a, r, c, i, j)) {
-            const int pg = paged_page(a.table, a.max_pages, a.n_pages, c, j, a.log2_page);
-            if (pg < 0) {
+    if (bad && threadIdx.x == 0 && g == 0 && tp == 0) set_status(a.status, DARTREE_EINTERNAL);
+    const int t0 = tp * NT * x.tt;                                        // first token
+    const int live = min(max(r.n_new - t0, 0), NT * x.tt);                // tokens
+    const int nact = NT == 1 ? (live > 0) : (live + x.tt - 1) / x.tt;     // tiles with a token
+    const int end = a.mask ? r.n_keys : min(r.n_keys, r.n_old + t0 + live);
+    const int blocks = live > 0 ? (end + PG_BN - 1) / PG_BN : 0;
+    const int per = (blocks + x.nchunk - 1) / x.nchunk;
+    const int b0 = chunk * per, nblk = max(min(blocks, b0 + per) - b0, 0);
+
+    if (warp == 0) {
+        // ---------------------------------------------------------------- producer
+        if (nblk > 0) {
+            const int pr = min(a.page, PG_BN), sub = PG_BN / pr;          // rows and copies per panel of a block
+            if (lane == 0) {
+                mbar_arrive_expect_tx(qfull, uint32_t(nact * L::PANELS * x.tt * x.grp * 128));
+                for (int t = 0; t < nact; ++t)
+                    for (int p = 0; p < L::PANELS; ++p)
+                        tc::tma_load_3d(smem + t * L::TILE + p * L::PANEL, &tmQ, 64 * p, g * x.grp,
+                                        r.q0 + t0 + t * x.tt, qfull);
+            }
+            const int su = lane % sub, pn = lane / sub;                   // this lane's page and panel
+            const bool mine = sub <= 32 && pn < L::PANELS;
+            const int32_t* table = a.table + size_t(c) * a.max_pages;
+            auto page_of = [&](int b) -> int {                            // (n_pages: beyond the pool, zeros)
+                const int j = b * PG_BN + su * pr;
+                if (!mine || j >= r.n_keys) return a.n_pages;
+                const int p = table[j >> a.log2_page];
+                if (unsigned(p) < unsigned(a.n_pages)) return p;
                 set_status(a.status, DARTREE_EINTERNAL);
-            } else {
-                off = (long long)paged_offset(a, pg, g, j);
-                float x = 0.f;
-                for (int d = 0; d < D; ++d) x = fmaf(sq[warp][d], to_float(kp[off + d]), x);
-                s = x * scale;
+                return a.n_pages;
+            };
+            int pg = page_of(b0), issued = 0;
+            for (int i = 0; i < nblk; ++i) {
+                const int next = i + 1 < nblk ? page_of(b0 + i + 1) : 0;
+                bool ok = true;
+                for (int kv = 0; kv < 2 && ok; ++kv) {
+                    const int idx = 2 * i + kv, s = idx % ST;
+                    if (lane == 0 && idx >= ST)
+                        ok = mbar_wait_bounded(&empty[s], uint32_t((idx / ST) & 1) ^ 1u, a.status);
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_expect_tx(&full[s], uint32_t(L::TILE));
+                    __syncwarp();
+                    if (mine)
+                        tc::tma_load_4d(smem + L::RING_OFF + s * L::TILE + pn * L::PANEL + size_t(su) * pr * 128,
+                                        kv ? &tmV : &tmK, 64 * pn, ((b0 + i) * PG_BN + su * pr) & (a.page - 1), g, pg,
+                                        &full[s]);
+                    issued = idx + 1;
+                }
+                if (!ok) break;
+                pg = next;
+            }
+            // copies issued and not yet seen complete land before the CTA can exit
+            if (lane == 0) {
+                mbar_wait_bounded(qfull, 0, a.status);
+                for (int q = max(issued - ST, 0); q < issued; ++q)
+                    mbar_wait_bounded(&full[q % ST], uint32_t(q / ST) & 1u, a.status);
             }
         }
-        const float mx = fmaxf(m, warp_max(s));
-        if (mx == -INFINITY) continue;
-        const float f = expf(m - mx), p = expf(s - mx);
-        l = l * f + warp_sum(p);
-        m = mx;
-        const float pb = to_float(from_float<bf16_t>(p));
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- MMA issue
+        if (nblk > 0) {
+            constexpr uint32_t idS = tc::idesc_bf16_f32(PG_BM, PG_BN);
+            constexpr uint32_t idO = tc::idesc_bf16_f32(PG_BM, D) | tc::IDESC_B_MNMAJOR;
+            auto wait = [&](uint64_t* bar, int phase) -> bool {
+                bool ok = true;
+                if (lane == 0) ok = mbar_wait_bounded(bar, uint32_t(phase) & 1u, a.status);
+                return __shfl_sync(0xffffffffu, ok, 0);
+            };
+            auto scores = [&](int t, int idx) {
+                const uint32_t kb = smem_u32(smem + L::RING_OFF + (idx % ST) * L::TILE);
+                const uint32_t qb = smem_u32(smem + t * L::TILE);
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) acc[e] *= f;
-        for (int t = 0; t < 32; ++t) {
-            const float w = __shfl_sync(0xffffffffu, pb, t);
-            const long long o = __shfl_sync(0xffffffffu, off, t);
-            if (o < 0) continue;
+                for (int p = 0; p < L::PANELS; ++p) {
+                    const uint64_t da = tc::desc_sw128_kmajor(qb + uint32_t(p * L::PANEL));
+                    const uint64_t db = tc::desc_sw128_kmajor(kb + uint32_t(p * L::PANEL));
 #pragma unroll
-            for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(w, to_float(vp[o + lane + 32 * e]), acc[e]);
+                    for (int kk = 0; kk < 4; ++kk)
+                        tc::mma_bf16(tmem + uint32_t(t * PG_BN), da + 2u * kk, db + 2u * kk, idS, p > 0 || kk > 0);
+                }
+                tc::mma_commit(&sfull[t]);
+            };
+            bool ok = wait(qfull, 0) && wait(&full[0], 0);
+            if (ok && lane == 0) {
+                tc::fence_after_sync();
+                for (int t = 0; t < nact; ++t) scores(t, 0);
+                tc::mma_commit(&empty[0]);
+            }
+            for (int i = 0; i < nblk && ok; ++i) {
+                const int vi = 2 * i + 1, ki = 2 * i + 2;
+                const bool last = i + 1 == nblk;
+                for (int t = 0; t < nact && ok; ++t) {
+                    if (t == 0) {
+                        ok = wait(&full[vi % ST], vi / ST);
+                        const int have = r.n_keys - (b0 + i) * PG_BN;   // value rows of the block
+                        if (ok && have < PG_BN) {                       // zero the others (last block only)
+                            uint8_t* vb = smem + L::RING_OFF + (vi % ST) * L::TILE;
+                            for (int e = lane; e < (PG_BN - have) * 8; e += 32)
+#pragma unroll
+                                for (int p = 0; p < L::PANELS; ++p)
+                                    reinterpret_cast<uint4*>(vb + p * L::PANEL + size_t(have) * 128)[e] =
+                                        make_uint4(0, 0, 0, 0);
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                        }
+                        if (ok && !last) ok = wait(&full[ki % ST], ki / ST);
+                    }
+                    ok = ok && wait(&pfull[t], i);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        tc::fence_after_sync();
+                        const uint64_t db = tc::desc_sw128_mnmajor(
+                            smem_u32(smem + L::RING_OFF + (vi % ST) * L::TILE), uint32_t(L::PANEL));
+#pragma unroll
+                        for (int kk = 0; kk < PG_BN / 16; ++kk)
+                            tc::mma_bf16_ts(tmem + OCOL + uint32_t(t * D), tmem + uint32_t(t * PG_BN + 8 * kk),
+                                            db + 128u * kk, idO, i > 0 || kk > 0);
+                        if (t == nact - 1) tc::mma_commit(&empty[vi % ST]);
+                        if (!last) {
+                            scores(t, ki);
+                            if (t == nact - 1) tc::mma_commit(&empty[ki % ST]);
+                        } else {
+                            tc::mma_commit(&ofull[t]);
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+    } else {
+        // ---------------------------------------------------------------- softmax
+        const int t = (warp - 2) >> 2, quarter = warp & 3;
+        const int row = quarter * 32 + lane;                     // row of the tile (TMEM lane)
+        const int ti = row / x.grp, hg = row - ti * x.grp;
+        const int i_tok = t0 + t * x.tt + ti;                    // token of the request
+        const bool slot_ok = ti < x.tt && i_tok < a.S;
+        const bool real = slot_ok && i_tok < r.n_new;
+        const int limit = !real ? 0 : a.mask ? r.n_keys : min(r.n_keys, r.n_old + i_tok + 1);
+        const bool work = __any_sync(0xffffffffu, real);         // a warp without a token forms no weights
+        const uint32_t trow = tmem + (uint32_t(quarter * 32) << 16);
+        const uint32_t scol = trow + uint32_t(t * PG_BN), ocol = trow + OCOL + uint32_t(t * D);
+        float m = -INFINITY, l = 0.f;
+        bool ok = true;
+        if (t < nact) {
+            for (int i = 0; i < nblk; ++i) {
+                ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&sfull[t], uint32_t(i) & 1u, a.status));
+                if (ok && work) {
+                    tc::fence_after_sync();
+                    const int key0 = (b0 + i) * PG_BN;
+                    uint32_t s[4][32];
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) tc::tmem_ld32_async(scol + 32u * w, s[w]);
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) tc::tmem_wait_ld(s[w]);
+                    // hidden keys: the block's columns from `lim` on, and what the tree's mask hides
+                    const int lim = limit - key0;
+                    if (a.mask && key0 + PG_BN > r.n_old) {
+                        // the mask rows of this warp's tokens, 32 slots at a time: lane q reads slot
+                        // q of a token's word and the vote is the word
+                        const int tok0 = (quarter * 32) / x.grp, tok1 = (quarter * 32 + 31) / x.grp;
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            const int sl = key0 + 32 * w + lane - r.n_old;
+                            uint32_t bits = 0;
+                            for (int q = tok0; q <= tok1; ++q) {
+                                const int i_q = t0 + t * x.tt + q;
+                                bool v = sl < 0;
+                                if (sl >= 0 && sl < r.n_new && q < x.tt && i_q < r.n_new)
+                                    v = a.mask[(size_t(c) * a.S + i_q) * a.S + sl] != 0;
+                                const uint32_t word = __ballot_sync(0xffffffffu, v);
+                                if (q == ti) bits = word;
+                            }
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!((bits >> e) & 1u) || 32 * w + e >= lim) s[w][e] = 0xff800000u;
+                        }
+                    } else if (__any_sync(0xffffffffu, lim < PG_BN)) {
+#pragma unroll
+                        for (int w = 0; w < 4; ++w)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (32 * w + e >= lim) s[w][e] = 0xff800000u;  // -inf
+                    }
+                    float mx = -INFINITY;
+                    {
+                        float p[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+#pragma unroll
+                            for (int w = 0; w < 4; ++w) p[w] = fmaxf(p[w], __uint_as_float(s[w][e]));
+                        mx = fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3]));
+                    }
+                    mx *= x.sl2;                                 // (sl2 > 0: -inf stays)
+                    const bool grow = mx > m + PG_RESCALE || (m == -INFINITY && mx > -INFINITY);
+                    const bool resc = grow && m > -INFINITY;
+                    if (__any_sync(0xffffffffu, resc)) {         // O's products up to block i - 1 are done
+                        const float f = resc ? ex2(m - mx) : 1.0f;
+#pragma unroll 1
+                        for (int c0 = 0; c0 < D; c0 += 32) {
+                            uint32_t o[32];
+                            tc::tmem_ld32(ocol + uint32_t(c0), o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tc::tmem_st32(ocol + uint32_t(c0), o);
+                        }
+                        l *= f;
+                    }
+                    if (grow) m = mx;
+                    const float ms = m > -INFINITY ? m : 0.f;    // (a row that has seen nothing: 2^-inf = 0)
+                    float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const float p0 = ex2(fmaf(__uint_as_float(s[w][e]), x.sl2, -ms));
+                            const float p1 = ex2(fmaf(__uint_as_float(s[w][e + 1]), x.sl2, -ms));
+                            ls[(e >> 1) & 3] += p0 + p1;
+                            pk[e / 2] = pack2(p0, p1);
+                        }
+                        tc::tmem_st16_async(scol + 16u * w, pk);
+                    }
+                    l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                    tc::tmem_wait_st();
+                    tc::fence_before_sync();
+                }
+                __syncwarp();
+                if (lane == 0 && ok) mbar_arrive(&pfull[t]);
+            }
+            if (nblk > 0) {
+                ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&ofull[t], 0, a.status));
+                if (ok) tc::fence_after_sync();
+            }
+        }
+        const bool has = ok && t < nact && nblk > 0 && real && l > 0.f;
+        const bool load = ok && t < nact && nblk > 0 && work;    // (TMEM loads are warp-wide)
+        const size_t orow = (size_t(r.q0) + i_tok) * a.Hq + size_t(g) * x.grp + hg;
+        if (x.nchunk == 1) {
+            // tree slots without a node get zeros; rows of ragged batches only their own tokens
+            const bool write = real || (slot_ok && !a.q_start);
+            const float inv = has ? 1.0f / l : 0.f;
+            uint4* dst = reinterpret_cast<uint4*>(x.out + orow * D);
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 32) {
+                uint32_t o[32];
+                __syncwarp();
+                if (load) tc::tmem_ld32(ocol + uint32_t(c0), o);
+                if (write)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t pk[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            pk[e] = has ? pack2(__uint_as_float(o[8 * q + 2 * e]) * inv,
+                                                __uint_as_float(o[8 * q + 2 * e + 1]) * inv)
+                                        : 0u;
+                        dst[c0 / 8 + q] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    }
+            }
+            if (x.lse && write) x.lse[orow] = has ? (m + log2f(l)) * 0.6931471805599453f : real ? -INFINITY : 0.f;
+        } else if (slot_ok) {
+            const size_t pr = ((size_t(cg) * x.tiles + tp * NT + t) * x.nchunk + chunk) * x.rows + row;
+            if (real) x.part_ml[pr] = has ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
+        }
+        if (x.nchunk > 1 && load) {
+            const size_t pr = ((size_t(cg) * x.tiles + tp * NT + t) * x.nchunk + chunk) * x.rows + row;
+            float4* dst = reinterpret_cast<float4*>(x.part_o + pr * D);
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 32) {
+                uint32_t o[32];
+                __syncwarp();
+                tc::tmem_ld32(ocol + uint32_t(c0), o);
+                if (has)
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        dst[c0 / 4 + q] =
+                            make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]),
+                                        __uint_as_float(o[4 * q + 2]), __uint_as_float(o[4 * q + 3]));
+            }
         }
     }
-    const float inv = l > 0.f ? 1.0f / l : 0.f;
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) out[(row * a.Hq + h) * D + lane + 32 * e] = from_float<bf16_t>(acc[e] * inv);
-    if (lse && lane == 0) lse[row * a.Hq + h] = l > 0.f ? m + logf(l) : -INFINITY;
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 1) tc::tmem_dealloc(tmem, TCOLS);
 }
 
-size_t paged_attention_part_bytes(const PagedArgs&) { return 0; }
-
-int launch_paged_attention(const PagedArgs& a, const void* q, float scale, void* out, float* lse, void*,
-                           cudaStream_t stream) {
-    const size_t warps = size_t(a.C) * a.S * a.Hq;
-    const unsigned grid = unsigned((warps + PG_NT / 32 - 1) / (PG_NT / 32));
-    KTimer kt_(KID_PAGED_ATTN, stream);
-    if (a.D == 64)
-        paged_attn_kernel<64><<<grid, PG_NT, 0, stream>>>(a, static_cast<const bf16_t*>(q), scale,
-                                                          static_cast<bf16_t*>(out), lse);
-    else
-        paged_attn_kernel<128><<<grid, PG_NT, 0, stream>>>(a, static_cast<const bf16_t*>(q), scale,
-                                                           static_cast<bf16_t*>(out), lse);
-    return cudaGetLastError() == cudaSuccess ? DARTREE_OK : DARTREE_ECUDA;
-}
-
-// ----------------------------------------------------------------------------- weights
+// ----------------------------------------------------------------------------- combine
 //
-// One thread per cached row of a (request, key/value head): the key in registers, the
-// query rows of the group one after the other in shared memory.
-
-constexpr int PW_NT = 128;
+// One warp per (request, token, query head): the chunks' (max, sum) pairs by the lanes in
+// parallel, then their rows of O eight at a time.
 
 template <int D>
-__global__ void __launch_bounds__(PW_NT) paged_weights_kernel(PagedArgs a, const bf16_t* __restrict__ q,
-                                                              const float* __restrict__ lse, float scale, float decay,
-                                                              float* __restrict__ weights, int blocks) {
-    __shared__ float sq[D];
-    const int cg = int(blockIdx.x / blocks), c = cg / a.Hkv, g = cg - c * a.Hkv;
-    const int j = int(blockIdx.x % blocks) * PW_NT + threadIdx.x;
-    bool bad;
-    const PagedRequest r = paged_request(a, c, bad);
-    if (bad && threadIdx.x == 0) set_status(a.status, DARTREE_EINTERNAL);
-    const bool real = j < r.n_keys;
-    float key[D];
-    bool held = false;
-    if (real) {
-        const int pg = paged_page(a.table, a.max_pages, a.n_pages, c, j, a.log2_page);
-        if (pg < 0) {
-            set_status(a.status, DARTREE_EINTERNAL);
-        } else {
-            held = true;
-            const bf16_t* kp = static_cast<const bf16_t*>(a.k) + paged_offset(a, pg, g, j);
-#pragma unroll
-            for (int d = 0; d < D; ++d) key[d] = to_float(kp[d]);
+__global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constant__ PgArgs x) {
+    constexpr int V = D / 32;
+    const PagedArgs& a = x.a;
+    const int lane = threadIdx.x & 31;
+    const size_t id = size_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    griddep_launch_dependents();
+    griddep_wait();
+    if (id >= size_t(a.C) * a.S * a.Hq) return;
+    const int h = int(id % a.Hq), i = int(id / a.Hq % a.S), c = int(id / a.Hq / a.S);
+    const PagedRequest r = paged_request(a, c);
+    const bool real = i < r.n_new;
+    if (!real && a.q_start) return;
+    const size_t orow = (size_t(r.q0) + i) * a.Hq + h;
+    const int g = h / x.grp, tile = i / x.tt, row = (i - tile * x.tt) * x.grp + (h - g * x.grp);
+    const size_t p0 = ((size_t(c) * a.Hkv + g) * x.tiles + tile) * x.nchunk * size_t(x.rows) + row;
+    float mx = -INFINITY;
+    if (real)
+        for (int k = lane; k < x.nchunk; k += 32) {
+            const float2 ml = x.part_ml[p0 + size_t(k) * x.rows];
+            if (ml.y > 0.f) mx = fmaxf(mx, ml.x);
         }
-    }
-    const int grp = a.Hq / a.Hkv;
-    float sum = 0.f;
-    for (int i = 0; i < r.n_new; ++i)
-        for (int hg = 0; hg < grp; ++hg) {
-            const size_t row = (size_t(r.q0) + i) * a.Hq + g * grp + hg;
-            __syncthreads();
-            for (int d = threadIdx.x; d < D; d += PW_NT) sq[d] = to_float(q[row * D + d]);
-            __syncthreads();
-            if (!held || !paged_sees(a, r, c, i, j)) continue;
-            float x = 0.f;
+    mx = warp_max(mx);
+    float acc[V], sum = 0.f;
 #pragma unroll
-            for (int d = 0; d < D; ++d) x = fmaf(sq[d], key[d], x);
-            const float l = lse[row];
-            if (l > -INFINITY) sum += expf(x * scale - l);
+    for (int e = 0; e < V; ++e) acc[e] = 0.f;
+    if (mx > -INFINITY)
+        for (int k0 = 0; k0 < x.nchunk; k0 += 32) {
+            float f = 0.f;  // lane t: chunk k0 + t's factor 2^(m - mx)
+            if (k0 + lane < x.nchunk) {
+                const float2 ml = x.part_ml[p0 + size_t(k0 + lane) * x.rows];
+                if (ml.y > 0.f) {
+                    f = ex2(ml.x - mx);
+                    sum += f * ml.y;
+                }
+            }
+            const int nk = min(32, x.nchunk - k0);
+            for (int u0 = 0; u0 < nk; u0 += 8) {
+                float o[8][V];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const float fu = __shfl_sync(0xffffffffu, f, (u0 + u) & 31);
+                    const float* src = x.part_o + (p0 + size_t(k0 + u0 + u) * x.rows) * D + lane * V;
+#pragma unroll
+                    for (int e = 0; e < V; ++e) o[u][e] = 0.f;
+                    if (u0 + u < nk && fu > 0.f) {
+                        if (V == 4) {
+                            const float4 y = *reinterpret_cast<const float4*>(src);
+                            o[u][0] = y.x, o[u][1] = y.y, o[u][V - 2] = y.z, o[u][V - 1] = y.w;
+                        } else {
+                            const float2 y = *reinterpret_cast<const float2*>(src);
+                            o[u][0] = y.x, o[u][1] = y.y;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const float fu = __shfl_sync(0xffffffffu, f, (u0 + u) & 31);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) acc[e] = fmaf(fu, o[u][e], acc[e]);
+                }
+            }
         }
-    if (real) {
-        float* w = weights + size_t(cg) * (size_t(a.max_pages) << a.log2_page) + j;
-        *w = j < r.n_old ? fmaf(decay, *w, sum) : sum;
-    }
+    sum = warp_sum(sum);
+    const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(x.out + orow * D) + lane * (V / 2);
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) dst[e] = pack2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    if (x.lse && lane == 0)
+        x.lse[orow] = sum > 0.f ? (mx + log2f(sum)) * 0.6931471805599453f : real ? -INFINITY : 0.f;
 }
 
-int launch_paged_weights(const PagedArgs& a, const void* q, const float* lse, float scale, float decay,
-                         float* weights, cudaStream_t stream) {
-    const int blocks = ((a.max_pages << a.log2_page) + PW_NT - 1) / PW_NT;
-    const unsigned grid = unsigned(a.C) * a.Hkv * blocks;
-    KTimer kt_(KID_PAGED_WEIGHTS, stream);
+// ----------------------------------------------------------------------------- host
+
+static PgPlan paged_plan(const PagedArgs& a) {
+    PgPlan p{};
+    const int grp = a.Hq / a.Hkv;
+    p.tt = PG_BM / grp;
+    p.tiles = (a.S + p.tt - 1) / p.tt;
+    p.nt = p.tiles > 1 ? 2 : 1;
+    const int64_t base = int64_t(a.C) * a.Hkv * ((p.tiles + p.nt - 1) / p.nt);
+    const int64_t slots = int64_t(num_sms()) * (p.nt == 1 ? 2 : 1);
+    const int64_t blocks = (((int64_t(a.max_pages) << a.log2_page)) + PG_BN - 1) / PG_BN;
+    // as many chunks of a tile's key blocks as one wave of CTAs holds
+    int64_t n = base > 0 ? slots / base : 1;
+    if (n > blocks) n = blocks;
+    p.nchunk = n < 1 ? 1 : int(n);
+    p.rows = p.tiles > 1 ? PG_BM : a.S * grp;
+    if (p.nchunk > 1) {
+        auto up = [](size_t b) { return (b + 255) / 256 * 256; };
+        const size_t rows = size_t(a.C) * a.Hkv * p.tiles * p.nchunk * p.rows;
+        p.part_ml = up(rows * a.D * 4);
+        p.total = p.part_ml + up(rows * 8);
+    }
+    return p;
+}
+
+size_t paged_attention_part_bytes(const PagedArgs& a) { return a.dtype == DARTREE_BF16 ? paged_plan(a).total : 0; }
+
+// Tensor maps of a call: queries [T, Hq, D] in boxes of (tt tokens, grp heads, 64), pages
+// [n_pages, Hkv, page, D] in boxes of (1, 1, at most 128 rows, 64).
+static bool make_page_map(CUtensorMap* m, const PagedArgs& a, const void* pool) {
+    const uint64_t d[4] = {uint64_t(a.D), uint64_t(a.page), uint64_t(a.Hkv), uint64_t(a.n_pages)};
+    const uint64_t st[3] = {uint64_t(a.D) * 2, uint64_t(a.page) * a.D * 2, uint64_t(a.Hkv) * a.page * a.D * 2};
+    const uint32_t box[4] = {64, uint32_t(a.page < PG_BN ? a.page : PG_BN), 1, 1};
+    return make_tensor_map_bf16_nd(m, pool, 4, d, st, box);
+}
+static bool make_query_map(CUtensorMap* m, const PagedArgs& a, const void* q, int tt) {
+    const uint64_t d[3] = {uint64_t(a.D), uint64_t(a.Hq), uint64_t(a.T)};
+    const uint64_t st[2] = {uint64_t(a.D) * 2, uint64_t(a.Hq) * a.D * 2};
+    const uint32_t box[3] = {64, uint32_t(a.Hq / a.Hkv), uint32_t(tt)};
+    return make_tensor_map_bf16_nd(m, q, 3, d, st, box);
+}
+
+template <int D, int NT, int ST>
+static int launch_attn_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PgArgs& x,
+                         cudaStream_t stream) {
+    auto kern = paged_attn_kernel<D, NT, ST>;
+    const size_t smem = PgSmem<D, NT, ST>::TOTAL;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess)
+        return DARTREE_ECUDA;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned(x.nchunk) * unsigned(x.a.C) * x.a.Hkv * ((x.tiles + NT - 1) / NT));
+    cfg.blockDim = dim3(64 + 128 * NT);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1] = {pdl_attribute()};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    KTimer kt_(KID_PAGED_ATTN, stream);
+    return cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, x) == cudaSuccess ? DARTREE_OK : DARTREE_ECUDA;
+}
+
+int launch_paged_attention(const PagedArgs& a, const void* q, float scale, void* out, float* lse, void* part,
+                           cudaStream_t stream) {
+    const PgPlan p = paged_plan(a);
+    CUtensorMap tq, tk, tv;
+    if (!make_query_map(&tq, a, q, p.tt) || !make_page_map(&tk, a, a.k) || !make_page_map(&tv, a, a.v))
+        return DARTREE_ECUDA;
+    uint8_t* w = static_cast<uint8_t*>(part);
+    PgArgs x{a, a.Hq / a.Hkv, p.tt, p.tiles, p.nchunk, p.rows, scale * LOG2E, static_cast<bf16_t*>(out), lse,
+             reinterpret_cast<float*>(w), reinterpret_cast<float2*>(w + p.part_ml)};
+    int e;
     if (a.D == 64)
-        paged_weights_kernel<64><<<grid, PW_NT, 0, stream>>>(a, static_cast<const bf16_t*>(q), lse, scale, decay,
-                                                             weights, blocks);
+        e = p.nt == 2 ? launch_attn_t<64, 2, 8>(tq, tk, tv, x, stream) : launch_attn_t<64, 1, 4>(tq, tk, tv, x, stream);
     else
-        paged_weights_kernel<128><<<grid, PW_NT, 0, stream>>>(a, static_cast<const bf16_t*>(q), lse, scale, decay,
-                                                              weights, blocks);
-    return cudaGetLastError() == cudaSuccess ? DARTREE_OK : DARTREE_ECUDA;
+        e = p.nt == 2 ? launch_attn_t<128, 2, 5>(tq, tk, tv, x, stream)
+                      : launch_attn_t<128, 1, 2>(tq, tk, tv, x, stream);
+    if (e != DARTREE_OK || p.nchunk == 1) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned((size_t(a.C) * a.S * a.Hq + 7) / 8));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1] = {pdl_attribute()};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    KTimer kt_(KID_PAGED_COMBINE, stream);
+    const cudaError_t ce = a.D == 64 ? cudaLaunchKernelEx(&cfg, paged_combine_kernel<64>, x)
+                                     : cudaLaunchKernelEx(&cfg, paged_combine_kernel<128>, x);
+    return ce == cudaSuccess ? DARTREE_OK : DARTREE_ECUDA;
 }
 
 }  // namespace dartree

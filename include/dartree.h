@@ -300,7 +300,7 @@ DARTREE_API int dartree_tree_attention(const dartree_attn_params* p, const void*
  *                 [q_start[0], q_start[C]) are neither read nor written
  *   tree          (q_start NULL only) the new tokens are the S slots of a verification
  *                 tree; slots from tree->n_nodes[c] on are not stored, and their output
- *                 rows are zero
+ *                 rows (lse too) are zero
  * A new token sees all n_ctx cached rows and, of the new ones, those up to its own
  * (causal), or the slots tree->mask [C, S, S] marks.
  * Checked on the device, with DARTREE_EINTERNAL in the status word of ws: lengths below
@@ -367,7 +367,7 @@ DARTREE_API int dartree_paged_append(const dartree_paged_params* p, const dartre
  *   out   [T, Hq, D]; a token that sees no row (a tree slot with an empty mask row and
  *         no context) gives zeros
  *   lse   [T, Hq] float, natural logarithm of the sum of exponentials of a row's scaled
- *         scores (-inf for a row that sees nothing), or NULL
+ *         scores (-inf for a token that sees nothing), or NULL
  * bf16 only (DARTREE_EUNSUPPORTED otherwise). Scores and sums in fp32; probabilities
  * are rounded to bf16 for the product with the values. Page rows behind a request's
  * last one (n_ctx + its new tokens) may hold anything, infinities and NaN included; the

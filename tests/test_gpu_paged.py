@@ -180,7 +180,7 @@ def test_attention_matches_oracle(dd, i):
     if x.tree is not None:
         for c in range(x.C):
             dead = slice(x.first[c] + x.new[c], x.first[c] + x.S)
-            assert (out[dead] == 0).all() and (lse[dead] == -math.inf).all()
+            assert (out[dead] == 0).all() and (lse[dead] == 0).all()
 
 
 def test_attention_of_a_full_batch(dd):
