@@ -266,6 +266,10 @@ struct PagedArgs {
     const int32_t* n_nodes;
     int* status;
 };
+// Tensor maps of a call: queries [T, Hq, D] in boxes of (tt tokens, grp heads, 64), pages
+// [n_pages, Hkv, page, D] in boxes of (1, 1, at most 128 rows, 64).
+bool make_query_map(CUtensorMap* m, const PagedArgs& a, const void* q, int tt);
+bool make_page_map(CUtensorMap* m, const PagedArgs& a, const void* pool);
 int launch_paged_append(const PagedArgs& a, const void* q, const void* k, const void* v, int64_t ldq, int64_t ldk,
                         int64_t ldv, const void* gq, const void* gk, const int32_t* pos_base, float eps, double theta,
                         void* q_out, cudaStream_t stream);

@@ -514,16 +514,14 @@ static PgPlan paged_plan(const PagedArgs& a) {
 
 size_t paged_attention_part_bytes(const PagedArgs& a) { return a.dtype == DARTREE_BF16 ? paged_plan(a).total : 0; }
 
-// Tensor maps of a call: queries [T, Hq, D] in boxes of (tt tokens, grp heads, 64), pages
-// [n_pages, Hkv, page, D] in boxes of (1, 1, at most 128 rows, 64).
-static bool make_page_map(CUtensorMap* m, const PagedArgs& a, const void* pool) {
+bool make_page_map(CUtensorMap* m, const PagedArgs& a, const void* pool) {
     const uint64_t d[4] = {uint64_t(a.D), uint64_t(a.page), uint64_t(a.Hkv), uint64_t(a.n_pages)};
     const uint64_t st[3] = {uint64_t(a.D) * 2, uint64_t(a.page) * a.D * 2, uint64_t(a.Hkv) * a.page * a.D * 2};
     const uint32_t box[4] = {64, uint32_t(a.page < PG_BN ? a.page : PG_BN), 1, 1};
     return make_tensor_map_bf16_nd(m, pool, 4, d, st, box);
 }
-static bool make_query_map(CUtensorMap* m, const PagedArgs& a, const void* q, int tt) {
-    const uint64_t d[3] = {uint64_t(a.D), uint64_t(a.Hq), uint64_t(a.T)};
+bool make_query_map(CUtensorMap* m, const PagedArgs& a, const void* q, int tt) {
+    const uint64_t d[3] = {uint64_t(a.D), uint64_t(a.Hq), uint64_t(a.T > 0 ? a.T : 1)};
     const uint64_t st[2] = {uint64_t(a.D) * 2, uint64_t(a.Hq) * a.D * 2};
     const uint32_t box[3] = {64, uint32_t(a.Hq / a.Hkv), uint32_t(tt)};
     return make_tensor_map_bf16_nd(m, q, 3, d, st, box);

@@ -1,82 +1,319 @@
-// Attention weight each cached row of the paged cache receives (eviction's input).
+// Attention weight each cached row of the paged cache receives (eviction's input):
+//
+//   w_j <- decay * w_j + sum over the new tokens i that see j, and the query heads of the
+//          key/value head, of exp(scale <q_i, k_j> - lse_i)
+//
+// The scores are formed transposed, S^T = K Q^T: a block's 128 keys are the tile's rows
+// (tensor-memory lanes) and the queries its columns, so each thread owns a key and adds up
+// a row of its own: no reduction across threads, no atomics, a fixed order of addition.
+//
+// CTA = (chunk of key blocks, (request, key/value head)), over all query tiles of TT
+// tokens x grp heads (columns token * grp + head):
+//   warp 0      producer: key blocks and query tiles by TMA through two rings (a single
+//               query tile is fetched once)
+//   warp 1      issues S^T into one of two tensor-memory buffers
+//   warps 2..9  two groups of 128 threads, one per buffer: while one adds up a tile the
+//               other's is formed; the groups' sums of a block meet in shared memory
+// Single tokens are bound by reading the keys once; long chunks by the exponentials
+// (one per score) beside one matrix product.
+// Every mbarrier wait is bounded; one that runs out records DARTREE_ETIMEOUT.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <math.h>
 
 #include "paged.cuh"
+#include "tc.cuh"
 
 namespace dartree {
 
-// Whether new token i of request c sees row j of it (j < n_keys).
-__device__ __forceinline__ bool paged_sees(const PagedArgs& a, const PagedRequest& r, int c, int i, int j) {
-    if (j < r.n_old) return true;
-    const int s = j - r.n_old;
-    return a.mask ? a.mask[(size_t(c) * a.S + i) * a.S + s] != 0 : s <= i;
-}
-
-// ----------------------------------------------------------------------------- weights
-//
-// One thread per cached row of a (request, key/value head): the key in registers, the
-// query rows of the group one after the other in shared memory.
-
-constexpr int PW_NT = 128;
+constexpr int PW_BM = 128;   // keys of a block
+constexpr int PW_NT = 320;   // producer, MMA, two groups of four warps
+constexpr int PW_KS = 3;     // stages of the key ring
+constexpr int PW_QS = 3;     // stages of the query ring
 
 template <int D>
-__global__ void __launch_bounds__(PW_NT) paged_weights_kernel(PagedArgs a, const bf16_t* __restrict__ q,
-                                                              const float* __restrict__ lse, float scale, float decay,
-                                                              float* __restrict__ weights, int blocks) {
-    __shared__ float sq[D];
-    const int cg = int(blockIdx.x / blocks), c = cg / a.Hkv, g = cg - c * a.Hkv;
-    const int j = int(blockIdx.x % blocks) * PW_NT + threadIdx.x;
+struct PwSmem {
+    static constexpr int PANELS = D / 64;
+    static constexpr size_t PANEL = size_t(PW_BM) * 128;
+    static constexpr size_t TILE = PANELS * PANEL;
+    static constexpr size_t Q_OFF = PW_KS * TILE;
+    static constexpr size_t LSE_OFF = Q_OFF + PW_QS * TILE;             // float [2 groups][128]
+    static constexpr size_t SUM_OFF = LSE_OFF + 2 * 128 * 4;            // float [2 blocks][128]
+    static constexpr size_t BAR_OFF = SUM_OFF + 2 * 128 * 4;
+    // kfull, kempty [KS], qfull, qempty [QS], sfull, sfree [2]
+    static constexpr size_t SLOT_OFF = BAR_OFF + 8 * (2 * PW_KS + 2 * PW_QS + 4);
+    static constexpr size_t TOTAL = SLOT_OFF + 16 + 1024;
+    static_assert(TOTAL <= 227 * 1024, "rings fit in shared memory");
+};
+
+struct PwArgs {
+    PagedArgs a;
+    int grp, tt, tiles, nchunk;
+    float sl2, decay;
+    const float* lse;
+    float* weights;
+};
+
+template <int D>
+__global__ void __launch_bounds__(PW_NT, 1)
+    paged_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                         const __grid_constant__ PwArgs x) {
+    using L = PwSmem<D>;
+    const PagedArgs& a = x.a;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
+    uint64_t* kempty = kfull + PW_KS;
+    uint64_t* qfull = kempty + PW_KS;
+    uint64_t* qempty = qfull + PW_QS;
+    uint64_t* sfull = qempty + PW_QS;   // [2] scores written, by buffer
+    uint64_t* sfree = sfull + 2;        // [2] scores read
+    uint32_t* slot = reinterpret_cast<uint32_t*>(smem + L::SLOT_OFF);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < PW_KS; ++s) {
+            mbar_init(&kfull[s], 1);
+            mbar_init(&kempty[s], 1);
+        }
+        for (int s = 0; s < PW_QS; ++s) {
+            mbar_init(&qfull[s], 1);
+            mbar_init(&qempty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&sfull[s], 1);
+            mbar_init(&sfree[s], 4);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 1) tc::tmem_alloc(slot, 256);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *slot;
+    griddep_launch_dependents();
+    griddep_wait();
+
+    const int chunk = int(blockIdx.x % x.nchunk), cg = int(blockIdx.x / x.nchunk);
+    const int c = cg / a.Hkv, g = cg - c * a.Hkv;
     bool bad;
     const PagedRequest r = paged_request(a, c, bad);
-    if (bad && threadIdx.x == 0) set_status(a.status, DARTREE_EINTERNAL);
-    const bool real = j < r.n_keys;
-    float key[D];
-    bool held = false;
-    if (real) {
-        const int pg = paged_page(a.table, a.max_pages, a.n_pages, c, j, a.log2_page);
-        if (pg < 0) {
-            set_status(a.status, DARTREE_EINTERNAL);
-        } else {
-            held = true;
-            const bf16_t* kp = static_cast<const bf16_t*>(a.k) + paged_offset(a, pg, g, j);
+    if (bad && threadIdx.x == 0 && g == 0) set_status(a.status, DARTREE_EINTERNAL);
+    const int blocks = (r.n_keys + PW_BM - 1) / PW_BM;
+    const int per = (blocks + x.nchunk - 1) / x.nchunk;
+    const int b0 = chunk * per, b1 = min(blocks, b0 + per);
+    const int ntile = (r.n_new + x.tt - 1) / x.tt;
+    const bool once = x.tiles == 1;                       // one query tile: it stays in stage 0
+    // the first tile that sees a row of block b
+    auto first_tile = [&](int b) -> int { return a.mask ? 0 : max(0, (b * PW_BM - r.n_old) / x.tt); };
+
+    if (warp == 0) {
+        // ---------------------------------------------------------------- producer
+        if (b0 < b1 && ntile > 0) {
+            const int pr = min(a.page, PW_BM), sub = PW_BM / pr;
+            const int su = lane % sub, pn = lane / sub;
+            const bool mine = pn < L::PANELS;
+            const int32_t* table = a.table + size_t(c) * a.max_pages;
+            auto page_of = [&](int b) -> int {            // (n_pages: beyond the pool, zeros)
+                const int j = b * PW_BM + su * pr;
+                if (!mine || j >= r.n_keys) return a.n_pages;
+                const int p = table[j >> a.log2_page];
+                if (unsigned(p) < unsigned(a.n_pages)) return p;
+                set_status(a.status, DARTREE_EINTERNAL);
+                return a.n_pages;
+            };
+            const uint32_t qbytes = uint32_t(L::PANELS * x.tt * x.grp * 128);
+            int pg = page_of(b0), nk = 0, nq = 0;
+            bool ok = true;
+            for (int b = b0; b < b1 && ok; ++b) {
+                const int next = b + 1 < b1 ? page_of(b + 1) : 0;
+                if (lane == 0 && nk >= PW_KS)
+                    ok = mbar_wait_bounded(&kempty[nk % PW_KS], uint32_t((nk / PW_KS) & 1) ^ 1u, a.status);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
+                const int ks = nk % PW_KS;
+                if (lane == 0) mbar_arrive_expect_tx(&kfull[ks], uint32_t(L::TILE));
+                __syncwarp();
+                if (mine)
+                    tc::tma_load_4d(smem + ks * L::TILE + pn * L::PANEL + size_t(su) * pr * 128, &tmK, 64 * pn,
+                                    (b * PW_BM + su * pr) & (a.page - 1), g, pg, &kfull[ks]);
+                ++nk;
+                if (lane == 0 && !(once && nq > 0))
+                    for (int t = first_tile(b); t < ntile && ok; ++t) {
+                        const int qs = nq % PW_QS;
+                        if (nq >= PW_QS)
+                            ok = mbar_wait_bounded(&qempty[qs], uint32_t((nq / PW_QS) & 1) ^ 1u, a.status);
+                        if (!ok) break;
+                        mbar_arrive_expect_tx(&qfull[qs], qbytes);
+                        for (int p = 0; p < L::PANELS; ++p)
+                            tc::tma_load_3d(smem + L::Q_OFF + qs * L::TILE + p * L::PANEL, &tmQ, 64 * p, g * x.grp,
+                                            r.q0 + t * x.tt, &qfull[qs]);
+                        ++nq;
+                    }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                pg = next;
+            }
+            // copies issued and not yet seen complete land before the CTA can exit
+            if (lane == 0) {
+                for (int q = max(nk - PW_KS, 0); q < nk; ++q)
+                    mbar_wait_bounded(&kfull[q % PW_KS], uint32_t(q / PW_KS) & 1u, a.status);
+                for (int q = max(nq - PW_QS, 0); q < nq; ++q)
+                    mbar_wait_bounded(&qfull[q % PW_QS], uint32_t(q / PW_QS) & 1u, a.status);
+            }
+        }
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- MMA issue
+        if (lane == 0 && ntile > 0) {
+            const uint32_t id = tc::idesc_bf16_f32(PW_BM, (x.tt * x.grp + 15) / 16 * 16);
+            int nk = 0, nq = 0, n = 0;
+            bool ok = true;
+            for (int b = b0; b < b1 && ok; ++b, ++nk) {
+                const int ks = nk % PW_KS;
+                ok = mbar_wait_bounded(&kfull[ks], uint32_t(nk / PW_KS) & 1u, a.status);
+                for (int t = first_tile(b); t < ntile && ok; ++t, ++n) {
+                    const int qs = once ? 0 : nq % PW_QS;
+                    ok = mbar_wait_bounded(&qfull[qs], once ? 0u : uint32_t(nq / PW_QS) & 1u, a.status);
+                    if (ok && n >= 2) ok = mbar_wait_bounded(&sfree[n & 1], uint32_t((n >> 1) - 1) & 1u, a.status);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    const uint32_t ka = smem_u32(smem + ks * L::TILE), qb = smem_u32(smem + L::Q_OFF + qs * L::TILE);
 #pragma unroll
-            for (int d = 0; d < D; ++d) key[d] = to_float(kp[d]);
+                    for (int p = 0; p < L::PANELS; ++p) {
+                        const uint64_t da = tc::desc_sw128_kmajor(ka + uint32_t(p * L::PANEL));
+                        const uint64_t db = tc::desc_sw128_kmajor(qb + uint32_t(p * L::PANEL));
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            tc::mma_bf16(tmem + uint32_t((n & 1) * 128), da + 2u * kk, db + 2u * kk, id,
+                                         p > 0 || kk > 0);
+                    }
+                    tc::mma_commit(&sfull[n & 1]);
+                    if (!once) {
+                        tc::mma_commit(&qempty[qs]);
+                        ++nq;
+                    }
+                    if (t + 1 == ntile) tc::mma_commit(&kempty[ks]);
+                }
+            }
+        }
+    } else {
+        // ---------------------------------------------------------------- sums
+        const int group = (warp - 2) >> 2, quarter = warp & 3;
+        const int key = quarter * 32 + lane;
+        const uint32_t trow = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(group * 128);
+        float* slse = reinterpret_cast<float*>(smem + L::LSE_OFF) + group * 128;
+        float* ssum = reinterpret_cast<float*>(smem + L::SUM_OFF);
+        // log2-domain lse of column `key` of tile t; a row that saw nothing adds nothing
+        auto lse_of = [&](int t) -> float {
+            const int i = t * x.tt + key / x.grp;
+            if (key >= x.tt * x.grp || i >= r.n_new) return INFINITY;
+            const float v = x.lse[(size_t(r.q0) + i) * a.Hq + size_t(g) * x.grp + key % x.grp];
+            return v > -INFINITY ? v * 1.4426950408889634f : INFINITY;
+        };
+        auto ex2 = [](float v) {
+            float y;
+            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v));
+            return y;
+        };
+        int n = 0;
+        bool ok = true;
+        for (int b = b0; b < b1; ++b) {
+            const int j = b * PW_BM + key;
+            float sum = 0.f;
+            for (int t = first_tile(b); t < ntile; ++t, ++n) {
+                if ((n & 1) != group) continue;
+                const float mine = lse_of(t);
+                asm volatile("bar.sync %0, 128;" :: "r"(2 + group) : "memory");   // the last tile's values are read
+                slse[key] = mine;
+                asm volatile("bar.sync %0, 128;" :: "r"(2 + group) : "memory");
+                ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&sfull[group], uint32_t(n >> 1) & 1u, a.status));
+                if (ok) {
+                    tc::fence_after_sync();
+                    const int t0 = t * x.tt, cols = min(r.n_new - t0, x.tt) * x.grp;   // columns with a token
+                    // causal: a new row is seen by the tokens from its own on
+                    const int s = j - r.n_old, from = a.mask || s <= t0 ? 0 : (s - t0) * x.grp;
+                    float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                    for (int c0 = 0; c0 < cols; c0 += 32) {
+                        uint32_t v[32];
+                        tc::tmem_ld32(trow + uint32_t(c0), v);
+                        const bool whole = c0 + 32 <= cols && from <= c0 && !(a.mask && s >= 0);
+                        if (__all_sync(0xffffffffu, whole)) {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                const float4 z = *reinterpret_cast<const float4*>(slse + c0 + e);
+                                part[0] += ex2(fmaf(__uint_as_float(v[e]), x.sl2, -z.x));
+                                part[1] += ex2(fmaf(__uint_as_float(v[e + 1]), x.sl2, -z.y));
+                                part[2] += ex2(fmaf(__uint_as_float(v[e + 2]), x.sl2, -z.z));
+                                part[3] += ex2(fmaf(__uint_as_float(v[e + 3]), x.sl2, -z.w));
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const int col = c0 + e;
+                                bool seen = col < cols && col >= from;
+                                if (seen && a.mask && s >= 0)
+                                    seen = s < r.n_new &&
+                                           a.mask[(size_t(c) * a.S + t0 + col / x.grp) * a.S + s] != 0;
+                                if (seen) part[e & 3] += ex2(fmaf(__uint_as_float(v[e]), x.sl2, -slse[col]));
+                            }
+                            __syncwarp();
+                        }
+                    }
+                    sum += (part[0] + part[1]) + (part[2] + part[3]);
+                    tc::fence_before_sync();
+                }
+                __syncwarp();
+                if (lane == 0 && ok) mbar_arrive(&sfree[group]);
+            }
+            // the groups' sums of the block: group 1 hands over its own, by block parity
+            if (group == 1) ssum[(b & 1) * 128 + key] = sum;
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            if (group == 0 && j < r.n_keys && ok) {
+                sum += ssum[(b & 1) * 128 + key];
+                float* w = x.weights + size_t(cg) * (size_t(a.max_pages) << a.log2_page) + j;
+                *w = j < r.n_old ? fmaf(x.decay, *w, sum) : sum;
+            }
         }
     }
-    const int grp = a.Hq / a.Hkv;
-    float sum = 0.f;
-    for (int i = 0; i < r.n_new; ++i)
-        for (int hg = 0; hg < grp; ++hg) {
-            const size_t row = (size_t(r.q0) + i) * a.Hq + g * grp + hg;
-            __syncthreads();
-            for (int d = threadIdx.x; d < D; d += PW_NT) sq[d] = to_float(q[row * D + d]);
-            __syncthreads();
-            if (!held || !paged_sees(a, r, c, i, j)) continue;
-            float x = 0.f;
-#pragma unroll
-            for (int d = 0; d < D; ++d) x = fmaf(sq[d], key[d], x);
-            const float l = lse[row];
-            if (l > -INFINITY) sum += expf(x * scale - l);
-        }
-    if (real) {
-        float* w = weights + size_t(cg) * (size_t(a.max_pages) << a.log2_page) + j;
-        *w = j < r.n_old ? fmaf(decay, *w, sum) : sum;
-    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 1) tc::tmem_dealloc(tmem, 256);
+}
+
+// ----------------------------------------------------------------------------- host
+
+template <int D>
+static int launch_weights_t(const CUtensorMap& tq, const CUtensorMap& tk, const PwArgs& x, cudaStream_t stream) {
+    auto kern = paged_weights_kernel<D>;
+    const size_t smem = PwSmem<D>::TOTAL;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess)
+        return DARTREE_ECUDA;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned(x.nchunk) * unsigned(x.a.C) * x.a.Hkv);
+    cfg.blockDim = dim3(PW_NT);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1] = {pdl_attribute()};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    KTimer kt_(KID_PAGED_WEIGHTS, stream);
+    return cudaLaunchKernelEx(&cfg, kern, tq, tk, x) == cudaSuccess ? DARTREE_OK : DARTREE_ECUDA;
 }
 
 int launch_paged_weights(const PagedArgs& a, const void* q, const float* lse, float scale, float decay,
                          float* weights, cudaStream_t stream) {
-    const int blocks = ((a.max_pages << a.log2_page) + PW_NT - 1) / PW_NT;
-    const unsigned grid = unsigned(a.C) * a.Hkv * blocks;
-    KTimer kt_(KID_PAGED_WEIGHTS, stream);
-    if (a.D == 64)
-        paged_weights_kernel<64><<<grid, PW_NT, 0, stream>>>(a, static_cast<const bf16_t*>(q), lse, scale, decay,
-                                                             weights, blocks);
-    else
-        paged_weights_kernel<128><<<grid, PW_NT, 0, stream>>>(a, static_cast<const bf16_t*>(q), lse, scale, decay,
-                                                              weights, blocks);
-    return cudaGetLastError() == cudaSuccess ? DARTREE_OK : DARTREE_ECUDA;
+    PwArgs x{a, a.Hq / a.Hkv, 0, 0, 0, scale * 1.4426950408889634f, decay, lse, weights};
+    x.tt = 128 / x.grp < a.S ? 128 / x.grp : a.S;
+    x.tiles = (a.S + x.tt - 1) / x.tt;
+    const int64_t heads = int64_t(a.C) * a.Hkv;
+    const int64_t blocks = ((int64_t(a.max_pages) << a.log2_page) + PW_BM - 1) / PW_BM;
+    int64_t n = (4 * int64_t(num_sms()) + heads - 1) / heads;
+    if (n > blocks) n = blocks;
+    x.nchunk = n < 1 ? 1 : int(n);
+    CUtensorMap tq, tk;
+    // (a batch without tokens has no queries: its map is never used)
+    if (!make_query_map(&tq, a, a.T > 0 ? q : a.k, x.tt) || !make_page_map(&tk, a, a.k)) return DARTREE_ECUDA;
+    return a.D == 64 ? launch_weights_t<64>(tq, tk, x, stream) : launch_weights_t<128>(tq, tk, x, stream);
 }
 
 }  // namespace dartree

@@ -297,7 +297,7 @@ DARTREE_API int dartree_tree_attention(const dartree_attn_params* p, const void*
  *                 row c * S + i of q
  *   q_start       [C + 1], ascending: request c has q_start[c+1] - q_start[c] <= S new
  *                 tokens, in rows q_start[c] .. q_start[c+1] - 1 of q; rows outside
- *                 [q_start[0], q_start[C]) are neither read nor written
+ *                 [q_start[0], q_start[C]) are not used and not written
  *   tree          (q_start NULL only) the new tokens are the S slots of a verification
  *                 tree; slots from tree->n_nodes[c] on are not stored, and their output
  *                 rows (lse too) are zero
