@@ -28,22 +28,23 @@ namespace dartree {
 
 constexpr int PW_BM = 128;   // keys of a block
 constexpr int PW_NT = 320;   // producer, MMA, two groups of four warps
-constexpr int PW_KS = 3;     // stages of the key ring
-constexpr int PW_QS = 3;     // stages of the query ring
 
 template <int D>
 struct PwSmem {
     static constexpr int PANELS = D / 64;
     static constexpr size_t PANEL = size_t(PW_BM) * 128;
     static constexpr size_t TILE = PANELS * PANEL;
-    static constexpr size_t Q_OFF = PW_KS * TILE;
-    static constexpr size_t LSE_OFF = Q_OFF + PW_QS * TILE;             // float [2 groups][128]
+    // stages of the two rings: a single query tile stays, and the keys have the longer ring;
+    // otherwise the queries stream past a block of keys. 96 KB: two CTAs per SM
+    static constexpr int SHORT = D == 64 ? 2 : 1, LONG = D == 64 ? 4 : 2;
+    static constexpr int MAXS = 4;                                       // barriers per ring
+    static constexpr size_t LSE_OFF = (SHORT + LONG) * TILE;            // float [2 groups][128]
     static constexpr size_t SUM_OFF = LSE_OFF + 2 * 128 * 4;            // float [2 blocks][128]
     static constexpr size_t BAR_OFF = SUM_OFF + 2 * 128 * 4;
-    // kfull, kempty [KS], qfull, qempty [QS], sfull, sfree [2]
-    static constexpr size_t SLOT_OFF = BAR_OFF + 8 * (2 * PW_KS + 2 * PW_QS + 4);
+    // kfull, kempty, qfull, qempty [MAXS], sfull, sfree [2]
+    static constexpr size_t SLOT_OFF = BAR_OFF + 8 * (4 * MAXS + 4);
     static constexpr size_t TOTAL = SLOT_OFF + 16 + 1024;
-    static_assert(TOTAL <= 227 * 1024, "rings fit in shared memory");
+    static_assert(2 * (TOTAL + 1024) <= 228 * 1024, "two CTAs fit in shared memory");
 };
 
 struct PwArgs {
@@ -55,7 +56,7 @@ struct PwArgs {
 };
 
 template <int D>
-__global__ void __launch_bounds__(PW_NT, 1)
+__global__ void __launch_bounds__(PW_NT, 2)
     paged_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ PwArgs x) {
     using L = PwSmem<D>;
@@ -63,20 +64,18 @@ __global__ void __launch_bounds__(PW_NT, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
-    uint64_t* kempty = kfull + PW_KS;
-    uint64_t* qfull = kempty + PW_KS;
-    uint64_t* qempty = qfull + PW_QS;
-    uint64_t* sfull = qempty + PW_QS;   // [2] scores written, by buffer
+    uint64_t* kempty = kfull + L::MAXS;
+    uint64_t* qfull = kempty + L::MAXS;
+    uint64_t* qempty = qfull + L::MAXS;
+    uint64_t* sfull = qempty + L::MAXS;   // [2] scores written, by buffer
     uint64_t* sfree = sfull + 2;        // [2] scores read
     uint32_t* slot = reinterpret_cast<uint32_t*>(smem + L::SLOT_OFF);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < PW_KS; ++s) {
+        for (int s = 0; s < L::MAXS; ++s) {
             mbar_init(&kfull[s], 1);
             mbar_init(&kempty[s], 1);
-        }
-        for (int s = 0; s < PW_QS; ++s) {
             mbar_init(&qfull[s], 1);
             mbar_init(&qempty[s], 1);
         }
@@ -104,6 +103,9 @@ __global__ void __launch_bounds__(PW_NT, 1)
     const int b0 = chunk * per, b1 = min(blocks, b0 + per);
     const int ntile = (r.n_new + x.tt - 1) / x.tt;
     const bool once = x.tiles == 1;                       // one query tile: it stays in stage 0
+    const int ks_n = once ? L::LONG : L::SHORT, qs_n = once ? L::SHORT : L::LONG;
+    uint8_t* const kring = smem;
+    uint8_t* const qring = smem + ks_n * L::TILE;
     // the first tile that sees a row of block b
     auto first_tile = [&](int b) -> int { return a.mask ? 0 : max(0, (b * PW_BM - r.n_old) / x.tt); };
 
@@ -127,26 +129,26 @@ __global__ void __launch_bounds__(PW_NT, 1)
             bool ok = true;
             for (int b = b0; b < b1 && ok; ++b) {
                 const int next = b + 1 < b1 ? page_of(b + 1) : 0;
-                if (lane == 0 && nk >= PW_KS)
-                    ok = mbar_wait_bounded(&kempty[nk % PW_KS], uint32_t((nk / PW_KS) & 1) ^ 1u, a.status);
+                if (lane == 0 && nk >= ks_n)
+                    ok = mbar_wait_bounded(&kempty[nk % ks_n], uint32_t((nk / ks_n) & 1) ^ 1u, a.status);
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok) break;
-                const int ks = nk % PW_KS;
+                const int ks = nk % ks_n;
                 if (lane == 0) mbar_arrive_expect_tx(&kfull[ks], uint32_t(L::TILE));
                 __syncwarp();
                 if (mine)
-                    tc::tma_load_4d(smem + ks * L::TILE + pn * L::PANEL + size_t(su) * pr * 128, &tmK, 64 * pn,
+                    tc::tma_load_4d(kring + ks * L::TILE + pn * L::PANEL + size_t(su) * pr * 128, &tmK, 64 * pn,
                                     (b * PW_BM + su * pr) & (a.page - 1), g, pg, &kfull[ks]);
                 ++nk;
                 if (lane == 0 && !(once && nq > 0))
                     for (int t = first_tile(b); t < ntile && ok; ++t) {
-                        const int qs = nq % PW_QS;
-                        if (nq >= PW_QS)
-                            ok = mbar_wait_bounded(&qempty[qs], uint32_t((nq / PW_QS) & 1) ^ 1u, a.status);
+                        const int qs = nq % qs_n;
+                        if (nq >= qs_n)
+                            ok = mbar_wait_bounded(&qempty[qs], uint32_t((nq / qs_n) & 1) ^ 1u, a.status);
                         if (!ok) break;
                         mbar_arrive_expect_tx(&qfull[qs], qbytes);
                         for (int p = 0; p < L::PANELS; ++p)
-                            tc::tma_load_3d(smem + L::Q_OFF + qs * L::TILE + p * L::PANEL, &tmQ, 64 * p, g * x.grp,
+                            tc::tma_load_3d(qring + qs * L::TILE + p * L::PANEL, &tmQ, 64 * p, g * x.grp,
                                             r.q0 + t * x.tt, &qfull[qs]);
                         ++nq;
                     }
@@ -155,10 +157,10 @@ __global__ void __launch_bounds__(PW_NT, 1)
             }
             // copies issued and not yet seen complete land before the CTA can exit
             if (lane == 0) {
-                for (int q = max(nk - PW_KS, 0); q < nk; ++q)
-                    mbar_wait_bounded(&kfull[q % PW_KS], uint32_t(q / PW_KS) & 1u, a.status);
-                for (int q = max(nq - PW_QS, 0); q < nq; ++q)
-                    mbar_wait_bounded(&qfull[q % PW_QS], uint32_t(q / PW_QS) & 1u, a.status);
+                for (int q = max(nk - ks_n, 0); q < nk; ++q)
+                    mbar_wait_bounded(&kfull[q % ks_n], uint32_t(q / ks_n) & 1u, a.status);
+                for (int q = max(nq - qs_n, 0); q < nq; ++q)
+                    mbar_wait_bounded(&qfull[q % qs_n], uint32_t(q / qs_n) & 1u, a.status);
             }
         }
     } else if (warp == 1) {
@@ -168,15 +170,15 @@ __global__ void __launch_bounds__(PW_NT, 1)
             int nk = 0, nq = 0, n = 0;
             bool ok = true;
             for (int b = b0; b < b1 && ok; ++b, ++nk) {
-                const int ks = nk % PW_KS;
-                ok = mbar_wait_bounded(&kfull[ks], uint32_t(nk / PW_KS) & 1u, a.status);
+                const int ks = nk % ks_n;
+                ok = mbar_wait_bounded(&kfull[ks], uint32_t(nk / ks_n) & 1u, a.status);
                 for (int t = first_tile(b); t < ntile && ok; ++t, ++n) {
-                    const int qs = once ? 0 : nq % PW_QS;
-                    ok = mbar_wait_bounded(&qfull[qs], once ? 0u : uint32_t(nq / PW_QS) & 1u, a.status);
+                    const int qs = once ? 0 : nq % qs_n;
+                    ok = mbar_wait_bounded(&qfull[qs], once ? 0u : uint32_t(nq / qs_n) & 1u, a.status);
                     if (ok && n >= 2) ok = mbar_wait_bounded(&sfree[n & 1], uint32_t((n >> 1) - 1) & 1u, a.status);
                     if (!ok) break;
                     tc::fence_after_sync();
-                    const uint32_t ka = smem_u32(smem + ks * L::TILE), qb = smem_u32(smem + L::Q_OFF + qs * L::TILE);
+                    const uint32_t ka = smem_u32(kring + ks * L::TILE), qb = smem_u32(qring + qs * L::TILE);
 #pragma unroll
                     for (int p = 0; p < L::PANELS; ++p) {
                         const uint64_t da = tc::desc_sw128_kmajor(ka + uint32_t(p * L::PANEL));
@@ -202,11 +204,12 @@ __global__ void __launch_bounds__(PW_NT, 1)
         const uint32_t trow = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(group * 128);
         float* slse = reinterpret_cast<float*>(smem + L::LSE_OFF) + group * 128;
         float* ssum = reinterpret_cast<float*>(smem + L::SUM_OFF);
+        const int kti = key / x.grp, khg = key - kti * x.grp;   // token and head of column `key` of a tile
         // log2-domain lse of column `key` of tile t; a row that saw nothing adds nothing
         auto lse_of = [&](int t) -> float {
-            const int i = t * x.tt + key / x.grp;
-            if (key >= x.tt * x.grp || i >= r.n_new) return INFINITY;
-            const float v = x.lse[(size_t(r.q0) + i) * a.Hq + size_t(g) * x.grp + key % x.grp];
+            const int i = t * x.tt + kti;
+            if (kti >= x.tt || i >= r.n_new) return INFINITY;
+            const float v = x.lse[(size_t(r.q0) + i) * a.Hq + size_t(g) * x.grp + khg];
             return v > -INFINITY ? v * 1.4426950408889634f : INFINITY;
         };
         auto ex2 = [](float v) {
@@ -214,17 +217,36 @@ __global__ void __launch_bounds__(PW_NT, 1)
             asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v));
             return y;
         };
+        float* const wrow = x.weights + size_t(cg) * (size_t(a.max_pages) << a.log2_page);
         int n = 0;
         bool ok = true;
+        // this group's next tile's values are fetched while the current one is added up
+        int next_t = -1;
+        float next_lse = 0.f;
         for (int b = b0; b < b1; ++b) {
             const int j = b * PW_BM + key;
+            const bool owner = ntile == 1 ? (n & 1) == group : group == 0;   // writes the block's weights
+            float before = 0.f;
+            if (owner && j < r.n_old) before = wrow[j];
             float sum = 0.f;
             for (int t = first_tile(b); t < ntile; ++t, ++n) {
                 if ((n & 1) != group) continue;
-                const float mine = lse_of(t);
-                asm volatile("bar.sync %0, 128;" :: "r"(2 + group) : "memory");   // the last tile's values are read
-                slse[key] = mine;
-                asm volatile("bar.sync %0, 128;" :: "r"(2 + group) : "memory");
+                const float mine = next_t == t ? next_lse : lse_of(t);
+                if (ntile > 1 || next_t != t) {                               // (a lone tile's stay)
+                    asm volatile("bar.sync %0, 128;" :: "r"(2 + group) : "memory");  // the last tile's are read
+                    slse[key] = mine;
+                    asm volatile("bar.sync %0, 128;" :: "r"(2 + group) : "memory");
+                }
+                next_t = t;
+                next_lse = mine;
+                if (ntile > 1) {
+                    next_t = t + 2;
+                    if (next_t >= ntile && b + 1 < b1) {
+                        const int f = first_tile(b + 1);
+                        next_t = f + (((n + ntile - t) & 1) != group ? 1 : 0);
+                    }
+                    if (next_t < ntile) next_lse = lse_of(next_t);
+                }
                 ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&sfull[group], uint32_t(n >> 1) & 1u, a.status));
                 if (ok) {
                     tc::fence_after_sync();
@@ -232,10 +254,7 @@ __global__ void __launch_bounds__(PW_NT, 1)
                     // causal: a new row is seen by the tokens from its own on
                     const int s = j - r.n_old, from = a.mask || s <= t0 ? 0 : (s - t0) * x.grp;
                     float part[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-                    for (int c0 = 0; c0 < cols; c0 += 32) {
-                        uint32_t v[32];
-                        tc::tmem_ld32(trow + uint32_t(c0), v);
+                    auto add = [&](const uint32_t (&v)[32], int c0) {
                         const bool whole = c0 + 32 <= cols && from <= c0 && !(a.mask && s >= 0);
                         if (__all_sync(0xffffffffu, whole)) {
 #pragma unroll
@@ -258,6 +277,12 @@ __global__ void __launch_bounds__(PW_NT, 1)
                             }
                             __syncwarp();
                         }
+                    };
+#pragma unroll 1
+                    for (int c0 = 0; c0 < cols; c0 += 32) {
+                        uint32_t v[32];
+                        tc::tmem_ld32(trow + uint32_t(c0), v);
+                        add(v, c0);
                     }
                     sum += (part[0] + part[1]) + (part[2] + part[3]);
                     tc::fence_before_sync();
@@ -265,14 +290,12 @@ __global__ void __launch_bounds__(PW_NT, 1)
                 __syncwarp();
                 if (lane == 0 && ok) mbar_arrive(&sfree[group]);
             }
-            // the groups' sums of the block: group 1 hands over its own, by block parity
-            if (group == 1) ssum[(b & 1) * 128 + key] = sum;
-            asm volatile("bar.sync 1, 256;" ::: "memory");
-            if (group == 0 && j < r.n_keys && ok) {
-                sum += ssum[(b & 1) * 128 + key];
-                float* w = x.weights + size_t(cg) * (size_t(a.max_pages) << a.log2_page) + j;
-                *w = j < r.n_old ? fmaf(x.decay, *w, sum) : sum;
+            if (ntile > 1) {  // the groups' sums of the block: group 1 hands over its own, by block parity
+                if (group == 1) ssum[(b & 1) * 128 + key] = sum;
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                if (group == 0) sum += ssum[(b & 1) * 128 + key];
             }
+            if (owner && j < r.n_keys && ok) wrow[j] = j < r.n_old ? fmaf(x.decay, before, sum) : sum;
         }
     }
     tc::fence_before_sync();
