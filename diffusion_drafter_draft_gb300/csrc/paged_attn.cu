@@ -15,7 +15,7 @@
 //   warp 1      issues S = Q K^T (both operands in shared memory) and O += P V (P in
 //               tensor memory over S's columns, V as an MN-major operand straight from
 //               its pages: nothing is transposed)
-//   warps 2..   softmax, one thread per row: the row's 128 scores in registers, P in bf16
+//   warps 4..   softmax, one thread per row: the row's 128 scores in registers, P in bf16
 //               back to tensor memory; O is rescaled only when the maximum grows by more
 //               than 2^8
 // With NT = 2 the tensor cores work on one tile while the other tile's softmax runs.
@@ -45,8 +45,8 @@ struct PgSmem {
     static constexpr size_t TILE = PANELS * PANEL;              // a query tile, or a block's keys or values
     static constexpr size_t RING_OFF = NT * TILE;
     static constexpr size_t BAR_OFF = RING_OFF + ST * TILE;
-    // qfull, full[ST], empty[ST], sfull[NT], pfull[NT], ofull[NT]
-    static constexpr size_t SLOT_OFF = BAR_OFF + 8 * (1 + 2 * ST + 3 * NT);
+    // qfull, vclean, full[ST], empty[ST], sfull[NT], pfull[NT], ofull[NT]
+    static constexpr size_t SLOT_OFF = BAR_OFF + 8 * (2 + 2 * ST + 3 * NT);
     static constexpr size_t TOTAL = SLOT_OFF + 16 + 1024;       // (+ alignment of the base to 1024)
     static_assert(TOTAL <= 227 * 1024, "tiles and ring fit in shared memory");
 };
@@ -76,8 +76,34 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Two fp32 values per instruction (fma, add) and the larger of three.
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair(float lo, float hi) { return pair(__float_as_uint(lo), __float_as_uint(hi)); }
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 template <int D, int NT, int ST>
-__global__ void __launch_bounds__(64 + 128 * NT, NT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PgArgs x) {
     using L = PgSmem<D, NT, ST>;
@@ -87,7 +113,8 @@ __global__ void __launch_bounds__(64 + 128 * NT, NT == 1 ? 2 : 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* qfull = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
-    uint64_t* full = qfull + 1;       // [ST] stage landed
+    uint64_t* vclean = qfull + 1;     // value rows past the end zeroed (last block)
+    uint64_t* full = qfull + 2;       // [ST] stage landed
     uint64_t* empty = full + ST;      // [ST] the MMAs that read it are done
     uint64_t* sfull = empty + ST;     // [NT] scores written (and every earlier MMA done)
     uint64_t* pfull = sfull + NT;     // [NT] P written
@@ -97,6 +124,7 @@ __global__ void __launch_bounds__(64 + 128 * NT, NT == 1 ? 2 : 1)
 
     if (threadIdx.x == 0) {
         mbar_init(qfull, 1);
+        mbar_init(vclean, 1);
         for (int s = 0; s < ST; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
@@ -133,6 +161,12 @@ __global__ void __launch_bounds__(64 + 128 * NT, NT == 1 ? 2 : 1)
     const int per = (blocks + x.nchunk - 1) / x.nchunk;
     const int b0 = chunk * per, nblk = max(min(blocks, b0 + per) - b0, 0);
 
+    // the softmax holds a row of scores in registers: its warpgroups take over registers that the
+    // first one was launched with (NT = 2: 384 x 168 >= 128 x 80 + 256 x 208; NT = 1: 256 x 128 =
+    // 128 x 56 + 128 x 200)
+    if (warp < 4) {
+    if (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0) {
         // ---------------------------------------------------------------- producer
         if (nblk > 0) {
@@ -176,6 +210,23 @@ __global__ void __launch_bounds__(64 + 128 * NT, NT == 1 ? 2 : 1)
                 if (!ok) break;
                 pg = next;
             }
+            // the last block's value rows past the end are zeroed once they have landed
+            const int have = r.n_keys - (b0 + nblk - 1) * PG_BN, vl = 2 * nblk - 1;
+            if (have < PG_BN && issued > vl) {
+                bool ok = true;
+                if (lane == 0) ok = mbar_wait_bounded(&full[vl % ST], uint32_t(vl / ST) & 1u, a.status);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (ok) {
+                    uint8_t* vb = smem + L::RING_OFF + (vl % ST) * L::TILE + size_t(have) * 128;
+                    for (int e = lane; e < (PG_BN - have) * 8; e += 32)
+#pragma unroll
+                        for (int p = 0; p < L::PANELS; ++p)
+                            reinterpret_cast<uint4*>(vb + p * L::PANEL)[e] = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(vclean);
+                }
+            }
             // copies issued and not yet seen complete land before the CTA can exit
             if (lane == 0) {
                 mbar_wait_bounded(qfull, 0, a.status);
@@ -185,13 +236,11 @@ __global__ void __launch_bounds__(64 + 128 * NT, NT == 1 ? 2 : 1)
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issue
-        if (nblk > 0) {
+        if (nblk > 0 && lane == 0) {
             constexpr uint32_t idS = tc::idesc_bf16_f32(PG_BM, PG_BN);
             constexpr uint32_t idO = tc::idesc_bf16_f32(PG_BM, D) | tc::IDESC_B_MNMAJOR;
             auto wait = [&](uint64_t* bar, int phase) -> bool {
-                bool ok = true;
-                if (lane == 0) ok = mbar_wait_bounded(bar, uint32_t(phase) & 1u, a.status);
-                return __shfl_sync(0xffffffffu, ok, 0);
+                return mbar_wait_bounded(bar, uint32_t(phase) & 1u, a.status);
             };
             auto scores = [&](int t, int idx) {
                 const uint32_t kb = smem_u32(smem + L::RING_OFF + (idx % ST) * L::TILE);
@@ -207,7 +256,7 @@ __global__ void __launch_bounds__(64 + 128 * NT, NT == 1 ? 2 : 1)
                 tc::mma_commit(&sfull[t]);
             };
             bool ok = wait(qfull, 0) && wait(&full[0], 0);
-            if (ok && lane == 0) {
+            if (ok) {
                 tc::fence_after_sync();
                 for (int t = 0; t < nact; ++t) scores(t, 0);
                 tc::mma_commit(&empty[0]);
@@ -215,47 +264,34 @@ __global__ void __launch_bounds__(64 + 128 * NT, NT == 1 ? 2 : 1)
             for (int i = 0; i < nblk && ok; ++i) {
                 const int vi = 2 * i + 1, ki = 2 * i + 2;
                 const bool last = i + 1 == nblk;
+                ok = wait(&full[vi % ST], vi / ST) && (last || wait(&full[ki % ST], ki / ST));
+                if (ok && r.n_keys < (b0 + i + 1) * PG_BN) ok = wait(vclean, 0);
                 for (int t = 0; t < nact && ok; ++t) {
-                    if (t == 0) {
-                        ok = wait(&full[vi % ST], vi / ST);
-                        const int have = r.n_keys - (b0 + i) * PG_BN;   // value rows of the block
-                        if (ok && have < PG_BN) {                       // zero the others (last block only)
-                            uint8_t* vb = smem + L::RING_OFF + (vi % ST) * L::TILE;
-                            for (int e = lane; e < (PG_BN - have) * 8; e += 32)
-#pragma unroll
-                                for (int p = 0; p < L::PANELS; ++p)
-                                    reinterpret_cast<uint4*>(vb + p * L::PANEL + size_t(have) * 128)[e] =
-                                        make_uint4(0, 0, 0, 0);
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                        }
-                        if (ok && !last) ok = wait(&full[ki % ST], ki / ST);
-                    }
-                    ok = ok && wait(&pfull[t], i);
+                    ok = wait(&pfull[t], i);
                     if (!ok) break;
-                    if (lane == 0) {
-                        tc::fence_after_sync();
-                        const uint64_t db = tc::desc_sw128_mnmajor(
-                            smem_u32(smem + L::RING_OFF + (vi % ST) * L::TILE), uint32_t(L::PANEL));
+                    tc::fence_after_sync();
+                    const uint64_t db = tc::desc_sw128_mnmajor(smem_u32(smem + L::RING_OFF + (vi % ST) * L::TILE),
+                                                               uint32_t(L::PANEL));
 #pragma unroll
-                        for (int kk = 0; kk < PG_BN / 16; ++kk)
-                            tc::mma_bf16_ts(tmem + OCOL + uint32_t(t * D), tmem + uint32_t(t * PG_BN + 8 * kk),
-                                            db + 128u * kk, idO, i > 0 || kk > 0);
-                        if (t == nact - 1) tc::mma_commit(&empty[vi % ST]);
-                        if (!last) {
-                            scores(t, ki);
-                            if (t == nact - 1) tc::mma_commit(&empty[ki % ST]);
-                        } else {
-                            tc::mma_commit(&ofull[t]);
-                        }
+                    for (int kk = 0; kk < PG_BN / 16; ++kk)
+                        tc::mma_bf16_ts(tmem + OCOL + uint32_t(t * D), tmem + uint32_t(t * PG_BN + 8 * kk),
+                                        db + 128u * kk, idO, i > 0 || kk > 0);
+                    if (t == nact - 1) tc::mma_commit(&empty[vi % ST]);
+                    if (!last) {
+                        scores(t, ki);
+                        if (t == nact - 1) tc::mma_commit(&empty[ki % ST]);
+                    } else {
+                        tc::mma_commit(&ofull[t]);
                     }
-                    __syncwarp();
                 }
             }
         }
+    }
     } else {
         // ---------------------------------------------------------------- softmax
-        const int t = (warp - 2) >> 2, quarter = warp & 3;
+        if (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        const int t = (warp - 4) >> 2, quarter = warp & 3;
         const int row = quarter * 32 + lane;                     // row of the tile (TMEM lane)
         const int ti = row / x.grp, hg = row - ti * x.grp;
         const int i_tok = t0 + t * x.tt + ti;                    // token of the request
@@ -267,6 +303,22 @@ __global__ void __launch_bounds__(64 + 128 * NT, NT == 1 ? 2 : 1)
         const uint32_t scol = trow + uint32_t(t * PG_BN), ocol = trow + OCOL + uint32_t(t * D);
         float m = -INFINITY, l = 0.f;
         bool ok = true;
+        // the tree's mask for 32 keys from `key` on: the rows of this warp's tokens, lane q reading
+        // a token's slot q, and the vote is the word
+        auto tree_bits = [&](int key) -> uint32_t {
+            const int tok0 = (quarter * 32) / x.grp, tok1 = (quarter * 32 + 31) / x.grp;
+            const int sl = key + lane - r.n_old;
+            uint32_t bits = 0;
+            for (int q = tok0; q <= tok1; ++q) {
+                const int i_q = t0 + t * x.tt + q;
+                bool v = sl < 0;
+                if (sl >= 0 && sl < r.n_new && q < x.tt && i_q < r.n_new)
+                    v = a.mask[(size_t(c) * a.S + i_q) * a.S + sl] != 0;
+                const uint32_t word = __ballot_sync(0xffffffffu, v);
+                if (q == ti) bits = word;
+            }
+            return bits;
+        };
         if (t < nact) {
             for (int i = 0; i < nblk; ++i) {
                 ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&sfull[t], uint32_t(i) & 1u, a.status));
@@ -274,79 +326,98 @@ __global__ void __launch_bounds__(64 + 128 * NT, NT == 1 ? 2 : 1)
                     tc::fence_after_sync();
                     const int key0 = (b0 + i) * PG_BN;
                     uint32_t s[4][32];
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) tc::tmem_ld32_async(scol + 32u * w, s[w]);
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) tc::tmem_wait_ld(s[w]);
-                    // hidden keys: the block's columns from `lim` on, and what the tree's mask hides
-                    const int lim = limit - key0;
-                    if (a.mask && key0 + PG_BN > r.n_old) {
-                        // the mask rows of this warp's tokens, 32 slots at a time: lane q reads slot
-                        // q of a token's word and the vote is the word
-                        const int tok0 = (quarter * 32) / x.grp, tok1 = (quarter * 32 + 31) / x.grp;
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            const int sl = key0 + 32 * w + lane - r.n_old;
-                            uint32_t bits = 0;
-                            for (int q = tok0; q <= tok1; ++q) {
-                                const int i_q = t0 + t * x.tt + q;
-                                bool v = sl < 0;
-                                if (sl >= 0 && sl < r.n_new && q < x.tt && i_q < r.n_new)
-                                    v = a.mask[(size_t(c) * a.S + i_q) * a.S + sl] != 0;
-                                const uint32_t word = __ballot_sync(0xffffffffu, v);
-                                if (q == ti) bits = word;
-                            }
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!((bits >> e) & 1u) || 32 * w + e >= lim) s[w][e] = 0xff800000u;
-                        }
-                    } else if (__any_sync(0xffffffffu, lim < PG_BN)) {
-#pragma unroll
-                        for (int w = 0; w < 4; ++w)
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (32 * w + e >= lim) s[w][e] = 0xff800000u;  // -inf
-                    }
-                    float mx = -INFINITY;
-                    {
-                        float p[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-#pragma unroll
-                            for (int w = 0; w < 4; ++w) p[w] = fmaxf(p[w], __uint_as_float(s[w][e]));
-                        mx = fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3]));
-                    }
-                    mx *= x.sl2;                                 // (sl2 > 0: -inf stays)
-                    const bool grow = mx > m + PG_RESCALE || (m == -INFINITY && mx > -INFINITY);
-                    const bool resc = grow && m > -INFINITY;
-                    if (__any_sync(0xffffffffu, resc)) {         // O's products up to block i - 1 are done
-                        const float f = resc ? ex2(m - mx) : 1.0f;
-#pragma unroll 1
-                        for (int c0 = 0; c0 < D; c0 += 32) {
-                            uint32_t o[32];
-                            tc::tmem_ld32(ocol + uint32_t(c0), o);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tc::tmem_st32(ocol + uint32_t(c0), o);
-                        }
-                        l *= f;
-                    }
-                    if (grow) m = mx;
-                    const float ms = m > -INFINITY ? m : 0.f;    // (a row that has seen nothing: 2^-inf = 0)
-                    float ls[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
+                    const int lim = limit - key0;                // columns from `lim` on are hidden
+                    const bool tree = a.mask && key0 + PG_BN > r.n_old;
+                    const bool cut = tree || __any_sync(0xffffffffu, lim < PG_BN);
+                    // 32 scores weighted against the maximum `base`: P to tensor memory (columns 16 w:
+                    // over scores that are in registers), their sum and largest
+                    float p[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    uint64_t ls[4] = {0, 0, 0, 0};
+                    const uint64_t sl = pair(x.sl2, x.sl2);
+                    auto weigh = [&](const uint32_t (&v)[32], int w, uint64_t off, bool top) {
                         uint32_t pk[16];
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
-                            const float p0 = ex2(fmaf(__uint_as_float(s[w][e]), x.sl2, -ms));
-                            const float p1 = ex2(fmaf(__uint_as_float(s[w][e + 1]), x.sl2, -ms));
-                            ls[(e >> 1) & 3] += p0 + p1;
+                            if (top)
+                                p[(e >> 1) & 3] =
+                                    max3(p[(e >> 1) & 3], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+                            float y0, y1;
+                            unpair(fma2(pair(v[e], v[e + 1]), sl, off), y0, y1);
+                            const float p0 = ex2(y0), p1 = ex2(y1);
+                            ls[(e >> 1) & 3] = add2(ls[(e >> 1) & 3], pair(p0, p1));
                             pk[e / 2] = pack2(p0, p1);
                         }
                         tc::tmem_st16_async(scol + 16u * w, pk);
+                    };
+                    bool grow = true;
+                    float mx;
+                    tc::tmem_ld32_async(scol, s[0]);
+                    if (i > 0 && !cut) {
+                        // the usual block: weighted as the scores arrive, against the maximum so far
+                        const float ms = m > -INFINITY ? m : 0.f;
+                        const uint64_t off = pair(-ms, -ms);
+                        tc::tmem_wait_ld(s[0]);
+                        tc::tmem_ld32_async(scol + 32u, s[1]);
+                        weigh(s[0], 0, off, true);
+                        tc::tmem_wait_ld(s[1]);
+                        tc::tmem_ld32_async(scol + 64u, s[2]);
+                        weigh(s[1], 1, off, true);
+                        tc::tmem_wait_ld(s[2]);
+                        tc::tmem_ld32_async(scol + 96u, s[3]);
+                        weigh(s[2], 2, off, true);
+                        tc::tmem_wait_ld(s[3]);
+                        weigh(s[3], 3, off, true);
+                        mx = fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])) * x.sl2;   // (sl2 > 0: -inf stays)
+                        grow = mx > m + PG_RESCALE || (m == -INFINITY && mx > -INFINITY);
+                    } else {
+#pragma unroll
+                        for (int w = 1; w < 4; ++w) tc::tmem_ld32_async(scol + 32u * w, s[w]);
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) tc::tmem_wait_ld(s[w]);
+                        if (cut) {
+#pragma unroll
+                            for (int w = 0; w < 4; ++w) {
+                                const uint32_t bits = tree ? tree_bits(key0 + 32 * w) : 0xffffffffu;
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    if (!((bits >> e) & 1u) || 32 * w + e >= lim) s[w][e] = 0xff800000u;  // -inf
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2)
+#pragma unroll
+                            for (int w = 0; w < 4; ++w)
+                                p[w] = max3(p[w], __uint_as_float(s[w][e]), __uint_as_float(s[w][e + 1]));
+                        mx = fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])) * x.sl2;
+                        grow = mx > m + PG_RESCALE || (m == -INFINITY && mx > -INFINITY);
                     }
-                    l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                    const bool anew = i == 0 || cut;             // nothing weighted yet
+                    if (anew || __any_sync(0xffffffffu, grow)) {
+                        const bool resc = grow && m > -INFINITY;
+                        if (__any_sync(0xffffffffu, resc)) {     // O's products up to block i - 1 are done
+                            const float f = resc ? ex2(m - mx) : 1.0f;
+#pragma unroll 1
+                            for (int c0 = 0; c0 < D; c0 += 32) {
+                                uint32_t o[32];
+                                tc::tmem_ld32(ocol + uint32_t(c0), o);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tc::tmem_st32(ocol + uint32_t(c0), o);
+                            }
+                            l *= f;
+                        }
+                        if (grow) m = mx;
+                        const float ms = m > -INFINITY ? m : 0.f;    // (a row that has seen nothing: 2^-inf = 0)
+                        const uint64_t off = pair(-ms, -ms);
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) ls[w] = 0;
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) weigh(s[w], w, off, false);
+                    }
+                    float sum, sum1;
+                    unpair(add2(add2(ls[0], ls[1]), add2(ls[2], ls[3])), sum, sum1);
+                    sum += sum1;
+                    l += sum;
                     tc::tmem_wait_st();
                     tc::fence_before_sync();
                 }
@@ -536,7 +607,7 @@ static int launch_attn_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUt
         return DARTREE_ECUDA;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned(x.nchunk) * unsigned(x.a.C) * x.a.Hkv * ((x.tiles + NT - 1) / NT));
-    cfg.blockDim = dim3(64 + 128 * NT);
+    cfg.blockDim = dim3(128 + 128 * NT);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1] = {pdl_attribute()};
