@@ -15,6 +15,7 @@
 //   warp 1      issues S = Q K^T (both operands in shared memory) and O += P V (P in
 //               tensor memory over S's columns, V as an MN-major operand straight from
 //               its pages: nothing is transposed)
+//   warp 2      passes on the landing of a group's keys and values
 //   warps 4..   softmax, one thread per row: the row's 128 scores in registers, P in bf16
 //               back to tensor memory; O is rescaled only when the maximum grows by more
 //               than 2^8
@@ -131,7 +132,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
         }
         for (int t = 0; t < NT; ++t) {
             mbar_init(&sfull[t], 1);
-            mbar_init(&pfull[t], 4);
+            mbar_init(&pfull[t], 5);  // four softmax warps and warp 2
             mbar_init(&ofull[t], 1);
         }
         fence_mbar_init();
@@ -236,53 +237,92 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issue
-        if (nblk > 0 && lane == 0) {
+        // The tensor cores take MMAs about as fast as one thread issues them, and a barrier
+        // test costs that thread a few hundred cycles beside two softmax warps: so a group
+        // (O += P V of a tile, then its next S) waits for one barrier, pfull, which also
+        // counts the landing of what the group reads (warp 2), and the next group's is
+        // tested while this group's last MMAs are issued.
+        // (warp-uniform values, one elected lane: descriptors stay in uniform registers)
+        const int nb = __shfl_sync(0xffffffffu, nblk, 0), na = __shfl_sync(0xffffffffu, nact, 0);
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        if (nb > 0 && tc::elect_one()) {
             constexpr uint32_t idS = tc::idesc_bf16_f32(PG_BM, PG_BN);
             constexpr uint32_t idO = tc::idesc_bf16_f32(PG_BM, D) | tc::IDESC_B_MNMAJOR;
-            auto wait = [&](uint64_t* bar, int phase) -> bool {
-                return mbar_wait_bounded(bar, uint32_t(phase) & 1u, a.status);
-            };
-            auto scores = [&](int t, int idx) {
-                const uint32_t kb = smem_u32(smem + L::RING_OFF + (idx % ST) * L::TILE);
-                const uint32_t qb = smem_u32(smem + t * L::TILE);
+            constexpr uint32_t PSTEP = L::PANEL >> 4, TSTEP = L::TILE >> 4;  // descriptor steps (low word)
+            const uint32_t q0 = smem_u32(smem) >> 4, r0 = smem_u32(smem + L::RING_OFF) >> 4;
+            constexpr uint32_t KHI = uint32_t(tc::DESC_SW128_KMAJOR >> 32), KLO = uint32_t(tc::DESC_SW128_KMAJOR);
+            constexpr uint64_t VD = tc::desc_sw128_mnmajor_base(uint32_t(L::PANEL));
+            auto kdesc = [&](uint32_t at) { return (uint64_t(KHI) << 32) | (KLO | at); };
+            auto score = [&](int t, int s, int p) {   // 64 values of D
+                const uint32_t da = q0 + t * TSTEP + p * PSTEP, db = r0 + s * TSTEP + p * PSTEP;
 #pragma unroll
-                for (int p = 0; p < L::PANELS; ++p) {
-                    const uint64_t da = tc::desc_sw128_kmajor(qb + uint32_t(p * L::PANEL));
-                    const uint64_t db = tc::desc_sw128_kmajor(kb + uint32_t(p * L::PANEL));
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        tc::mma_bf16(tmem + uint32_t(t * PG_BN), da + 2u * kk, db + 2u * kk, idS, p > 0 || kk > 0);
-                }
-                tc::mma_commit(&sfull[t]);
+                for (int kk = 0; kk < 4; ++kk)
+                    tc::mma_bf16(tm + uint32_t(t * PG_BN), kdesc(da + 2u * kk), kdesc(db + 2u * kk), idS,
+                                 p > 0 || kk > 0);
             };
-            bool ok = wait(qfull, 0) && wait(&full[0], 0);
+            bool ok = mbar_wait_bounded(qfull, 0, a.status) && mbar_wait_bounded(&full[0], 0, a.status);
             if (ok) {
                 tc::fence_after_sync();
-                for (int t = 0; t < nact; ++t) scores(t, 0);
-                tc::mma_commit(&empty[0]);
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    if (t < na) {
+#pragma unroll
+                        for (int p = 0; p < L::PANELS; ++p) score(t, 0, p);
+                        tc::mma_commit(&sfull[t]);
+                    }
+                if (ST < 2 * nb) tc::mma_commit(&empty[0]);
             }
+            int vs = 1 % ST, ks = 2 % ST;             // stages of block i's values and block i + 1's keys
+            bool ready = false;
+            for (int i = 0; i < nb && ok; ++i) {
+                const bool last = i + 1 == nb;
+                // (a stage is handed back only when it is filled again)
+                const bool back_v = 2 * i + 1 + ST < 2 * nb, back_k = 2 * i + 2 + ST < 2 * nb;
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    if (t >= na) break;
+                    if (!ready) ok = mbar_wait_bounded(&pfull[t], uint32_t(i) & 1u, a.status);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    const uint32_t db = r0 + vs * TSTEP;
+#pragma unroll
+                    for (int kk = 0; kk < PG_BN / 16; ++kk)
+                        tc::mma_bf16_ts(tm + OCOL + uint32_t(t * D), tm + uint32_t(t * PG_BN + 8 * kk),
+                                        (VD & ~0xffffffffull) | (uint32_t(VD) | (db + 128u * kk)), idO,
+                                        i > 0 || kk > 0);
+                    const bool end_v = t == na - 1;
+                    if (end_v && back_v) tc::mma_commit(&empty[vs]);
+                    if (last) {
+                        ready = false;
+                        tc::mma_commit(&ofull[t]);
+                    } else {
+#pragma unroll
+                        for (int p = 0; p + 1 < L::PANELS; ++p) score(t, ks, p);
+                        ready = mbar_try_wait(end_v ? &pfull[0] : &pfull[NT - 1], uint32_t(end_v ? i + 1 : i) & 1u);
+                        score(t, ks, L::PANELS - 1);
+                        tc::mma_commit(&sfull[t]);
+                        if (end_v && back_k) tc::mma_commit(&empty[ks]);
+                    }
+                }
+                vs += 2;
+                if (vs >= ST) vs -= ST;
+                ks += 2;
+                if (ks >= ST) ks -= ST;
+            }
+        }
+    } else if (warp == 2) {
+        // ---------------------------------------------------------------- landing of the groups' operands
+        if (nblk > 0 && lane == 0) {
+            bool ok = true;
             for (int i = 0; i < nblk && ok; ++i) {
                 const int vi = 2 * i + 1, ki = 2 * i + 2;
                 const bool last = i + 1 == nblk;
-                ok = wait(&full[vi % ST], vi / ST) && (last || wait(&full[ki % ST], ki / ST));
-                if (ok && r.n_keys < (b0 + i + 1) * PG_BN) ok = wait(vclean, 0);
+                ok = mbar_wait_bounded(&full[vi % ST], uint32_t(vi / ST) & 1u, a.status) &&
+                     (last || mbar_wait_bounded(&full[ki % ST], uint32_t(ki / ST) & 1u, a.status));
+                if (ok && last && r.n_keys < (b0 + nblk) * PG_BN) ok = mbar_wait_bounded(vclean, 0, a.status);
                 for (int t = 0; t < nact && ok; ++t) {
-                    ok = wait(&pfull[t], i);
-                    if (!ok) break;
-                    tc::fence_after_sync();
-                    const uint64_t db = tc::desc_sw128_mnmajor(smem_u32(smem + L::RING_OFF + (vi % ST) * L::TILE),
-                                                               uint32_t(L::PANEL));
-#pragma unroll
-                    for (int kk = 0; kk < PG_BN / 16; ++kk)
-                        tc::mma_bf16_ts(tmem + OCOL + uint32_t(t * D), tmem + uint32_t(t * PG_BN + 8 * kk),
-                                        db + 128u * kk, idO, i > 0 || kk > 0);
-                    if (t == nact - 1) tc::mma_commit(&empty[vi % ST]);
-                    if (!last) {
-                        scores(t, ki);
-                        if (t == nact - 1) tc::mma_commit(&empty[ki % ST]);
-                    } else {
-                        tc::mma_commit(&ofull[t]);
-                    }
+                    if (i > 0) ok = mbar_wait_bounded(&pfull[t], uint32_t(i - 1) & 1u, a.status);
+                    if (ok) mbar_arrive(&pfull[t]);
                 }
             }
         }

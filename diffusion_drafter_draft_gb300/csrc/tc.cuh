@@ -16,27 +16,21 @@ namespace tc {
 // K-major operand tile staged with 128-byte swizzle: rows of 64 bf16 (128 B),
 // 8-row groups 1024 B apart; the tile base is 1024-byte aligned. Moving 16
 // elements (32 B) along K adds 2 to the encoded start address.
+constexpr uint64_t DESC_SW128_KMAJOR = (uint64_t(1u) << 16)              // leading byte offset (unused for swizzled K-major)
+                                       | (uint64_t(1024u >> 4) << 32)  // stride byte offset: 8 rows x 128 B
+                                       | (uint64_t(1u) << 46)          // descriptor version
+                                       | (uint64_t(2u) << 61);         // 128-byte swizzle
 __device__ __forceinline__ uint64_t desc_sw128_kmajor(uint32_t smem_addr) {
-    uint64_t d = 0;
-    d |= uint64_t((smem_addr >> 4) & 0x3fffu);         // start address
-    d |= uint64_t(1u) << 16;                            // leading byte offset (unused for swizzled K-major)
-    d |= uint64_t(1024u >> 4) << 32;                    // stride byte offset: 8 rows x 128 B
-    d |= uint64_t(1u) << 46;                            // descriptor version
-    d |= uint64_t(2u) << 61;                            // 128-byte swizzle
-    return d;
+    return DESC_SW128_KMAJOR | uint64_t((smem_addr >> 4) & 0x3fffu);  // start address
 }
 
 // MN-major B operand staged with 128-byte swizzle: K rows of 64 bf16 (128 B) along N,
 // 8-row groups 1024 B apart; `lead` bytes lead to the next 64 of N. Moving 16 rows
 // along K adds 128 to the encoded start address.
-__device__ __forceinline__ uint64_t desc_sw128_mnmajor(uint32_t smem_addr, uint32_t lead) {
-    uint64_t d = 0;
-    d |= uint64_t((smem_addr >> 4) & 0x3fffu);
-    d |= uint64_t((lead >> 4) & 0x3fffu) << 16;         // leading byte offset: the next 64 of N
-    d |= uint64_t(1024u >> 4) << 32;                    // stride byte offset: 8 rows of K
-    d |= uint64_t(1u) << 46;
-    d |= uint64_t(2u) << 61;
-    return d;
+__host__ __device__ constexpr uint64_t desc_sw128_mnmajor_base(uint32_t lead) {  // (start address: low 14 bits)
+    return (uint64_t((lead >> 4) & 0x3fffu) << 16)  // leading byte offset: the next 64 of N
+           | (uint64_t(1024u >> 4) << 32)           // stride byte offset: 8 rows of K
+           | (uint64_t(1u) << 46) | (uint64_t(2u) << 61);
 }
 constexpr uint32_t IDESC_B_MNMAJOR = 1u << 16;          // added to idesc_bf16_f32
 
@@ -97,6 +91,12 @@ __device__ __forceinline__ void mma_bf16(uint32_t tmem_d, uint64_t adesc, uint64
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
         :: "r"(tmem_d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate ? 1u : 0u)
         : "memory");
+}
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(p));
+    return p != 0;
 }
 // Arrive on `bar` once every MMA issued so far by this thread has completed.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
