@@ -313,7 +313,9 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
     } else if (warp == 2) {
         // ---------------------------------------------------------------- landing of the groups' operands
         if (nblk > 0 && lane == 0) {
-            bool ok = true;
+            // (every phase of a stage is waited for, block 0's keys' too: a wait two phases ahead would
+            // take the phase before for its own)
+            bool ok = mbar_wait_bounded(&full[0], 0, a.status);
             for (int i = 0; i < nblk && ok; ++i) {
                 const int vi = 2 * i + 1, ki = 2 * i + 2;
                 const bool last = i + 1 == nblk;
@@ -365,72 +367,54 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
                 if (ok && work) {
                     tc::fence_after_sync();
                     const int key0 = (b0 + i) * PG_BN;
-                    uint32_t s[4][32];
+                    uint32_t s[128];
+                    tc::tmem_ld128(scol, s);
                     const int lim = limit - key0;                // columns from `lim` on are hidden
                     const bool tree = a.mask && key0 + PG_BN > r.n_old;
-                    const bool cut = tree || __any_sync(0xffffffffu, lim < PG_BN);
-                    // 32 scores weighted against the maximum `base`: P to tensor memory (columns 16 w:
-                    // over scores that are in registers), their sum and largest
+                    const bool cut = tree || __any_sync(0xffffffffu, real && lim < PG_BN);
+                    // 32 scores weighted against a maximum (off = -maximum): P to tensor memory over the
+                    // scores, their sum and largest
                     float p[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                     uint64_t ls[4] = {0, 0, 0, 0};
                     const uint64_t sl = pair(x.sl2, x.sl2);
-                    auto weigh = [&](const uint32_t (&v)[32], int w, uint64_t off, bool top) {
+                    auto weigh = [&](int w, uint64_t off, bool top) {
                         uint32_t pk[16];
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
                             if (top)
                                 p[(e >> 1) & 3] =
-                                    max3(p[(e >> 1) & 3], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+                                    max3(p[(e >> 1) & 3], __uint_as_float(s[32 * w + e]),
+                                         __uint_as_float(s[32 * w + e + 1]));
                             float y0, y1;
-                            unpair(fma2(pair(v[e], v[e + 1]), sl, off), y0, y1);
+                            unpair(fma2(pair(s[32 * w + e], s[32 * w + e + 1]), sl, off), y0, y1);
                             const float p0 = ex2(y0), p1 = ex2(y1);
                             ls[(e >> 1) & 3] = add2(ls[(e >> 1) & 3], pair(p0, p1));
                             pk[e / 2] = pack2(p0, p1);
                         }
                         tc::tmem_st16_async(scol + 16u * w, pk);
                     };
-                    bool grow = true;
-                    float mx;
-                    tc::tmem_ld32_async(scol, s[0]);
                     if (i > 0 && !cut) {
-                        // the usual block: weighted as the scores arrive, against the maximum so far
+                        // the usual block: weighted against the maximum so far
                         const float ms = m > -INFINITY ? m : 0.f;
                         const uint64_t off = pair(-ms, -ms);
-                        tc::tmem_wait_ld(s[0]);
-                        tc::tmem_ld32_async(scol + 32u, s[1]);
-                        weigh(s[0], 0, off, true);
-                        tc::tmem_wait_ld(s[1]);
-                        tc::tmem_ld32_async(scol + 64u, s[2]);
-                        weigh(s[1], 1, off, true);
-                        tc::tmem_wait_ld(s[2]);
-                        tc::tmem_ld32_async(scol + 96u, s[3]);
-                        weigh(s[2], 2, off, true);
-                        tc::tmem_wait_ld(s[3]);
-                        weigh(s[3], 3, off, true);
-                        mx = fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])) * x.sl2;   // (sl2 > 0: -inf stays)
-                        grow = mx > m + PG_RESCALE || (m == -INFINITY && mx > -INFINITY);
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) weigh(w, off, true);
                     } else {
-#pragma unroll
-                        for (int w = 1; w < 4; ++w) tc::tmem_ld32_async(scol + 32u * w, s[w]);
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) tc::tmem_wait_ld(s[w]);
                         if (cut) {
 #pragma unroll
                             for (int w = 0; w < 4; ++w) {
                                 const uint32_t bits = tree ? tree_bits(key0 + 32 * w) : 0xffffffffu;
 #pragma unroll
                                 for (int e = 0; e < 32; ++e)
-                                    if (!((bits >> e) & 1u) || 32 * w + e >= lim) s[w][e] = 0xff800000u;  // -inf
+                                    if (!((bits >> e) & 1u) || 32 * w + e >= lim) s[32 * w + e] = 0xff800000u;  // -inf
                             }
                         }
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2)
-#pragma unroll
-                            for (int w = 0; w < 4; ++w)
-                                p[w] = max3(p[w], __uint_as_float(s[w][e]), __uint_as_float(s[w][e + 1]));
-                        mx = fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])) * x.sl2;
-                        grow = mx > m + PG_RESCALE || (m == -INFINITY && mx > -INFINITY);
+                        for (int e = 0; e < 128; e += 2)
+                            p[(e >> 1) & 3] = max3(p[(e >> 1) & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
                     }
+                    const float mx = fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])) * x.sl2;   // (sl2 > 0: -inf stays)
+                    const bool grow = real && (mx > m + PG_RESCALE || (m == -INFINITY && mx > -INFINITY));
                     const bool anew = i == 0 || cut;             // nothing weighted yet
                     if (anew || __any_sync(0xffffffffu, grow)) {
                         const bool resc = grow && m > -INFINITY;
@@ -452,7 +436,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
 #pragma unroll
                         for (int w = 0; w < 4; ++w) ls[w] = 0;
 #pragma unroll
-                        for (int w = 0; w < 4; ++w) weigh(s[w], w, off, false);
+                        for (int w = 0; w < 4; ++w) weigh(w, off, false);
                     }
                     float sum, sum1;
                     unpair(add2(add2(ls[0], ls[1]), add2(ls[2], ls[3])), sum, sum1);
