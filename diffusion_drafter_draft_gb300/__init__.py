@@ -697,7 +697,8 @@ class PagedCache:
     captured into a CUDA graph. read_status(cache.ws) tells what the kernels found wrong
     in lengths and tables. Calls run on `stream` (default: the current stream of the
     pages' device) and outputs they allocate belong to it; the workspace is made on the
-    stream that is current when the object is.
+    stream that is current when the object is. An object is used by one host thread at
+    a time.
     """
 
     def __init__(self, k_pages, v_pages, table, n_ctx, Hq, S, T=None, q_start=None, ws=None):
@@ -733,86 +734,106 @@ class PagedCache:
         else:
             self._need(ws, "ws", torch.uint8)
         self.ws = ws
-        self._wsp = (ctypes.c_void_p(ws.data_ptr()), ws.numel())
+        self._wsp = (ws.data_ptr(), ws.numel())
         self.rows = self.max_pages * self.page
+        L = lib()
+        self._fn = {n: getattr(L, "dartree_paged_" + n) for n in ("append", "attention", "weights", "evict", "commit")}
+        self._pp, self._mp = ctypes.byref(self.p), ctypes.byref(self._m)
+        self._t = Tree()
+        self._tp = ctypes.byref(self._t)
+        self._x = PagedTokens()
+        self._xp = ctypes.byref(self._x)
+        self._shapes = dict(q=torch.Size((self.T, self.Hq, self.D)), k=torch.Size((self.T, self.Hkv, self.D)),
+                            lse=torch.Size((self.T, self.Hq)),
+                            mask=torch.Size((self.C, self.S, self.S)), pos=torch.Size((self.C, self.S)),
+                            C=torch.Size((self.C,)), D=torch.Size((self.D,)),
+                            w=torch.Size((self.C, self.Hkv, self.rows)))
 
     def _need(self, t, name, dtype=None, shape=None) -> int:
+        """Address of a contiguous tensor on the pages' device; raises for any other."""
+        if isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.device == self.device \
+                and t.is_contiguous():
+            return t.data_ptr()
         ptr = _need(t, name, dtype, shape)
         if t.device != self.device:
             raise ValueError(f"{name} must be on {self.device}, got {t.device}")
         return ptr
 
     def _run(self, name, stream, *args):
-        s = stream if stream is not None else torch.cuda.current_stream(self.device)
+        # (the current stream as its handle: a torch.cuda.Stream object costs more than the launch)
+        s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(self.device.index)
         if torch.cuda.current_device() == self.device.index:
-            return _call(name, *args, *self._wsp, ctypes.c_void_p(s.cuda_stream))
-        with torch.cuda.device(self.device):
-            _call(name, *args, *self._wsp, ctypes.c_void_p(s.cuda_stream))
+            rc = self._fn[name](*args, *self._wsp, s)
+        else:
+            with torch.cuda.device(self.device):
+                rc = self._fn[name](*args, *self._wsp, s)
+        if rc != OK:
+            raise DartreeError(rc, "dartree_paged_" + name)
 
     def _new(self, make, shape, dtype, stream):
         """An output tensor that belongs to the stream of the call that fills it."""
-        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(self.device)):
+        if stream is None:
+            return make(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(stream):
             return make(shape, dtype=dtype, device=self.device)
 
-    def _tree(self, tree, *keys):
+    def _tree(self, tree, key):
+        """The tree's n_nodes and its mask or pos, or None."""
         if tree is None:
             return None
-        shapes = dict(mask=(self.C, self.S, self.S), pos=(self.C, self.S), n_nodes=(self.C,))
-        for k in keys:
-            self._need(tree[k], f"tree[{k!r}]", torch.uint8 if k == "mask" else torch.int32, shapes[k])
-        return ctypes.byref(_tree_struct({k: tree[k] for k in keys}))
+        self._t.n_nodes = self._need(tree["n_nodes"], "tree['n_nodes']", torch.int32, self._shapes["C"])
+        setattr(self._t, key, self._need(tree[key], f"tree[{key!r}]", torch.uint8 if key == "mask" else torch.int32,
+                                         self._shapes[key]))
+        return self._tp
 
-    def _heads(self, t, name, heads):
+    def _heads(self, t, name, shape):
         """A [T, heads, D] tensor whose tokens may lie further apart: (address, elements between tokens)."""
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch tensor")
-        if t.device != self.device or t.dtype != self.dtype or tuple(t.shape) != (self.T, heads, self.D):
-            raise ValueError(f"{name} must be {self.dtype} {(self.T, heads, self.D)} on {self.device}, got {t.dtype} "
+        if t.shape != shape or t.dtype is not self.dtype or t.device != self.device:
+            raise ValueError(f"{name} must be {self.dtype} {tuple(shape)} on {self.device}, got {t.dtype} "
                              f"{tuple(t.shape)} on {t.device}")
         ld, h, one = t.stride()
-        if (one != 1 and self.D > 1) or (h != self.D and heads > 1):
+        if one != 1 or (h != self.D and shape[1] > 1):
             raise ValueError(f"{name}: the heads of a token must be contiguous")
-        return t.data_ptr(), (ld if self.T > 1 else heads * self.D)
+        return t.data_ptr(), (ld if self.T > 1 else shape[1] * self.D)
 
     def append(self, q, k, v, q_gain=None, k_gain=None, eps=1e-6, theta=1.0e6, tree=None, pos_base=None, out=None,
                stream=None):
         """Head norms (with gains [D]), rotation and store of the new tokens (dartree_paged_append):
         q [T, Hq, D], k and v [T, Hkv, D], parts of one tensor or not -> rotated queries [T, Hq, D]."""
-        qp, ldq = self._heads(q, "q", self.Hq)
-        kp, ldk = self._heads(k, "k", self.Hkv)
-        vp, ldv = self._heads(v, "v", self.Hkv)
-        gains = [None if g is None else self._need(g, n, self.dtype, (self.D,))
-                 for g, n in ((q_gain, "q_gain"), (k_gain, "k_gain"))]
-        base = None if pos_base is None else self._need(pos_base, "pos_base", torch.int32, (self.C,))
+        sh, x = self._shapes, self._x
+        x.q, x.ldq = self._heads(q, "q", sh["q"])
+        x.k, x.ldk = self._heads(k, "k", sh["k"])
+        x.v, x.ldv = self._heads(v, "v", sh["k"])
+        x.gq = None if q_gain is None else self._need(q_gain, "q_gain", self.dtype, sh["D"])
+        x.gk = None if k_gain is None else self._need(k_gain, "k_gain", self.dtype, sh["D"])
+        x.pos_base = None if pos_base is None else self._need(pos_base, "pos_base", torch.int32, sh["C"])
+        x.eps, x.theta = eps, theta
         if out is None:
-            out = self._new(torch.empty, (self.T, self.Hq, self.D), self.dtype, stream)
-        op = self._need(out, "out", self.dtype, (self.T, self.Hq, self.D))
-        x = PagedTokens(qp, kp, vp, ldq, ldk, ldv, gains[0], gains[1], base, float(eps), float(theta))
-        self._run("dartree_paged_append", stream, ctypes.byref(self.p), ctypes.byref(x), ctypes.byref(self._m),
-                  self._tree(tree, "pos", "n_nodes"), ctypes.c_void_p(op))
+            out = self._new(torch.empty, self._shapes["q"], self.dtype, stream)
+        op = self._need(out, "out", self.dtype, self._shapes["q"])
+        self._run("append", stream, self._pp, self._xp, self._mp, self._tree(tree, "pos"), op)
         return out
 
     def attention(self, q, tree=None, scale=None, out=None, lse=None, stream=None):
         """Attention of the new tokens, already appended, over the pages (dartree_paged_attention):
         q [T, Hq, D] rotated -> out [T, Hq, D]; lse [T, Hq] float32 is filled when given."""
-        qp = self._need(q, "q", self.dtype, (self.T, self.Hq, self.D))
+        qp = self._need(q, "q", self.dtype, self._shapes["q"])
         if out is None:
-            out = self._new(torch.empty, (self.T, self.Hq, self.D), self.dtype, stream)
-        op = self._need(out, "out", self.dtype, (self.T, self.Hq, self.D))
-        lp = None if lse is None else ctypes.c_void_p(self._need(lse, "lse", torch.float32, (self.T, self.Hq)))
-        self._run("dartree_paged_attention", stream, ctypes.byref(self.p), ctypes.c_void_p(qp), ctypes.byref(self._m),
-                  self._tree(tree, "mask", "n_nodes"), float(scale or 0.0), ctypes.c_void_p(op), lp)
+            out = self._new(torch.empty, self._shapes["q"], self.dtype, stream)
+        op = self._need(out, "out", self.dtype, self._shapes["q"])
+        lp = None if lse is None else self._need(lse, "lse", torch.float32, self._shapes["lse"])
+        self._run("attention", stream, self._pp, qp, self._mp, self._tree(tree, "mask"), scale or 0.0, op, lp)
         return out
 
     def weights(self, q, lse, weights, tree=None, scale=None, decay=1.0, stream=None):
         """weights [C, Hkv, max_pages * page] float32 decayed and increased by the attention weight each
         cached row receives from the new tokens (dartree_paged_weights)."""
-        qp = self._need(q, "q", self.dtype, (self.T, self.Hq, self.D))
-        lp = self._need(lse, "lse", torch.float32, (self.T, self.Hq))
-        wp = self._need(weights, "weights", torch.float32, (self.C, self.Hkv, self.rows))
-        self._run("dartree_paged_weights", stream, ctypes.byref(self.p), ctypes.c_void_p(qp), ctypes.c_void_p(lp),
-                  ctypes.byref(self._m), self._tree(tree, "mask", "n_nodes"), float(scale or 0.0), float(decay),
-                  ctypes.c_void_p(wp))
+        qp = self._need(q, "q", self.dtype, self._shapes["q"])
+        lp = self._need(lse, "lse", torch.float32, self._shapes["lse"])
+        wp = self._need(weights, "weights", torch.float32, self._shapes["w"])
+        self._run("weights", stream, self._pp, qp, lp, self._mp, self._tree(tree, "mask"), scale or 0.0, decay, wp)
         return weights
 
     def evict(self, weights, budget, dst_table, sink=0, recent=0, keep=None, n_out=None, weights_out=None,
@@ -821,7 +842,7 @@ class PagedCache:
         head, `budget` in all, copied into the pages of dst_table [C, dst_pages] (dartree_paged_evict) ->
         dict(keep [C, Hkv, budget], n [C], weights [C, Hkv, dst_pages * page])."""
         budget = int(budget)
-        wp = self._need(weights, "weights", torch.float32, (self.C, self.Hkv, self.rows))
+        wp = self._need(weights, "weights", torch.float32, self._shapes["w"])
         if not isinstance(dst_table, torch.Tensor) or dst_table.dim() != 2:
             raise ValueError("dst_table must be [C, dst_pages]")
         pages = dst_table.shape[1]
@@ -837,9 +858,8 @@ class PagedCache:
         n_out = output(n_out, "n_out", torch.int32, (self.C,), torch.empty)
         weights_out = output(weights_out, "weights_out", torch.float32, (self.C, self.Hkv, pages * self.page),
                              torch.zeros)
-        self._run("dartree_paged_evict", stream, ctypes.byref(self.p), ctypes.byref(self._m), ctypes.c_void_p(wp),
-                  budget, int(sink), int(recent), ctypes.c_void_p(dp), pages, ctypes.c_void_p(keep.data_ptr()),
-                  ctypes.c_void_p(n_out.data_ptr()), ctypes.c_void_p(weights_out.data_ptr()))
+        self._run("evict", stream, self._pp, self._mp, wp, budget, int(sink), int(recent), dp, pages, keep.data_ptr(),
+                  n_out.data_ptr(), weights_out.data_ptr())
         return dict(keep=keep, n=n_out, weights=weights_out)
 
     def commit(self, path, accepted_len, n_out=None, stream=None):
@@ -849,10 +869,9 @@ class PagedCache:
             raise ValueError("path must be [C, L]")
         L = path.shape[1]
         pp = self._need(path, "path", torch.int32, (self.C, L))
-        ap = self._need(accepted_len, "accepted_len", torch.int32, (self.C,))
+        ap = self._need(accepted_len, "accepted_len", torch.int32, self._shapes["C"])
         if n_out is None:
             n_out = self._new(torch.empty, (self.C,), torch.int32, stream)
-        np_ = self._need(n_out, "n_out", torch.int32, (self.C,))
-        self._run("dartree_paged_commit", stream, ctypes.byref(self.p), ctypes.byref(self._m), ctypes.c_void_p(pp),
-                  ctypes.c_void_p(ap), int(L), ctypes.c_void_p(np_))
+        self._run("commit", stream, self._pp, self._mp, pp, ap, L,
+                  self._need(n_out, "n_out", torch.int32, self._shapes["C"]))
         return n_out

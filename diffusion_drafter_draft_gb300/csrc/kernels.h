@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <mutex>
 #include <stdint.h>
 
@@ -55,6 +56,19 @@ inline cudaLaunchAttribute pdl_attribute() {
     a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     a.val.programmaticStreamSerializationAllowed = 1;
     return a;
+}
+
+// Dynamic shared memory of a kernel raised to `bytes`, on the first launch on each device
+// (`done`: one bit per device, one word per kernel).
+template <typename K>
+inline bool raise_smem(K* kernel, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return true;
 }
 
 // Rows of a bf16 [V, H] matrix copied, per top-K row r and rank i, to out[r*K + i]

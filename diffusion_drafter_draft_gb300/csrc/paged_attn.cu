@@ -627,8 +627,8 @@ static int launch_attn_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUt
                          cudaStream_t stream) {
     auto kern = paged_attn_kernel<D, NT, ST>;
     const size_t smem = PgSmem<D, NT, ST>::TOTAL;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess)
-        return DARTREE_ECUDA;
+    static std::atomic<uint64_t> raised{0};
+    if (!raise_smem(kern, int(smem), raised)) return DARTREE_ECUDA;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned(x.nchunk) * unsigned(x.a.C) * x.a.Hkv * ((x.tiles + NT - 1) / NT));
     cfg.blockDim = dim3(128 + 128 * NT);

@@ -435,9 +435,8 @@ int launch_paged_evict(const PagedArgs& a, const float* weights, int budget, int
     {
         const int64_t cap = int64_t(a.max_pages) << a.log2_page;
         const int held = int(cap < PS_KEYS ? cap : PS_KEYS);
-        if (cudaFuncSetAttribute(paged_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PS_KEYS * 4) !=
-            cudaSuccess)
-            return DARTREE_ECUDA;
+        static std::atomic<uint64_t> raised{0};
+        if (!raise_smem(paged_select_kernel, PS_KEYS * 4, raised)) return DARTREE_ECUDA;
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3(unsigned(a.C) * a.Hkv);
         cfg.blockDim = dim3(PS_NT);

@@ -309,8 +309,8 @@ template <int D>
 static int launch_weights_t(const CUtensorMap& tq, const CUtensorMap& tk, const PwArgs& x, cudaStream_t stream) {
     auto kern = paged_weights_kernel<D>;
     const size_t smem = PwSmem<D>::TOTAL;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess)
-        return DARTREE_ECUDA;
+    static std::atomic<uint64_t> raised{0};
+    if (!raise_smem(kern, int(smem), raised)) return DARTREE_ECUDA;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned(x.nchunk) * unsigned(x.a.C) * x.a.Hkv);
     cfg.blockDim = dim3(PW_NT);
