@@ -67,40 +67,9 @@ struct PgArgs {
     float2* part_ml;
 };
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// Two fp32 values per instruction (fma, add) and the larger of three.
-__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-    return r;
-}
-__device__ __forceinline__ uint64_t pair(float lo, float hi) { return pair(__float_as_uint(lo), __float_as_uint(hi)); }
-__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
 }
 
 template <int D, int NT, int ST>
@@ -584,19 +553,29 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
 
 // ----------------------------------------------------------------------------- host
 
+// Tiles per CTA and chunks of a tile's key blocks, by the time of a wave of CTAs in block
+// times: two tiles share a block's keys and values and one CTA an SM, two CTAs of one
+// tile read them each (1.15). A CTA's start and end take 2 block times, a partial result
+// and its merging about 3 more (4 of two whole tiles).
 static PgPlan paged_plan(const PagedArgs& a) {
     PgPlan p{};
     const int grp = a.Hq / a.Hkv;
     p.tt = PG_BM / grp;
     p.tiles = (a.S + p.tt - 1) / p.tt;
-    p.nt = p.tiles > 1 ? 2 : 1;
-    const int64_t base = int64_t(a.C) * a.Hkv * ((p.tiles + p.nt - 1) / p.nt);
-    const int64_t slots = int64_t(num_sms()) * (p.nt == 1 ? 2 : 1);
+    const int64_t heads = int64_t(a.C) * a.Hkv;
     const int64_t blocks = (((int64_t(a.max_pages) << a.log2_page)) + PG_BN - 1) / PG_BN;
-    // as many chunks of a tile's key blocks as one wave of CTAs holds
-    int64_t n = base > 0 ? slots / base : 1;
-    if (n > blocks) n = blocks;
-    p.nchunk = n < 1 ? 1 : int(n);
+    p.nt = 1, p.nchunk = 1;
+    double best = 1e300;
+    for (int nt = 1; nt <= (p.tiles > 1 ? 2 : 1) && heads > 0; ++nt) {
+        const int64_t base = heads * ((p.tiles + nt - 1) / nt), slots = int64_t(num_sms()) * (nt == 1 ? 2 : 1);
+        const int64_t most = slots / base > 16 ? slots / base : 16;
+        for (int64_t n = 1; n <= blocks && n <= most; ++n) {
+            const double waves = double((base * n + slots - 1) / slots);
+            const double t = waves * (double((blocks + n - 1) / n) * (nt == 1 ? 1.15 : 1.0) + 2.0) +
+                             (n > 1 ? (p.tiles == 1 ? 3.0 : 3.0 + waves) : 0.0);
+            if (t < best) best = t, p.nt = nt, p.nchunk = int(n);
+        }
+    }
     p.rows = p.tiles > 1 ? PG_BM : a.S * grp;
     if (p.nchunk > 1) {
         auto up = [](size_t b) { return (b + 255) / 256 * 256; };

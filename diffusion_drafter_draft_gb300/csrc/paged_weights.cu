@@ -165,36 +165,41 @@ __global__ void __launch_bounds__(PW_NT, 2)
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issue
-        if (lane == 0 && ntile > 0) {
+        // (warp-uniform values, one elected lane: descriptors stay in uniform registers)
+        const int n_t = __shfl_sync(0xffffffffu, ntile, 0), u0 = __shfl_sync(0xffffffffu, b0, 0),
+                  u1 = __shfl_sync(0xffffffffu, b1, 0);
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        if (n_t > 0 && tc::elect_one()) {
             const uint32_t id = tc::idesc_bf16_f32(PW_BM, (x.tt * x.grp + 15) / 16 * 16);
-            int nk = 0, nq = 0, n = 0;
+            constexpr uint32_t PSTEP = L::PANEL >> 4, TSTEP = L::TILE >> 4;  // descriptor steps (low word)
+            const uint32_t k0 = smem_u32(kring) >> 4, q0 = smem_u32(qring) >> 4;
+            constexpr uint32_t HI = uint32_t(tc::DESC_SW128_KMAJOR >> 32), LO = uint32_t(tc::DESC_SW128_KMAJOR);
+            auto desc = [&](uint32_t at) { return (uint64_t(HI) << 32) | (LO | at); };
+            int ks = 0, qs = 0, n = 0;
+            uint32_t kp = 0, qp = 0;
             bool ok = true;
-            for (int b = b0; b < b1 && ok; ++b, ++nk) {
-                const int ks = nk % ks_n;
-                ok = mbar_wait_bounded(&kfull[ks], uint32_t(nk / ks_n) & 1u, a.status);
-                for (int t = first_tile(b); t < ntile && ok; ++t, ++n) {
-                    const int qs = once ? 0 : nq % qs_n;
-                    ok = mbar_wait_bounded(&qfull[qs], once ? 0u : uint32_t(nq / qs_n) & 1u, a.status);
+            for (int b = u0; b < u1 && ok; ++b) {
+                ok = mbar_wait_bounded(&kfull[ks], kp, a.status);
+                for (int t = first_tile(b); t < n_t && ok; ++t, ++n) {
+                    ok = mbar_wait_bounded(&qfull[qs], qp, a.status);
                     if (ok && n >= 2) ok = mbar_wait_bounded(&sfree[n & 1], uint32_t((n >> 1) - 1) & 1u, a.status);
                     if (!ok) break;
                     tc::fence_after_sync();
-                    const uint32_t ka = smem_u32(kring + ks * L::TILE), qb = smem_u32(qring + qs * L::TILE);
+                    const uint32_t da = k0 + ks * TSTEP, db = q0 + qs * TSTEP;
 #pragma unroll
-                    for (int p = 0; p < L::PANELS; ++p) {
-                        const uint64_t da = tc::desc_sw128_kmajor(ka + uint32_t(p * L::PANEL));
-                        const uint64_t db = tc::desc_sw128_kmajor(qb + uint32_t(p * L::PANEL));
+                    for (int p = 0; p < L::PANELS; ++p)
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            tc::mma_bf16(tmem + uint32_t((n & 1) * 128), da + 2u * kk, db + 2u * kk, id,
-                                         p > 0 || kk > 0);
-                    }
-                    tc::mma_commit(&sfull[n & 1]);
+                            tc::mma_bf16(tm + uint32_t((n & 1) * 128), desc(da + p * PSTEP + 2u * kk),
+                                         desc(db + p * PSTEP + 2u * kk), id, p > 0 || kk > 0);
                     if (!once) {
                         tc::mma_commit(&qempty[qs]);
-                        ++nq;
+                        if (++qs == qs_n) qs = 0, qp ^= 1u;
                     }
-                    if (t + 1 == ntile) tc::mma_commit(&kempty[ks]);
+                    if (t + 1 == n_t) tc::mma_commit(&kempty[ks]);
+                    tc::mma_commit(&sfull[n & 1]);
                 }
+                if (++ks == ks_n) ks = 0, kp ^= 1u;
             }
         }
     } else {
@@ -205,17 +210,12 @@ __global__ void __launch_bounds__(PW_NT, 2)
         float* slse = reinterpret_cast<float*>(smem + L::LSE_OFF) + group * 128;
         float* ssum = reinterpret_cast<float*>(smem + L::SUM_OFF);
         const int kti = key / x.grp, khg = key - kti * x.grp;   // token and head of column `key` of a tile
-        // log2-domain lse of column `key` of tile t; a row that saw nothing adds nothing
+        // minus the lse of column `key` of tile t, in the log2 domain; a row that saw nothing adds nothing
         auto lse_of = [&](int t) -> float {
             const int i = t * x.tt + kti;
-            if (kti >= x.tt || i >= r.n_new) return INFINITY;
+            if (kti >= x.tt || i >= r.n_new) return -INFINITY;
             const float v = x.lse[(size_t(r.q0) + i) * a.Hq + size_t(g) * x.grp + khg];
-            return v > -INFINITY ? v * 1.4426950408889634f : INFINITY;
-        };
-        auto ex2 = [](float v) {
-            float y;
-            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v));
-            return y;
+            return v > -INFINITY ? v * -1.4426950408889634f : -INFINITY;
         };
         float* const wrow = x.weights + size_t(cg) * (size_t(a.max_pages) << a.log2_page);
         int n = 0;
@@ -253,38 +253,39 @@ __global__ void __launch_bounds__(PW_NT, 2)
                     const int t0 = t * x.tt, cols = min(r.n_new - t0, x.tt) * x.grp;   // columns with a token
                     // causal: a new row is seen by the tokens from its own on
                     const int s = j - r.n_old, from = a.mask || s <= t0 ? 0 : (s - t0) * x.grp;
-                    float part[4] = {0.f, 0.f, 0.f, 0.f};
-                    auto add = [&](const uint32_t (&v)[32], int c0) {
-                        const bool whole = c0 + 32 <= cols && from <= c0 && !(a.mask && s >= 0);
-                        if (__all_sync(0xffffffffu, whole)) {
-#pragma unroll
-                            for (int e = 0; e < 32; e += 4) {
-                                const float4 z = *reinterpret_cast<const float4*>(slse + c0 + e);
-                                part[0] += ex2(fmaf(__uint_as_float(v[e]), x.sl2, -z.x));
-                                part[1] += ex2(fmaf(__uint_as_float(v[e + 1]), x.sl2, -z.y));
-                                part[2] += ex2(fmaf(__uint_as_float(v[e + 2]), x.sl2, -z.z));
-                                part[3] += ex2(fmaf(__uint_as_float(v[e + 3]), x.sl2, -z.w));
-                            }
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const int col = c0 + e;
-                                bool seen = col < cols && col >= from;
-                                if (seen && a.mask && s >= 0)
-                                    seen = s < r.n_new &&
-                                           a.mask[(size_t(c) * a.S + t0 + col / x.grp) * a.S + s] != 0;
-                                if (seen) part[e & 3] += ex2(fmaf(__uint_as_float(v[e]), x.sl2, -slse[col]));
-                            }
-                            __syncwarp();
-                        }
-                    };
+                    uint64_t part[2] = {0, 0};
+                    const uint64_t sl = pair(x.sl2, x.sl2);
+                    const bool tree = a.mask && s >= 0;
 #pragma unroll 1
                     for (int c0 = 0; c0 < cols; c0 += 32) {
                         uint32_t v[32];
                         tc::tmem_ld32(trow + uint32_t(c0), v);
-                        add(v, c0);
+                        if (__any_sync(0xffffffffu, c0 + 32 > cols || from > c0 || tree)) {
+                            // hidden columns: a score of -inf (what lies behind the last token may be anything)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const int col = c0 + e;
+                                bool seen = col < cols && col >= from;
+                                if (seen && tree)
+                                    seen = s < r.n_new &&
+                                           a.mask[(size_t(c) * a.S + t0 + col / x.grp) * a.S + s] != 0;
+                                if (!seen) v[e] = 0xff800000u;
+                            }
+                            __syncwarp();
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const ulonglong2 z = *reinterpret_cast<const ulonglong2*>(slse + c0 + e);
+                            float y0, y1, y2, y3;
+                            unpair(fma2(pair(v[e], v[e + 1]), sl, z.x), y0, y1);
+                            unpair(fma2(pair(v[e + 2], v[e + 3]), sl, z.y), y2, y3);
+                            part[0] = add2(part[0], pair(ex2(y0), ex2(y1)));
+                            part[1] = add2(part[1], pair(ex2(y2), ex2(y3)));
+                        }
                     }
-                    sum += (part[0] + part[1]) + (part[2] + part[3]);
+                    float s0, s1;
+                    unpair(add2(part[0], part[1]), s0, s1);
+                    sum += s0 + s1;
                     tc::fence_before_sync();
                 }
                 __syncwarp();
@@ -330,9 +331,15 @@ int launch_paged_weights(const PagedArgs& a, const void* q, const float* lse, fl
     x.tiles = (a.S + x.tt - 1) / x.tt;
     const int64_t heads = int64_t(a.C) * a.Hkv;
     const int64_t blocks = ((int64_t(a.max_pages) << a.log2_page) + PW_BM - 1) / PW_BM;
-    int64_t n = (4 * int64_t(num_sms()) + heads - 1) / heads;
-    if (n > blocks) n = blocks;
-    x.nchunk = n < 1 ? 1 : int(n);
+    // chunks of key blocks: the fewest block times of all waves of CTAs (two an SM), a CTA's start
+    // and end counted as two
+    const int64_t slots = 2 * int64_t(num_sms()), most = slots / heads > 16 ? slots / heads : 16;
+    int64_t best = INT64_MAX;
+    x.nchunk = 1;
+    for (int64_t n = 1; n <= blocks && n <= most; ++n) {
+        const int64_t t = (heads * n + slots - 1) / slots * ((blocks + n - 1) / n + 2);
+        if (t < best) best = t, x.nchunk = int(n);
+    }
     CUtensorMap tq, tk;
     // (a batch without tokens has no queries: its map is never used)
     if (!make_query_map(&tq, a, a.T > 0 ? q : a.k, x.tt) || !make_page_map(&tk, a, a.k)) return DARTREE_ECUDA;
