@@ -151,17 +151,22 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
             const int su = lane % sub, pn = lane / sub;                   // this lane's page and panel
             const bool mine = sub <= 32 && pn < L::PANELS;
             const int32_t* table = a.table + size_t(c) * a.max_pages;
-            auto page_of = [&](int b) -> int {                            // (n_pages: beyond the pool, zeros)
+            // this lane's table entry of block b (looked up two blocks ahead, checked when it is used), and
+            // the page to fetch: n_pages, beyond the pool and so all zeros, past the end and for no page
+            auto entry_of = [&](int b) -> int {
                 const int j = b * PG_BN + su * pr;
-                if (!mine || j >= r.n_keys) return a.n_pages;
-                const int p = table[j >> a.log2_page];
-                if (unsigned(p) < unsigned(a.n_pages)) return p;
-                set_status(a.status, DARTREE_EINTERNAL);
+                return mine && j < r.n_keys ? table[j >> a.log2_page] : a.n_pages;
+            };
+            auto page_of = [&](int e, int b) -> int {
+                if (unsigned(e) < unsigned(a.n_pages)) return e;
+                if (mine && b * PG_BN + su * pr < r.n_keys) set_status(a.status, DARTREE_EINTERNAL);
                 return a.n_pages;
             };
-            int pg = page_of(b0), issued = 0;
+            int e0 = entry_of(b0), e1 = entry_of(b0 + 1), issued = 0;
             for (int i = 0; i < nblk; ++i) {
-                const int next = i + 1 < nblk ? page_of(b0 + i + 1) : 0;
+                const int pg = page_of(e0, b0 + i);
+                e0 = e1;
+                e1 = entry_of(b0 + i + 2);
                 bool ok = true;
                 for (int kv = 0; kv < 2 && ok; ++kv) {
                     const int idx = 2 * i + kv, s = idx % ST;
@@ -178,7 +183,6 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
                     issued = idx + 1;
                 }
                 if (!ok) break;
-                pg = next;
             }
             // the last block's value rows past the end are zeroed once they have landed
             const int have = r.n_keys - (b0 + nblk - 1) * PG_BN, vl = 2 * nblk - 1;
@@ -553,15 +557,17 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
 
 // ----------------------------------------------------------------------------- host
 
-// Tiles per CTA and chunks of a tile's key blocks, by the time of a wave of CTAs in block
-// times: two tiles share a block's keys and values and one CTA an SM, two CTAs of one
-// tile read them each (1.15). A CTA's start and end take 2 block times, a partial result
-// and its merging about 3 more (4 of two whole tiles).
+// Tiles per CTA and chunks of a tile's key blocks: the least of (all CTAs' time / CTAs in
+// flight + one CTA's time), which bounds any order of CTAs of different lengths. In units
+// of a block's time (~1.6 us at D = 128): a block 1 (two tiles, one CTA an SM) or 1.15
+// (two CTAs of one tile, each reading the block), a CTA's start and end 2, a whole tile's
+// partial result 1.5, and merging 2 and its bytes.
 static PgPlan paged_plan(const PagedArgs& a) {
     PgPlan p{};
     const int grp = a.Hq / a.Hkv;
     p.tt = PG_BM / grp;
     p.tiles = (a.S + p.tt - 1) / p.tt;
+    p.rows = p.tiles > 1 ? PG_BM : a.S * grp;
     const int64_t heads = int64_t(a.C) * a.Hkv;
     const int64_t blocks = (((int64_t(a.max_pages) << a.log2_page)) + PG_BN - 1) / PG_BN;
     p.nt = 1, p.nchunk = 1;
@@ -570,13 +576,15 @@ static PgPlan paged_plan(const PagedArgs& a) {
         const int64_t base = heads * ((p.tiles + nt - 1) / nt), slots = int64_t(num_sms()) * (nt == 1 ? 2 : 1);
         const int64_t most = slots / base > 16 ? slots / base : 16;
         for (int64_t n = 1; n <= blocks && n <= most; ++n) {
-            const double waves = double((base * n + slots - 1) / slots);
-            const double t = waves * (double((blocks + n - 1) / n) * (nt == 1 ? 1.15 : 1.0) + 2.0) +
-                             (n > 1 ? (p.tiles == 1 ? 3.0 : 3.0 + waves) : 0.0);
+            double cta = double((blocks + n - 1) / n) * (nt == 1 ? 1.15 : 1.0) + 2.0, merge = 0.0;
+            if (n > 1) {
+                cta += 1.5 * nt * p.rows / PG_BM;
+                merge = 2.0 + double(heads) * p.tiles * double(n) * p.rows * a.D * 4.0 / 1e7;
+            }
+            const double t = double(base * n) * cta / double(slots) + cta + merge;
             if (t < best) best = t, p.nt = nt, p.nchunk = int(n);
         }
     }
-    p.rows = p.tiles > 1 ? PG_BM : a.S * grp;
     if (p.nchunk > 1) {
         auto up = [](size_t b) { return (b + 255) / 256 * 256; };
         const size_t rows = size_t(a.C) * a.Hkv * p.tiles * p.nchunk * p.rows;

@@ -35,11 +35,15 @@ struct PwSmem {
     static constexpr size_t PANEL = size_t(PW_BM) * 128;
     static constexpr size_t TILE = PANELS * PANEL;
     // stages of the two rings: a single query tile stays, and the keys have the longer ring;
-    // otherwise the queries stream past a block of keys. 96 KB: two CTAs per SM
-    static constexpr int SHORT = D == 64 ? 2 : 1, LONG = D == 64 ? 4 : 2;
-    static constexpr int MAXS = 4;                                       // barriers per ring
-    static constexpr size_t LSE_OFF = (SHORT + LONG) * TILE;            // float [2 groups][128]
-    static constexpr size_t SUM_OFF = LSE_OFF + 2 * 128 * 4;            // float [2 blocks][128]
+    // otherwise the queries stream past a block of keys. A tile of at most 16 columns (single
+    // tokens) has a place of its own, and the keys all stages. 100 KB: two CTAs per SM
+    static constexpr int SHORT = D == 64 ? 2 : 1, LONG = D == 64 ? 4 : 2, ALL = SHORT + LONG;
+    static constexpr int FEW = 16;
+    static constexpr size_t FEW_PANEL = FEW * 128;
+    static constexpr int MAXS = ALL;                                     // barriers per ring
+    static constexpr size_t FEW_OFF = ALL * TILE;
+    static constexpr size_t LSE_OFF = FEW_OFF + PANELS * FEW_PANEL;     // float [2 groups][2][128]
+    static constexpr size_t SUM_OFF = LSE_OFF + 4 * 128 * 4;            // float [2 blocks][128]
     static constexpr size_t BAR_OFF = SUM_OFF + 2 * 128 * 4;
     // kfull, kempty, qfull, qempty [MAXS], sfull, sfree [2]
     static constexpr size_t SLOT_OFF = BAR_OFF + 8 * (4 * MAXS + 4);
@@ -103,11 +107,16 @@ __global__ void __launch_bounds__(PW_NT, 2)
     const int b0 = chunk * per, b1 = min(blocks, b0 + per);
     const int ntile = (r.n_new + x.tt - 1) / x.tt;
     const bool once = x.tiles == 1;                       // one query tile: it stays in stage 0
-    const int ks_n = once ? L::LONG : L::SHORT, qs_n = once ? L::SHORT : L::LONG;
+    const bool few = once && x.tt * x.grp <= L::FEW;
+    const int ks_n = few ? L::ALL : once ? L::LONG : L::SHORT, qs_n = few ? 1 : once ? L::SHORT : L::LONG;
     uint8_t* const kring = smem;
-    uint8_t* const qring = smem + ks_n * L::TILE;
+    uint8_t* const qring = few ? smem + L::FEW_OFF : smem + ks_n * L::TILE;
+    const uint32_t qpanel = uint32_t(few ? L::FEW_PANEL : L::PANEL);
     // the first tile that sees a row of block b
-    auto first_tile = [&](int b) -> int { return a.mask ? 0 : max(0, (b * PW_BM - r.n_old) / x.tt); };
+    auto first_tile = [&](int b) -> int {
+        const int ahead = b * PW_BM - r.n_old;
+        return a.mask || ahead <= 0 ? 0 : ahead / x.tt;
+    };
 
     if (warp == 0) {
         // ---------------------------------------------------------------- producer
@@ -116,19 +125,24 @@ __global__ void __launch_bounds__(PW_NT, 2)
             const int su = lane % sub, pn = lane / sub;
             const bool mine = pn < L::PANELS;
             const int32_t* table = a.table + size_t(c) * a.max_pages;
-            auto page_of = [&](int b) -> int {            // (n_pages: beyond the pool, zeros)
+            // this lane's table entry of block b (looked up two blocks ahead, checked when it is used), and
+            // the page to fetch: n_pages, beyond the pool and so all zeros, past the end and for no page
+            auto entry_of = [&](int b) -> int {
                 const int j = b * PW_BM + su * pr;
-                if (!mine || j >= r.n_keys) return a.n_pages;
-                const int p = table[j >> a.log2_page];
-                if (unsigned(p) < unsigned(a.n_pages)) return p;
-                set_status(a.status, DARTREE_EINTERNAL);
+                return mine && j < r.n_keys ? table[j >> a.log2_page] : a.n_pages;
+            };
+            auto page_of = [&](int e, int b) -> int {
+                if (unsigned(e) < unsigned(a.n_pages)) return e;
+                if (mine && b * PW_BM + su * pr < r.n_keys) set_status(a.status, DARTREE_EINTERNAL);
                 return a.n_pages;
             };
             const uint32_t qbytes = uint32_t(L::PANELS * x.tt * x.grp * 128);
-            int pg = page_of(b0), nk = 0, nq = 0;
+            int e0 = entry_of(b0), e1 = entry_of(b0 + 1), nk = 0, nq = 0;
             bool ok = true;
             for (int b = b0; b < b1 && ok; ++b) {
-                const int next = b + 1 < b1 ? page_of(b + 1) : 0;
+                const int pg = page_of(e0, b);
+                e0 = e1;
+                e1 = entry_of(b + 2);
                 if (lane == 0 && nk >= ks_n)
                     ok = mbar_wait_bounded(&kempty[nk % ks_n], uint32_t((nk / ks_n) & 1) ^ 1u, a.status);
                 ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -148,12 +162,11 @@ __global__ void __launch_bounds__(PW_NT, 2)
                         if (!ok) break;
                         mbar_arrive_expect_tx(&qfull[qs], qbytes);
                         for (int p = 0; p < L::PANELS; ++p)
-                            tc::tma_load_3d(qring + qs * L::TILE + p * L::PANEL, &tmQ, 64 * p, g * x.grp,
+                            tc::tma_load_3d(qring + qs * L::TILE + p * qpanel, &tmQ, 64 * p, g * x.grp,
                                             r.q0 + t * x.tt, &qfull[qs]);
                         ++nq;
                     }
                 ok = __shfl_sync(0xffffffffu, ok, 0);
-                pg = next;
             }
             // copies issued and not yet seen complete land before the CTA can exit
             if (lane == 0) {
@@ -172,7 +185,7 @@ __global__ void __launch_bounds__(PW_NT, 2)
         if (n_t > 0 && tc::elect_one()) {
             const uint32_t id = tc::idesc_bf16_f32(PW_BM, (x.tt * x.grp + 15) / 16 * 16);
             constexpr uint32_t PSTEP = L::PANEL >> 4, TSTEP = L::TILE >> 4;  // descriptor steps (low word)
-            const uint32_t k0 = smem_u32(kring) >> 4, q0 = smem_u32(qring) >> 4;
+            const uint32_t k0 = smem_u32(kring) >> 4, q0 = smem_u32(qring) >> 4, qstep = qpanel >> 4;
             constexpr uint32_t HI = uint32_t(tc::DESC_SW128_KMAJOR >> 32), LO = uint32_t(tc::DESC_SW128_KMAJOR);
             auto desc = [&](uint32_t at) { return (uint64_t(HI) << 32) | (LO | at); };
             int ks = 0, qs = 0, n = 0;
@@ -181,7 +194,7 @@ __global__ void __launch_bounds__(PW_NT, 2)
             for (int b = u0; b < u1 && ok; ++b) {
                 ok = mbar_wait_bounded(&kfull[ks], kp, a.status);
                 for (int t = first_tile(b); t < n_t && ok; ++t, ++n) {
-                    ok = mbar_wait_bounded(&qfull[qs], qp, a.status);
+                    if (!once || n == 0) ok = mbar_wait_bounded(&qfull[qs], qp, a.status);
                     if (ok && n >= 2) ok = mbar_wait_bounded(&sfree[n & 1], uint32_t((n >> 1) - 1) & 1u, a.status);
                     if (!ok) break;
                     tc::fence_after_sync();
@@ -191,7 +204,7 @@ __global__ void __launch_bounds__(PW_NT, 2)
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             tc::mma_bf16(tm + uint32_t((n & 1) * 128), desc(da + p * PSTEP + 2u * kk),
-                                         desc(db + p * PSTEP + 2u * kk), id, p > 0 || kk > 0);
+                                         desc(db + p * qstep + 2u * kk), id, p > 0 || kk > 0);
                     if (!once) {
                         tc::mma_commit(&qempty[qs]);
                         if (++qs == qs_n) qs = 0, qp ^= 1u;
@@ -207,18 +220,17 @@ __global__ void __launch_bounds__(PW_NT, 2)
         const int group = (warp - 2) >> 2, quarter = warp & 3;
         const int key = quarter * 32 + lane;
         const uint32_t trow = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(group * 128);
-        float* slse = reinterpret_cast<float*>(smem + L::LSE_OFF) + group * 128;
+        float* slse = reinterpret_cast<float*>(smem + L::LSE_OFF) + group * 256;   // [2][128]
         float* ssum = reinterpret_cast<float*>(smem + L::SUM_OFF);
         const int kti = key / x.grp, khg = key - kti * x.grp;   // token and head of column `key` of a tile
-        // minus the lse of column `key` of tile t, in the log2 domain; a row that saw nothing adds nothing
-        auto lse_of = [&](int t) -> float {
-            const int i = t * x.tt + kti;
-            if (kti >= x.tt || i >= r.n_new) return -INFINITY;
-            const float v = x.lse[(size_t(r.q0) + i) * a.Hq + size_t(g) * x.grp + khg];
-            return v > -INFINITY ? v * -1.4426950408889634f : -INFINITY;
-        };
+        const float* const lrow = x.lse + (size_t(r.q0) + kti) * a.Hq + size_t(g) * x.grp + khg;
+        const size_t lstep = size_t(x.tt) * a.Hq;
+        const int lmax = kti < x.tt ? r.n_new - kti : 0;        // tiles with t * tt below it have a token here
+        // lse of column `key` of tile t (-inf: no token)
+        auto lse_of = [&](int t) -> float { return t * x.tt < lmax ? lrow[t * lstep] : -INFINITY; };
         float* const wrow = x.weights + size_t(cg) * (size_t(a.max_pages) << a.log2_page);
-        int n = 0;
+        const uint64_t sl = pair(x.sl2, x.sl2);
+        int n = 0, buf = 0;
         bool ok = true;
         // this group's next tile's values are fetched while the current one is added up
         int next_t = -1;
@@ -233,18 +245,17 @@ __global__ void __launch_bounds__(PW_NT, 2)
                 if ((n & 1) != group) continue;
                 const float mine = next_t == t ? next_lse : lse_of(t);
                 if (ntile > 1 || next_t != t) {                               // (a lone tile's stay)
-                    asm volatile("bar.sync %0, 128;" :: "r"(2 + group) : "memory");  // the last tile's are read
-                    slse[key] = mine;
+                    buf ^= 1;                                                 // (the last tile's may still be read)
+                    // minus it, in the log2 domain; a row that saw nothing adds nothing
+                    slse[buf * 128 + key] = mine > -INFINITY ? mine * -1.4426950408889634f : -INFINITY;
                     asm volatile("bar.sync %0, 128;" :: "r"(2 + group) : "memory");
                 }
                 next_t = t;
                 next_lse = mine;
                 if (ntile > 1) {
                     next_t = t + 2;
-                    if (next_t >= ntile && b + 1 < b1) {
-                        const int f = first_tile(b + 1);
-                        next_t = f + (((n + ntile - t) & 1) != group ? 1 : 0);
-                    }
+                    if (next_t >= ntile && b + 1 < b1)
+                        next_t = first_tile(b + 1) + (((n + ntile - t) & 1) != group ? 1 : 0);
                     if (next_t < ntile) next_lse = lse_of(next_t);
                 }
                 ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&sfull[group], uint32_t(n >> 1) & 1u, a.status));
@@ -253,38 +264,60 @@ __global__ void __launch_bounds__(PW_NT, 2)
                     const int t0 = t * x.tt, cols = min(r.n_new - t0, x.tt) * x.grp;   // columns with a token
                     // causal: a new row is seen by the tokens from its own on
                     const int s = j - r.n_old, from = a.mask || s <= t0 ? 0 : (s - t0) * x.grp;
-                    uint64_t part[2] = {0, 0};
-                    const uint64_t sl = pair(x.sl2, x.sl2);
-                    const bool tree = a.mask && s >= 0;
-#pragma unroll 1
-                    for (int c0 = 0; c0 < cols; c0 += 32) {
-                        uint32_t v[32];
-                        tc::tmem_ld32(trow + uint32_t(c0), v);
-                        if (__any_sync(0xffffffffu, c0 + 32 > cols || from > c0 || tree)) {
-                            // hidden columns: a score of -inf (what lies behind the last token may be anything)
+                    uint64_t part[4] = {0, 0, 0, 0};
+                    const float* z = slse + buf * 128;
+                    // 2^(s sl2 - lse2) of 16 columns
+                    auto add = [&](const uint32_t* v, int c0) {
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const int col = c0 + e;
-                                bool seen = col < cols && col >= from;
-                                if (seen && tree)
-                                    seen = s < r.n_new &&
-                                           a.mask[(size_t(c) * a.S + t0 + col / x.grp) * a.S + s] != 0;
-                                if (!seen) v[e] = 0xff800000u;
-                            }
-                            __syncwarp();
-                        }
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            const ulonglong2 z = *reinterpret_cast<const ulonglong2*>(slse + c0 + e);
+                        for (int e = 0; e < 16; e += 4) {
+                            const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(z + c0 + e);
                             float y0, y1, y2, y3;
-                            unpair(fma2(pair(v[e], v[e + 1]), sl, z.x), y0, y1);
-                            unpair(fma2(pair(v[e + 2], v[e + 3]), sl, z.y), y2, y3);
-                            part[0] = add2(part[0], pair(ex2(y0), ex2(y1)));
-                            part[1] = add2(part[1], pair(ex2(y2), ex2(y3)));
+                            unpair(fma2(pair(v[e], v[e + 1]), sl, w.x), y0, y1);
+                            unpair(fma2(pair(v[e + 2], v[e + 3]), sl, w.y), y2, y3);
+                            const int k = (e >> 1) & 2;
+                            part[k] = add2(part[k], pair(ex2(y0), ex2(y1)));
+                            part[k + 1] = add2(part[k + 1], pair(ex2(y2), ex2(y3)));
+                        }
+                    };
+                    // hidden columns get a score of -inf (what lies behind the last token may be anything)
+                    if (__all_sync(0xffffffffu, cols == 128 && from <= 0 && !(a.mask && s >= 0))) {
+#pragma unroll
+                        for (int c0 = 0; c0 < 128; c0 += 32) {
+                            uint32_t v[32];
+                            tc::tmem_ld32(trow + uint32_t(c0), v);
+                            add(v, c0);
+                            add(v + 16, c0 + 16);
+                        }
+                    } else if (__all_sync(0xffffffffu, !(a.mask && s >= 0))) {
+#pragma unroll 1
+                        for (int c0 = 0; c0 < cols; c0 += 16) {
+                            uint32_t v[16];
+                            tc::tmem_ld16(trow + uint32_t(c0), v);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                if (c0 + e >= cols || c0 + e < from) v[e] = 0xff800000u;
+                            add(v, c0);
+                        }
+                    } else {
+                        // a tree's rows: token by token (`row`: the mask's byte of this key, if it is a new row's)
+                        const uint8_t* row = a.mask + (size_t(c) * a.S + t0) * a.S + (s >= 0 && s < r.n_new ? s : 0);
+                        int ti = 0, hg = 0;
+#pragma unroll 1
+                        for (int c0 = 0; c0 < cols; c0 += 16) {
+                            uint32_t v[16];
+                            __syncwarp();
+                            tc::tmem_ld16(trow + uint32_t(c0), v);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                const bool seen = c0 + e < cols && (s < 0 || (s < r.n_new && row[size_t(ti) * a.S] != 0));
+                                if (!seen) v[e] = 0xff800000u;
+                                if (++hg == x.grp) hg = 0, ++ti;
+                            }
+                            add(v, c0);
                         }
                     }
                     float s0, s1;
-                    unpair(add2(part[0], part[1]), s0, s1);
+                    unpair(add2(add2(part[0], part[1]), add2(part[2], part[3])), s0, s1);
                     sum += s0 + s1;
                     tc::fence_before_sync();
                 }
@@ -331,13 +364,17 @@ int launch_paged_weights(const PagedArgs& a, const void* q, const float* lse, fl
     x.tiles = (a.S + x.tt - 1) / x.tt;
     const int64_t heads = int64_t(a.C) * a.Hkv;
     const int64_t blocks = ((int64_t(a.max_pages) << a.log2_page) + PW_BM - 1) / PW_BM;
-    // chunks of key blocks: the fewest block times of all waves of CTAs (two an SM), a CTA's start
-    // and end counted as two
-    const int64_t slots = 2 * int64_t(num_sms()), most = slots / heads > 16 ? slots / heads : 16;
-    int64_t best = INT64_MAX;
+    // Chunks of key blocks: the least of (all CTAs' time / CTAs in flight + one CTA's time), which
+    // bounds any order of CTAs of different lengths. One query tile: in block times of reading keys
+    // (two CTAs an SM), a CTA's start and end counted as four; more: in tiles (an SM's CTAs share its
+    // arithmetic), counted as six.
+    const int64_t sms = num_sms(), most = 4 * sms / heads > 64 ? 4 * sms / heads : 64;
+    double best = 1e300;
     x.nchunk = 1;
     for (int64_t n = 1; n <= blocks && n <= most; ++n) {
-        const int64_t t = (heads * n + slots - 1) / slots * ((blocks + n - 1) / n + 2);
+        const int64_t per = (blocks + n - 1) / n;
+        const double cta = x.tiles == 1 ? double(per + 4) : double(per * x.tiles + 6);
+        const double t = double(heads * n) * cta / double(x.tiles == 1 ? 2 * sms : sms) + cta;
         if (t < best) best = t, x.nchunk = int(n);
     }
     CUtensorMap tq, tk;
