@@ -17,8 +17,9 @@
 //               its pages: nothing is transposed)
 //   warp 2      passes on the landing of a group's keys and values
 //   warps 4..   softmax, one thread per row: the row's 128 scores in registers, P in bf16
-//               back to tensor memory; O is rescaled only when the maximum grows by more
-//               than 2^8
+//               back to tensor memory, weighted against the maximum of the blocks before:
+//               bf16 and fp32 carry 2^14 as well as 1, so only a block whose weights add up
+//               to more (and the first, and masked ones) takes its own and rescales O
 // With NT = 2 the tensor cores work on one tile while the other tile's softmax runs.
 // Rows of a partly used page may hold anything: the last block's value rows past the end
 // are zeroed in shared memory (0 * NaN is NaN), its scores are masked.
@@ -36,7 +37,7 @@ namespace dartree {
 
 constexpr int PG_BM = 128;            // rows of a tile
 constexpr int PG_BN = 128;            // keys of a block
-constexpr float PG_RESCALE = 8.0f;    // log2 growth of the maximum that forces a rescale
+constexpr float PG_MOST = 16384.0f;    // sum of a block's weights from which a new maximum is taken
 constexpr float LOG2E = 1.4426950408889634f;
 
 template <int D, int NT, int ST>
@@ -345,52 +346,52 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
                     const int lim = limit - key0;                // columns from `lim` on are hidden
                     const bool tree = a.mask && key0 + PG_BN > r.n_old;
                     const bool cut = tree || __any_sync(0xffffffffu, real && lim < PG_BN);
-                    // 32 scores weighted against a maximum (off = -maximum): P to tensor memory over the
-                    // scores, their sum and largest
-                    float p[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    uint64_t ls[4] = {0, 0, 0, 0};
+                    // 32 scores weighted against the maximum in use: P to tensor memory over the scores,
+                    // and their sum
+                    uint64_t ls[4];
                     const uint64_t sl = pair(x.sl2, x.sl2);
-                    auto weigh = [&](int w, uint64_t off, bool top) {
+                    auto weigh = [&](int w, uint64_t off) {
                         uint32_t pk[16];
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
-                            if (top)
-                                p[(e >> 1) & 3] =
-                                    max3(p[(e >> 1) & 3], __uint_as_float(s[32 * w + e]),
-                                         __uint_as_float(s[32 * w + e + 1]));
                             float y0, y1;
                             unpair(fma2(pair(s[32 * w + e], s[32 * w + e + 1]), sl, off), y0, y1);
                             const float p0 = ex2(y0), p1 = ex2(y1);
-                            ls[(e >> 1) & 3] = add2(ls[(e >> 1) & 3], pair(p0, p1));
+                            ls[(e >> 1) & 3] = w == 0 && e < 8 ? pair(p0, p1) : add2(ls[(e >> 1) & 3], pair(p0, p1));
                             pk[e / 2] = pack2(p0, p1);
                         }
                         tc::tmem_st16_async(scol + 16u * w, pk);
                     };
+                    auto weigh_all = [&]() -> float {
+                        const float ms = m > -INFINITY ? -m : 0.f;   // (a row that has seen nothing: 2^-inf = 0)
+                        const uint64_t off = pair(ms, ms);
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) weigh(w, off);
+                        float s0, s1;
+                        unpair(add2(add2(ls[0], ls[1]), add2(ls[2], ls[3])), s0, s1);
+                        return s0 + s1;
+                    };
+                    float sum = 0.f;
+                    bool anew = true;                            // a maximum of this block's is wanted
                     if (i > 0 && !cut) {
-                        // the usual block: weighted against the maximum so far
-                        const float ms = m > -INFINITY ? m : 0.f;
-                        const uint64_t off = pair(-ms, -ms);
+                        sum = weigh_all();
+                        anew = __any_sync(0xffffffffu, real && !(sum <= PG_MOST && m > -INFINITY));
+                    } else if (cut) {
 #pragma unroll
-                        for (int w = 0; w < 4; ++w) weigh(w, off, true);
-                    } else {
-                        if (cut) {
+                        for (int w = 0; w < 4; ++w) {
+                            const uint32_t bits = tree ? tree_bits(key0 + 32 * w) : 0xffffffffu;
 #pragma unroll
-                            for (int w = 0; w < 4; ++w) {
-                                const uint32_t bits = tree ? tree_bits(key0 + 32 * w) : 0xffffffffu;
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    if (!((bits >> e) & 1u) || 32 * w + e >= lim) s[32 * w + e] = 0xff800000u;  // -inf
-                            }
+                            for (int e = 0; e < 32; ++e)
+                                if (!((bits >> e) & 1u) || 32 * w + e >= lim) s[32 * w + e] = 0xff800000u;  // -inf
                         }
+                    }
+                    if (anew) {
+                        float p[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                         for (int e = 0; e < 128; e += 2)
                             p[(e >> 1) & 3] = max3(p[(e >> 1) & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-                    }
-                    const float mx = fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])) * x.sl2;   // (sl2 > 0: -inf stays)
-                    const bool grow = real && (mx > m + PG_RESCALE || (m == -INFINITY && mx > -INFINITY));
-                    const bool anew = i == 0 || cut;             // nothing weighted yet
-                    if (anew || __any_sync(0xffffffffu, grow)) {
-                        const bool resc = grow && m > -INFINITY;
+                        const float mx = fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])) * x.sl2;   // (sl2 > 0: -inf stays)
+                        const bool grow = real && mx > m, resc = grow && m > -INFINITY;
                         if (__any_sync(0xffffffffu, resc)) {     // O's products up to block i - 1 are done
                             const float f = resc ? ex2(m - mx) : 1.0f;
 #pragma unroll 1
@@ -404,16 +405,8 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
                             l *= f;
                         }
                         if (grow) m = mx;
-                        const float ms = m > -INFINITY ? m : 0.f;    // (a row that has seen nothing: 2^-inf = 0)
-                        const uint64_t off = pair(-ms, -ms);
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) ls[w] = 0;
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) weigh(w, off, false);
+                        sum = weigh_all();
                     }
-                    float sum, sum1;
-                    unpair(add2(add2(ls[0], ls[1]), add2(ls[2], ls[3])), sum, sum1);
-                    sum += sum1;
                     l += sum;
                     tc::tmem_wait_st();
                     tc::fence_before_sync();
