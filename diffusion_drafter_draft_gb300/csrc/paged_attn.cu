@@ -47,8 +47,8 @@ struct PgSmem {
     static constexpr size_t TILE = PANELS * PANEL;              // a query tile, or a block's keys or values
     static constexpr size_t RING_OFF = NT * TILE;
     static constexpr size_t BAR_OFF = RING_OFF + ST * TILE;
-    // qfull, vclean, full[ST], empty[ST], sfull[NT], pfull[NT], ofull[NT]
-    static constexpr size_t SLOT_OFF = BAR_OFF + 8 * (2 + 2 * ST + 3 * NT);
+    // qfull, vclean, full[ST], empty[ST], sfull[NT], pfull[NT], phalf[NT], pdone[NT], ofull[NT]
+    static constexpr size_t SLOT_OFF = BAR_OFF + 8 * (2 + 2 * ST + 5 * NT);
     static constexpr size_t TOTAL = SLOT_OFF + 16 + 1024;       // (+ alignment of the base to 1024)
     static_assert(TOTAL <= 227 * 1024, "tiles and ring fit in shared memory");
 };
@@ -88,8 +88,10 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
     uint64_t* full = qfull + 2;       // [ST] stage landed
     uint64_t* empty = full + ST;      // [ST] the MMAs that read it are done
     uint64_t* sfull = empty + ST;     // [NT] scores written (and every earlier MMA done)
-    uint64_t* pfull = sfull + NT;     // [NT] P written
-    uint64_t* ofull = pfull + NT;     // [NT] the last product with V done
+    uint64_t* phalf = sfull + NT;     // [NT] P of the block's first 64 keys written, what the group reads landed
+    uint64_t* pfull = phalf + NT;     // [NT] P of the others written
+    uint64_t* pdone = pfull + NT;     // [NT] the product of the first 64 keys done
+    uint64_t* ofull = pdone + NT;     // [NT] the last product with V done
     uint32_t* slot = reinterpret_cast<uint32_t*>(smem + L::SLOT_OFF);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -102,7 +104,9 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
         }
         for (int t = 0; t < NT; ++t) {
             mbar_init(&sfull[t], 1);
-            mbar_init(&pfull[t], 5);  // four softmax warps and warp 2
+            mbar_init(&phalf[t], 5);  // four softmax warps and warp 2
+            mbar_init(&pfull[t], 4);
+            mbar_init(&pdone[t], 1);
             mbar_init(&ofull[t], 1);
         }
         fence_mbar_init();
@@ -213,8 +217,9 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
         // ---------------------------------------------------------------- MMA issue
         // The tensor cores take MMAs about as fast as one thread issues them, and a barrier
         // test costs that thread a few hundred cycles beside two softmax warps: so a group
-        // (O += P V of a tile, then its next S) waits for one barrier, pfull, which also
-        // counts the landing of what the group reads (warp 2), and the next group's is
+        // (O += P V of a tile in two halves of the keys, the first while the other's weights
+        // are formed, then the tile's next S) waits for the two halves of P alone; the first
+        // also counts the landing of what the group reads (warp 2), and the next group's is
         // tested while this group's last MMAs are issued.
         // (warp-uniform values, one elected lane: descriptors stay in uniform registers)
         const int nb = __shfl_sync(0xffffffffu, nblk, 0), na = __shfl_sync(0xffffffffu, nact, 0);
@@ -255,15 +260,23 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     if (t >= na) break;
-                    if (!ready) ok = mbar_wait_bounded(&pfull[t], uint32_t(i) & 1u, a.status);
+                    const uint32_t db = r0 + vs * TSTEP;
+                    auto product = [&](int h) {       // 64 keys
+#pragma unroll
+                        for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+                            tc::mma_bf16_ts(tm + OCOL + uint32_t(t * D), tm + uint32_t(t * PG_BN + 8 * kk),
+                                            (VD & ~0xffffffffull) | (uint32_t(VD) | (db + 128u * kk)), idO,
+                                            i > 0 || kk > 0);
+                    };
+                    if (!ready) ok = mbar_wait_bounded(&phalf[t], uint32_t(i) & 1u, a.status);
                     if (!ok) break;
                     tc::fence_after_sync();
-                    const uint32_t db = r0 + vs * TSTEP;
-#pragma unroll
-                    for (int kk = 0; kk < PG_BN / 16; ++kk)
-                        tc::mma_bf16_ts(tm + OCOL + uint32_t(t * D), tm + uint32_t(t * PG_BN + 8 * kk),
-                                        (VD & ~0xffffffffull) | (uint32_t(VD) | (db + 128u * kk)), idO,
-                                        i > 0 || kk > 0);
+                    product(0);
+                    tc::mma_commit(&pdone[t]);
+                    ok = mbar_wait_bounded(&pfull[t], uint32_t(i) & 1u, a.status);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    product(1);
                     const bool end_v = t == na - 1;
                     if (end_v && back_v) tc::mma_commit(&empty[vs]);
                     if (last) {
@@ -272,7 +285,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
                     } else {
 #pragma unroll
                         for (int p = 0; p + 1 < L::PANELS; ++p) score(t, ks, p);
-                        ready = mbar_try_wait(end_v ? &pfull[0] : &pfull[NT - 1], uint32_t(end_v ? i + 1 : i) & 1u);
+                        ready = mbar_try_wait(end_v ? &phalf[0] : &phalf[NT - 1], uint32_t(end_v ? i + 1 : i) & 1u);
                         score(t, ks, L::PANELS - 1);
                         tc::mma_commit(&sfull[t]);
                         if (end_v && back_k) tc::mma_commit(&empty[ks]);
@@ -297,8 +310,8 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
                      (last || mbar_wait_bounded(&full[ki % ST], uint32_t(ki / ST) & 1u, a.status));
                 if (ok && last && r.n_keys < (b0 + nblk) * PG_BN) ok = mbar_wait_bounded(vclean, 0, a.status);
                 for (int t = 0; t < nact && ok; ++t) {
-                    if (i > 0) ok = mbar_wait_bounded(&pfull[t], uint32_t(i - 1) & 1u, a.status);
-                    if (ok) mbar_arrive(&pfull[t]);
+                    if (i > 0) ok = mbar_wait_bounded(&phalf[t], uint32_t(i - 1) & 1u, a.status);
+                    if (ok) mbar_arrive(&phalf[t]);
                 }
             }
         }
@@ -346,10 +359,10 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
                     const int lim = limit - key0;                // columns from `lim` on are hidden
                     const bool tree = a.mask && key0 + PG_BN > r.n_old;
                     const bool cut = tree || __any_sync(0xffffffffu, real && lim < PG_BN);
-                    // 32 scores weighted against the maximum in use: P to tensor memory over the scores,
-                    // and their sum
-                    uint64_t ls[4];
+                    // 32 scores weighted against the maximum in use: P to tensor memory over the scores;
+                    // sums of a half
                     const uint64_t sl = pair(x.sl2, x.sl2);
+                    uint64_t ls[4];
                     auto weigh = [&](int w, uint64_t off) {
                         uint32_t pk[16];
 #pragma unroll
@@ -357,42 +370,42 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
                             float y0, y1;
                             unpair(fma2(pair(s[32 * w + e], s[32 * w + e + 1]), sl, off), y0, y1);
                             const float p0 = ex2(y0), p1 = ex2(y1);
-                            ls[(e >> 1) & 3] = w == 0 && e < 8 ? pair(p0, p1) : add2(ls[(e >> 1) & 3], pair(p0, p1));
+                            const bool first = w % 2 == 0 && e < 8;
+                            ls[(e >> 1) & 3] = first ? pair(p0, p1) : add2(ls[(e >> 1) & 3], pair(p0, p1));
                             pk[e / 2] = pack2(p0, p1);
                         }
                         tc::tmem_st16_async(scol + 16u * w, pk);
                     };
-                    auto weigh_all = [&]() -> float {
+                    auto weigh_half = [&](int h) -> float {          // 64 keys
                         const float ms = m > -INFINITY ? -m : 0.f;   // (a row that has seen nothing: 2^-inf = 0)
                         const uint64_t off = pair(ms, ms);
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) weigh(w, off);
+                        weigh(2 * h, off);
+                        weigh(2 * h + 1, off);
                         float s0, s1;
                         unpair(add2(add2(ls[0], ls[1]), add2(ls[2], ls[3])), s0, s1);
                         return s0 + s1;
                     };
-                    float sum = 0.f;
-                    bool anew = true;                            // a maximum of this block's is wanted
-                    if (i > 0 && !cut) {
-                        sum = weigh_all();
-                        anew = __any_sync(0xffffffffu, real && !(sum <= PG_MOST && m > -INFINITY));
-                    } else if (cut) {
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            const uint32_t bits = tree ? tree_bits(key0 + 32 * w) : 0xffffffffu;
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!((bits >> e) & 1u) || 32 * w + e >= lim) s[32 * w + e] = 0xff800000u;  // -inf
-                        }
-                    }
-                    if (anew) {
+                    auto hand_over = [&](uint64_t* bar) {
+                        tc::tmem_wait_st();
+                        tc::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar);
+                    };
+                    // whether a half's weights are too large, in any row (or there is no maximum yet)
+                    auto too_large = [&](float v) -> bool {
+                        return __any_sync(0xffffffffu, real && !(v <= PG_MOST && m > -INFINITY));
+                    };
+                    // takes the maximum of the scores from `e0` on and rescales what was added up so far
+                    auto own_maximum = [&](int e0) {
                         float p[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                         for (int e = 0; e < 128; e += 2)
-                            p[(e >> 1) & 3] = max3(p[(e >> 1) & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                            if (e >= e0)
+                                p[(e >> 1) & 3] =
+                                    max3(p[(e >> 1) & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
                         const float mx = fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])) * x.sl2;   // (sl2 > 0: -inf stays)
                         const bool grow = real && mx > m, resc = grow && m > -INFINITY;
-                        if (__any_sync(0xffffffffu, resc)) {     // O's products up to block i - 1 are done
+                        if (__any_sync(0xffffffffu, resc)) {
                             const float f = resc ? ex2(m - mx) : 1.0f;
 #pragma unroll 1
                             for (int c0 = 0; c0 < D; c0 += 32) {
@@ -405,11 +418,41 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
                             l *= f;
                         }
                         if (grow) m = mx;
-                        sum = weigh_all();
+                    };
+                    bool first = false;                          // the first half is handed over
+                    if (i > 0 && !cut) {
+                        const float sum = weigh_half(0);
+                        if (!too_large(sum)) {
+                            l += sum;
+                            hand_over(&phalf[t]);
+                            first = true;
+                        }
+                    } else if (cut) {
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            const uint32_t bits = tree ? tree_bits(key0 + 32 * w) : 0xffffffffu;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!((bits >> e) & 1u) || 32 * w + e >= lim) s[32 * w + e] = 0xff800000u;  // -inf
+                        }
+                    }
+                    if (!first) {                                // O's products up to block i - 1 are done
+                        own_maximum(0);
+                        l += weigh_half(0);
+                        hand_over(&phalf[t]);
+                    }
+                    float sum = weigh_half(1);
+                    if (first && too_large(sum)) {               // O's product of the first half has to be, too
+                        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&pdone[t], uint32_t(i) & 1u, a.status));
+                        tc::fence_after_sync();
+                        own_maximum(64);
+                        sum = weigh_half(1);
                     }
                     l += sum;
                     tc::tmem_wait_st();
                     tc::fence_before_sync();
+                } else if (ok) {
+                    if (lane == 0) mbar_arrive(&phalf[t]);
                 }
                 __syncwarp();
                 if (lane == 0 && ok) mbar_arrive(&pfull[t]);

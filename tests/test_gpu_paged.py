@@ -242,6 +242,22 @@ def test_attention_running_maximum_that_keeps_growing(dd):
     _check_attention(x, out, lse)
 
 
+@pytest.mark.parametrize("at", [0, 63, 64, 127, 128, 190, 255, 300, 511])
+def test_attention_a_key_far_above_the_others(dd, at):
+    """One key's score lies a hundred powers of two above what came before it, at the ends of a block's
+    halves and inside them; a second one as far above the first."""
+    x = Case(dd, [1, 70], [600, 530], Hq=8, Hkv=2, page=64, seed=at).fill()
+    x.q.copy_((x.q.float() * 0.1 + 1).to(torch.bfloat16))
+    for c in range(2):
+        for j, v in ((at, 7.0), (min(at + 97, 599 - 70 * c), 14.0)):
+            p, r = op.place(x.np_table, c, [j], x.page)
+            x.k[int(p[0]), :, int(r[0])] = v
+    lse = torch.empty(x.T, x.Hq, device="cuda")
+    out = x.cache.attention(x.q, lse=lse)
+    x.ok()
+    _check_attention(x, out, lse)
+
+
 # ------------------------------------------------------------------------------ append
 
 APPEND = [
