@@ -332,32 +332,47 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
         const uint32_t scol = trow + uint32_t(t * PG_BN), ocol = trow + OCOL + uint32_t(t * D);
         float m = -INFINITY, l = 0.f;
         bool ok = true;
-        // the tree's mask for 32 keys from `key` on: the rows of this warp's tokens, lane q reading
-        // a token's slot q, and the vote is the word
-        auto tree_bits = [&](int key) -> uint32_t {
+        // the tree's mask for the 128 keys from `key` on: lane q reads slot q of a 32-key word of a token
+        // of this warp's, and the vote is the word (eight tokens' four words are loaded together)
+        auto tree_bits = [&](int key, uint32_t (&bits)[4]) {
             const int tok0 = (quarter * 32) / x.grp, tok1 = (quarter * 32 + 31) / x.grp;
             const int sl = key + lane - r.n_old;
-            uint32_t bits = 0;
-            for (int q = tok0; q <= tok1; ++q) {
-                const int i_q = t0 + t * x.tt + q;
-                bool v = sl < 0;
-                if (sl >= 0 && sl < r.n_new && q < x.tt && i_q < r.n_new)
-                    v = a.mask[(size_t(c) * a.S + i_q) * a.S + sl] != 0;
-                const uint32_t word = __ballot_sync(0xffffffffu, v);
-                if (q == ti) bits = word;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) bits[w] = 0;
+            for (int q0 = tok0; q0 <= tok1; q0 += 8) {
+                bool v[8][4];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const int q = q0 + u, i_q = t0 + t * x.tt + q;
+                    const uint8_t* mrow = a.mask + (size_t(c) * a.S + i_q) * a.S;
+                    const bool tok = q <= tok1 && q < x.tt && i_q < r.n_new;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const int j = sl + 32 * w;
+                        v[u][w] = j < 0 || (tok && j < r.n_new && mrow[j] != 0);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t word = __ballot_sync(0xffffffffu, v[u][w]);
+                        if (q0 + u == ti) bits[w] = word;
+                    }
             }
-            return bits;
         };
         if (t < nact) {
             for (int i = 0; i < nblk; ++i) {
+                const int key0 = (b0 + i) * PG_BN;
+                const bool tree = a.mask && key0 + PG_BN > r.n_old;
+                uint32_t bits[4];
+                if (tree && work) tree_bits(key0, bits);
                 ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&sfull[t], uint32_t(i) & 1u, a.status));
                 if (ok && work) {
                     tc::fence_after_sync();
-                    const int key0 = (b0 + i) * PG_BN;
                     uint32_t s[128];
                     tc::tmem_ld128(scol, s);
                     const int lim = limit - key0;                // columns from `lim` on are hidden
-                    const bool tree = a.mask && key0 + PG_BN > r.n_old;
                     const bool cut = tree || __any_sync(0xffffffffu, real && lim < PG_BN);
                     // 32 scores weighted against the maximum in use: P to tensor memory over the scores;
                     // sums of a half
@@ -430,10 +445,10 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
                     } else if (cut) {
 #pragma unroll
                         for (int w = 0; w < 4; ++w) {
-                            const uint32_t bits = tree ? tree_bits(key0 + 32 * w) : 0xffffffffu;
+                            const uint32_t seen = tree ? bits[w] : 0xffffffffu;
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
-                                if (!((bits >> e) & 1u) || 32 * w + e >= lim) s[32 * w + e] = 0xff800000u;  // -inf
+                                if (!((seen >> e) & 1u) || 32 * w + e >= lim) s[32 * w + e] = 0xff800000u;  // -inf
                         }
                     }
                     if (!first) {                                // O's products up to block i - 1 are done
