@@ -146,6 +146,13 @@ __device__ __forceinline__ uint32_t ld_dsmem_u32(uint32_t addr) {
 __device__ __forceinline__ uint64_t ld_dsmem_u64(uint32_t addr) {
     uint64_t v; asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory"); return v;
 }
+__device__ __forceinline__ void ld_dsmem_f32x2(uint32_t addr, float& a, float& b) {
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(a), "=f"(b) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ld_dsmem_f32x4(uint32_t addr, float& a, float& b, float& c, float& d) {
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(a), "=f"(b), "=f"(c), "=f"(d) : "r"(addr) : "memory");
+}
 __device__ __forceinline__ void st_dsmem_u64(uint32_t addr, uint64_t v) {
     asm volatile("st.shared::cluster.u64 [%0], %1;" :: "r"(addr), "l"(v) : "memory");
 }

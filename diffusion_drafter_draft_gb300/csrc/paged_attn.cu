@@ -24,7 +24,8 @@
 // Rows of a partly used page may hold anything: the last block's value rows past the end
 // are zeroed in shared memory (0 * NaN is NaN), its scores are masked.
 //
-// A second launch (several chunks only) merges the chunks' partial rows.
+// Up to eight chunks of a tile may be a cluster (CL) and merge through shared memory; else
+// their partial rows go through memory to a second launch.
 // Every mbarrier wait is bounded; one that runs out records DARTREE_ETIMEOUT.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -51,10 +52,18 @@ struct PgSmem {
     static constexpr size_t SLOT_OFF = BAR_OFF + 8 * (2 + 2 * ST + 5 * NT);
     static constexpr size_t TOTAL = SLOT_OFF + 16 + 1024;       // (+ alignment of the base to 1024)
     static_assert(TOTAL <= 227 * 1024, "tiles and ring fit in shared memory");
+    // merge of a cluster's chunks, over tiles and ring: O of each row in fp32 (a row's 16 extra bytes
+    // keep the rows of a warp in different banks), then (maximum, sum)
+    static constexpr int PITCH = D + 4;
+    static constexpr size_t ML_OFF = size_t(NT) * PG_BM * PITCH * 4;
+    static_assert(ML_OFF + NT * PG_BM * 8 <= BAR_OFF, "merge fits in the tiles' place");
 };
+
+constexpr int PG_CLUSTER = 8;         // chunks that merge through shared memory
 
 struct PgPlan {
     int tt, tiles, nt, nchunk, rows;  // tokens per tile, tiles, tiles per CTA, chunks, rows kept per partial tile
+    bool cluster;                     // the chunks merge through shared memory
     size_t part_o, part_ml, total;    // workspace (partials): offsets and bytes
 };
 
@@ -73,7 +82,7 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <int D, int NT, int ST>
+template <int D, int NT, int ST, bool CL>
 __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PgArgs x) {
@@ -228,7 +237,8 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
             constexpr uint32_t idS = tc::idesc_bf16_f32(PG_BM, PG_BN);
             constexpr uint32_t idO = tc::idesc_bf16_f32(PG_BM, D) | tc::IDESC_B_MNMAJOR;
             constexpr uint32_t PSTEP = L::PANEL >> 4, TSTEP = L::TILE >> 4;  // descriptor steps (low word)
-            const uint32_t q0 = smem_u32(smem) >> 4, r0 = smem_u32(smem + L::RING_OFF) >> 4;
+            // (14 bits: in a cluster the address carries the rank of the CTA above them)
+            const uint32_t q0 = (smem_u32(smem) >> 4) & 0x3fffu, r0 = (smem_u32(smem + L::RING_OFF) >> 4) & 0x3fffu;
             constexpr uint32_t KHI = uint32_t(tc::DESC_SW128_KMAJOR >> 32), KLO = uint32_t(tc::DESC_SW128_KMAJOR);
             constexpr uint64_t VD = tc::desc_sw128_mnmajor_base(uint32_t(L::PANEL));
             auto kdesc = [&](uint32_t at) { return (uint64_t(KHI) << 32) | (KLO | at); };
@@ -315,6 +325,11 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
                 }
             }
         }
+    }
+    if constexpr (CL) {                            // (the softmax warps merge between these)
+        __syncwarp();
+        cluster_sync();
+        cluster_sync();
     }
     } else {
         // ---------------------------------------------------------------- softmax
@@ -480,7 +495,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
         const bool has = ok && t < nact && nblk > 0 && real && l > 0.f;
         const bool load = ok && t < nact && nblk > 0 && work;    // (TMEM loads are warp-wide)
         const size_t orow = (size_t(r.q0) + i_tok) * a.Hq + size_t(g) * x.grp + hg;
-        if (x.nchunk == 1) {
+        if (!CL && x.nchunk == 1) {
             // tree slots without a node get zeros; rows of ragged batches only their own tokens
             const bool write = real || (slot_ok && !a.q_start);
             const float inv = has ? 1.0f / l : 0.f;
@@ -503,25 +518,87 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
                     }
             }
             if (x.lse && write) x.lse[orow] = has ? (m + log2f(l)) * 0.6931471805599453f : real ? -INFINITY : 0.f;
-        } else if (slot_ok) {
-            const size_t pr = ((size_t(cg) * x.tiles + tp * NT + t) * x.nchunk + chunk) * x.rows + row;
-            if (real) x.part_ml[pr] = has ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
-        }
-        if (x.nchunk > 1 && load) {
-            const size_t pr = ((size_t(cg) * x.tiles + tp * NT + t) * x.nchunk + chunk) * x.rows + row;
-            float4* dst = reinterpret_cast<float4*>(x.part_o + pr * D);
+        } else if constexpr (CL) {
+            // the chunks of a tile are a cluster: every CTA puts its rows' O, maximum and sum into its
+            // shared memory and merges every nchunk-th row from all of them
+            float* const ob = reinterpret_cast<float*>(smem);
+            float2* const ml = reinterpret_cast<float2*>(smem + L::ML_OFF);
+            // (over the tiles' place: once the last MMA of the CTA is done, the other tile's too)
+            if (nblk > 0) mbar_wait_bounded(&ofull[nact - 1], 0, a.status);
+            __syncwarp();
+            const int rr = t * PG_BM + row;
+            ml[rr] = has ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
+            if (load)
 #pragma unroll 1
-            for (int c0 = 0; c0 < D; c0 += 32) {
-                uint32_t o[32];
-                __syncwarp();
-                tc::tmem_ld32(ocol + uint32_t(c0), o);
-                if (has)
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    uint32_t o[32];
+                    __syncwarp();
+                    tc::tmem_ld32(ocol + uint32_t(c0), o);
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
-                        dst[c0 / 4 + q] =
-                            make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]),
-                                        __uint_as_float(o[4 * q + 2]), __uint_as_float(o[4 * q + 3]));
+                        reinterpret_cast<uint4*>(ob + rr * L::PITCH + c0)[q] =
+                            make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                }
+            __syncwarp();
+            cluster_sync();
+            constexpr int V = D / 32;                            // values of a row per lane
+            for (int k = chunk + x.nchunk * (warp - 4); k < NT * PG_BM; k += x.nchunk * 4 * NT) {
+                const int kt = k / PG_BM, ki = (k % PG_BM) / x.grp, kh = k % PG_BM - ki * x.grp;
+                const int tok = t0 + kt * x.tt + ki;
+                const bool is_tok = ki < x.tt && tok < r.n_new;
+                if (!is_tok && (ki >= x.tt || tok >= a.S || a.q_start)) continue;
+                float f[PG_CLUSTER], ol[PG_CLUSTER], o[PG_CLUSTER][V], top = -INFINITY, sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < PG_CLUSTER; ++j) {
+                    f[j] = -INFINITY, ol[j] = 0.f;
+#pragma unroll
+                    for (int e = 0; e < V; ++e) o[j][e] = 0.f;
+                    if (j < x.nchunk && is_tok) {
+                        ld_dsmem_f32x2(dsmem_addr(ml + k, j), f[j], ol[j]);
+                        const uint32_t src = dsmem_addr(ob + k * L::PITCH + lane * V, j);
+                        if (V == 4) ld_dsmem_f32x4(src, o[j][0], o[j][1], o[j][V - 2], o[j][V - 1]);
+                        else ld_dsmem_f32x2(src, o[j][0], o[j][1]);
+                    }
+                    top = fmaxf(top, f[j]);
+                }
+                float acc[V];
+#pragma unroll
+                for (int e = 0; e < V; ++e) acc[e] = 0.f;
+#pragma unroll
+                for (int j = 0; j < PG_CLUSTER; ++j) {
+                    if (!(ol[j] > 0.f)) continue;                // (nothing seen there: O may be anything)
+                    const float w = ex2(f[j] - top);
+                    sum = fmaf(w, ol[j], sum);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) acc[e] = fmaf(w, o[j][e], acc[e]);
+                }
+                const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+                const size_t at = (size_t(r.q0) + tok) * a.Hq + size_t(g) * x.grp + kh;
+                uint32_t* dst = reinterpret_cast<uint32_t*>(x.out + at * D) + lane * (V / 2);
+#pragma unroll
+                for (int e = 0; e < V / 2; ++e) dst[e] = pack2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+                if (x.lse && lane == 0)
+                    x.lse[at] = sum > 0.f ? (top + log2f(sum)) * 0.6931471805599453f : is_tok ? -INFINITY : 0.f;
             }
+            __syncwarp();
+            cluster_sync();                                      // (no CTA leaves while its rows are read)
+        } else {
+            const size_t pr = ((size_t(cg) * x.tiles + tp * NT + t) * x.nchunk + chunk) * x.rows + row;
+            if (real) x.part_ml[pr] = has ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
+            float4* dst = reinterpret_cast<float4*>(x.part_o + pr * D);
+            if (load)
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    uint32_t o[32];
+                    __syncwarp();
+                    tc::tmem_ld32(ocol + uint32_t(c0), o);
+                    if (has)
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            dst[c0 / 4 + q] =
+                                make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]),
+                                            __uint_as_float(o[4 * q + 2]), __uint_as_float(o[4 * q + 3]));
+                }
         }
     }
     tc::fence_before_sync();
@@ -531,7 +608,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
 
 // ----------------------------------------------------------------------------- combine
 //
-// One warp per (request, token, query head): the chunks' (max, sum) pairs by the lanes in
+// Chunks that are no cluster. One warp per (request, token, query head): the chunks' (max, sum) pairs by the lanes in
 // parallel, then their rows of O eight at a time.
 
 template <int D>
@@ -611,8 +688,11 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
 // Tiles per CTA and chunks of a tile's key blocks: the least of (all CTAs' time / CTAs in
 // flight + one CTA's time), which bounds any order of CTAs of different lengths. In units
 // of a block's time (~1.6 us at D = 128): a block 1 (two tiles, one CTA an SM) or 1.15
-// (two CTAs of one tile, each reading the block), a CTA's start and end 2, a whole tile's
-// partial result 1.5, and merging 2 and its bytes.
+// (two CTAs of one tile, each reading the block), a CTA's start and end 2. Merging through
+// memory: 1.5 for a whole tile's partial result, 4 for the second launch, and the bytes;
+// within a cluster of one-tile CTAs, 1 for a whole tile and 1.5, where all CTAs run at
+// once (in several waves the CTAs that wait for their cluster's last hold up the next:
+// 64 tokens over 6144 rows 293 us in clusters, 261 us through memory).
 static PgPlan paged_plan(const PagedArgs& a) {
     PgPlan p{};
     const int grp = a.Hq / a.Hkv;
@@ -627,16 +707,21 @@ static PgPlan paged_plan(const PagedArgs& a) {
         const int64_t base = heads * ((p.tiles + nt - 1) / nt), slots = int64_t(num_sms()) * (nt == 1 ? 2 : 1);
         const int64_t most = slots / base > 16 ? slots / base : 16;
         for (int64_t n = 1; n <= blocks && n <= most; ++n) {
-            double cta = double((blocks + n - 1) / n) * (nt == 1 ? 1.15 : 1.0) + 2.0, merge = 0.0;
-            if (n > 1) {
-                cta += 1.5 * nt * p.rows / PG_BM;
-                merge = 2.0 + double(heads) * p.tiles * double(n) * p.rows * a.D * 4.0 / 1e7;
+            const double run = double((blocks + n - 1) / n) * (nt == 1 ? 1.15 : 1.0) + 2.0;
+            auto consider = [&](double cta, double merge, bool cluster) {
+                const double t = double(base * n) * cta / double(slots) + cta + merge;
+                if (t < best) best = t, p.nt = nt, p.nchunk = int(n), p.cluster = cluster;
+            };
+            if (n == 1) {
+                consider(run, 0.0, false);
+                continue;
             }
-            const double t = double(base * n) * cta / double(slots) + cta + merge;
-            if (t < best) best = t, p.nt = nt, p.nchunk = int(n);
+            consider(run + 1.5 * nt * p.rows / PG_BM,
+                     4.0 + double(heads) * p.tiles * double(n) * p.rows * a.D * 4.0 / 1e7, false);
+            if (nt == 1 && n <= PG_CLUSTER && base * n <= slots) consider(run + 1.0 * p.rows / PG_BM, 1.5, true);
         }
     }
-    if (p.nchunk > 1) {
+    if (p.nchunk > 1 && !p.cluster) {
         auto up = [](size_t b) { return (b + 255) / 256 * 256; };
         const size_t rows = size_t(a.C) * a.Hkv * p.tiles * p.nchunk * p.rows;
         p.part_ml = up(rows * a.D * 4);
@@ -660,10 +745,10 @@ bool make_query_map(CUtensorMap* m, const PagedArgs& a, const void* q, int tt) {
     return make_tensor_map_bf16_nd(m, q, 3, d, st, box);
 }
 
-template <int D, int NT, int ST>
+template <int D, int NT, int ST, bool CL = false>
 static int launch_attn_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PgArgs& x,
                          cudaStream_t stream) {
-    auto kern = paged_attn_kernel<D, NT, ST>;
+    auto kern = paged_attn_kernel<D, NT, ST, CL>;
     const size_t smem = PgSmem<D, NT, ST>::TOTAL;
     static std::atomic<uint64_t> raised{0};
     if (!raise_smem(kern, int(smem), raised)) return DARTREE_ECUDA;
@@ -672,9 +757,12 @@ static int launch_attn_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUt
     cfg.blockDim = dim3(128 + 128 * NT);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1] = {pdl_attribute()};
+    cudaLaunchAttribute attr[2] = {pdl_attribute()};
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(x.nchunk);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = CL ? 2 : 1;
     KTimer kt_(KID_PAGED_ATTN, stream);
     return cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, x) == cudaSuccess ? DARTREE_OK : DARTREE_ECUDA;
 }
@@ -688,13 +776,12 @@ int launch_paged_attention(const PagedArgs& a, const void* q, float scale, void*
     uint8_t* w = static_cast<uint8_t*>(part);
     PgArgs x{a, a.Hq / a.Hkv, p.tt, p.tiles, p.nchunk, p.rows, scale * LOG2E, static_cast<bf16_t*>(out), lse,
              reinterpret_cast<float*>(w), reinterpret_cast<float2*>(w + p.part_ml)};
-    int e;
-    if (a.D == 64)
-        e = p.nt == 2 ? launch_attn_t<64, 2, 8>(tq, tk, tv, x, stream) : launch_attn_t<64, 1, 4>(tq, tk, tv, x, stream);
-    else
-        e = p.nt == 2 ? launch_attn_t<128, 2, 5>(tq, tk, tv, x, stream)
-                      : launch_attn_t<128, 1, 2>(tq, tk, tv, x, stream);
-    if (e != DARTREE_OK || p.nchunk == 1) return e;
+    auto run = [&](auto two, auto one, auto cluster) {
+        return (p.nt == 2 ? two : p.cluster ? cluster : one)(tq, tk, tv, x, stream);
+    };
+    const int e = a.D == 64 ? run(launch_attn_t<64, 2, 8>, launch_attn_t<64, 1, 4>, launch_attn_t<64, 1, 4, true>)
+                            : run(launch_attn_t<128, 2, 5>, launch_attn_t<128, 1, 2>, launch_attn_t<128, 1, 2, true>);
+    if (e != DARTREE_OK || p.nchunk == 1 || p.cluster) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned((size_t(a.C) * a.S * a.Hq + 7) / 8));
     cfg.blockDim = dim3(256);

@@ -185,7 +185,8 @@ __global__ void __launch_bounds__(PW_NT, 2)
         if (n_t > 0 && tc::elect_one()) {
             const uint32_t id = tc::idesc_bf16_f32(PW_BM, (x.tt * x.grp + 15) / 16 * 16);
             constexpr uint32_t PSTEP = L::PANEL >> 4, TSTEP = L::TILE >> 4;  // descriptor steps (low word)
-            const uint32_t k0 = smem_u32(kring) >> 4, q0 = smem_u32(qring) >> 4, qstep = qpanel >> 4;
+            const uint32_t k0 = (smem_u32(kring) >> 4) & 0x3fffu, q0 = (smem_u32(qring) >> 4) & 0x3fffu,
+                           qstep = qpanel >> 4;
             constexpr uint32_t HI = uint32_t(tc::DESC_SW128_KMAJOR >> 32), LO = uint32_t(tc::DESC_SW128_KMAJOR);
             auto desc = [&](uint32_t at) { return (uint64_t(HI) << 32) | (LO | at); };
             int ks = 0, qs = 0, n = 0;

@@ -165,6 +165,9 @@ ATTN = [
     dict(new=[7, 1, 0, 12], old=[0, 130, 9, 128], S=12, tree=True),
     dict(new=[128, 100], old=[500, 31], tree=True, S=128, Hq=8, Hkv=8, D=64, page=32),
     dict(new=[300], old=[90], tree=True, S=300, Hq=4, Hkv=2),
+    # long contexts of few rows: many chunks, merged through memory
+    dict(new=[20, 11], old=[6000, 3000], tree=True, S=20, Hq=4, Hkv=1, page=64),
+    dict(new=[2, 0, 1], old=[7000, 10, 130], Hq=8, Hkv=1, D=64, page=256, pad=(1, 2)),
 ]
 
 
