@@ -467,21 +467,21 @@ int launch_paged_evict(const PagedArgs& a, const float* weights, int budget, int
 constexpr int PC_NT = 512;
 constexpr int PC_V = 8;
 
+template <int VECS>  // 16-byte vectors of a row
 __global__ void __launch_bounds__(PC_NT) paged_commit_kernel(PagedArgs a, const int32_t* __restrict__ path,
-                                                             const int32_t* accepted_len, int L, int32_t* n_out,
-                                                             int row_vecs) {
+                                                             const int32_t* accepted_len, int L, int32_t* n_out) {
     __shared__ long long s_src[DARTREE_MAX_L], s_dst[DARTREE_MAX_L];  // element offsets of head 0, -1: not moved
     griddep_launch_dependents();
     griddep_wait();
     const int c = int(blockIdx.x);
     const long cap = long(a.max_pages) << a.log2_page;
-    const int n0 = a.n_ctx[c], acc0 = accepted_len[c];
+    const int n0 = a.n_ctx[c], acc0 = accepted_len[c];  // (these and the path in one round trip)
+    const int slot = int(threadIdx.x) < L ? path[size_t(c) * L + threadIdx.x] : 0;
     const int old = int(min(max(long(n0), 0l), cap));
     const int acc = min(max(acc0, 0), min(L, a.S - 1));
     const long end = long(old) + 1 + acc;
     if (threadIdx.x == 0 && (old != n0 || acc != acc0 || end > cap)) set_status(a.status, DARTREE_EINTERNAL);
     if (int(threadIdx.x) < acc) {
-        const int slot = path[size_t(c) * L + threadIdx.x];
         const long src = long(old) + slot, dst = long(old) + 1 + threadIdx.x;
         long long so = -1, d_o = -1;
         if (slot < 1 || slot >= a.S || src >= cap || dst >= cap) {
@@ -502,42 +502,44 @@ __global__ void __launch_bounds__(PC_NT) paged_commit_kernel(PagedArgs a, const 
     __syncthreads();
     if (threadIdx.x == 0) n_out[c] = int(min(end, cap));
     if (acc == 0) return;
-    const int per = a.D / row_vecs;                     // elements of a vector
-    const int head_vecs = acc * row_vecs;               // of one head of keys or values
-    const int heads = min(2 * a.Hkv, PC_NT * PC_V / head_vecs);  // >= 2: 64 rows x 32 vectors at most
+    const int per = a.D / VECS;                         // elements of a vector
+    const int heads = min(2 * a.Hkv, PC_NT * PC_V / (acc * VECS));  // >= 2: 64 rows x 32 vectors at most
+    const uint32_t inv = 0xffffffffu / uint32_t(acc) + 1u;  // q / acc = high word of q * inv (q < 2^16, acc > 1)
+    const size_t head = size_t(a.page) * a.D / per;     // vectors between a page's heads
     for (int h0 = 0; h0 < 2 * a.Hkv; h0 += heads) {
-        const int total = min(heads, 2 * a.Hkv - h0) * head_vecs;
+        const int total = min(heads, 2 * a.Hkv - h0) * acc * VECS;
         uint4 x[PC_V];
-        size_t to[PC_V];
-        bool put[PC_V];
+        uint4* to[PC_V];
 #pragma unroll
         for (int u = 0; u < PC_V; ++u) {
             const int e = u * PC_NT + int(threadIdx.x);
-            put[u] = false;
+            to[u] = nullptr;
             if (e < total) {
-                const int h = h0 + e / head_vecs, f = e % head_vecs, r = f / row_vecs, v = f % row_vecs;
+                const int q = e / VECS, v = e % VECS;
+                const int hq = acc == 1 ? q : int(__umulhi(uint32_t(q), inv)), r = q - hq * acc, h = h0 + hq;
                 if (s_src[r] >= 0) {
-                    const size_t off = size_t(h >> 1) * (size_t(a.page) * a.D);
-                    const uint4* pool = static_cast<const uint4*>(h & 1 ? a.v : a.k);
-                    x[u] = pool[(size_t(s_src[r]) + off) / per + v];
-                    to[u] = (size_t(s_dst[r]) + off) / per + v;
-                    put[u] = true;
+                    uint4* pool = static_cast<uint4*>(h & 1 ? a.v : a.k) + size_t(h >> 1) * head + v;
+                    x[u] = pool[size_t(s_src[r]) / per];
+                    to[u] = pool + size_t(s_dst[r]) / per;
                 }
             }
         }
         __syncthreads();
 #pragma unroll
-        for (int u = 0; u < PC_V; ++u) {
-            const int e = u * PC_NT + int(threadIdx.x);
-            if (put[u]) static_cast<uint4*>((h0 + e / head_vecs) & 1 ? a.v : a.k)[to[u]] = x[u];
-        }
+        for (int u = 0; u < PC_V; ++u)
+            if (to[u]) *to[u] = x[u];
         // (the next batch holds other heads: no row of this one)
     }
 }
 
+template <int VECS>
+static cudaError_t launch_commit_t(const cudaLaunchConfig_t& cfg, const PagedArgs& a, const int32_t* path,
+                                   const int32_t* accepted_len, int L, int32_t* n_out) {
+    return cudaLaunchKernelEx(&cfg, paged_commit_kernel<VECS>, a, path, accepted_len, L, n_out);
+}
+
 int launch_paged_commit(const PagedArgs& a, const int32_t* path, const int32_t* accepted_len, int L, int32_t* n_out,
                         cudaStream_t stream) {
-    const int row_vecs = a.D * (a.dtype == DARTREE_BF16 ? 2 : 4) / 16;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned(a.C));
     cfg.blockDim = dim3(PC_NT);
@@ -546,9 +548,9 @@ int launch_paged_commit(const PagedArgs& a, const int32_t* path, const int32_t* 
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     KTimer kt_(KID_PAGED_COMMIT, stream);
-    return cudaLaunchKernelEx(&cfg, paged_commit_kernel, a, path, accepted_len, L, n_out, row_vecs) == cudaSuccess
-               ? DARTREE_OK
-               : DARTREE_ECUDA;
+    const int vecs = a.D * (a.dtype == DARTREE_BF16 ? 2 : 4) / 16;
+    const auto f = vecs == 8 ? launch_commit_t<8> : vecs == 16 ? launch_commit_t<16> : launch_commit_t<32>;
+    return f(cfg, a, path, accepted_len, L, n_out) == cudaSuccess ? DARTREE_OK : DARTREE_ECUDA;
 }
 
 }  // namespace dartree
