@@ -313,11 +313,25 @@ __global__ void __launch_bounds__(PS_NT) paged_select_kernel(PagedArgs a, const 
         for (int i = tid; i < PS_BINS; i += PS_NT) hist[i] = 0;
         __syncthreads();
         if (pass == 0 && in_smem) {
-#pragma unroll 8
-            for (int i = tid; i < m; i += PS_NT) {
-                const uint32_t k = evict_key(w[i]);
+            auto take = [&](int i, float f) {
+                const uint32_t k = evict_key(f);
                 keys[i] = k;
                 atomicAdd(&hist[k >> 21], 1u);
+            };
+            if ((reinterpret_cast<uintptr_t>(weights) & 15) == 0) {  // (a head's rows start 16-byte aligned)
+                const int first = sink & ~3;
+                const float4* w4 = reinterpret_cast<const float4*>(w - sink + first);
+#pragma unroll 4
+                for (int q = tid; first + 4 * q < n - recent; q += PS_NT) {
+                    const float4 f = w4[q];
+                    const int i = first + 4 * q - sink;
+                    if (i >= 0) take(i, f.x);
+                    if (i + 1 >= 0 && i + 1 < m) take(i + 1, f.y);
+                    if (i + 2 >= 0 && i + 2 < m) take(i + 2, f.z);
+                    if (i + 3 < m) take(i + 3, f.w);
+                }
+            } else {
+                for (int i = tid; i < m; i += PS_NT) take(i, w[i]);
             }
         } else {
 #pragma unroll 4
