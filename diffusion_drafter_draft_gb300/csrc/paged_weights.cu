@@ -367,14 +367,14 @@ int launch_paged_weights(const PagedArgs& a, const void* q, const float* lse, fl
     const int64_t blocks = ((int64_t(a.max_pages) << a.log2_page) + PW_BM - 1) / PW_BM;
     // Chunks of key blocks: the least of (all CTAs' time / CTAs in flight + one CTA's time), which
     // bounds any order of CTAs of different lengths. One query tile: in block times of reading keys
-    // (two CTAs an SM), a CTA's start and end counted as four; more: in tiles (an SM's CTAs share its
+    // (two CTAs an SM), a CTA's start and end counted as eight; more: in tiles (an SM's CTAs share its
     // arithmetic), counted as six.
     const int64_t sms = num_sms(), most = 4 * sms / heads > 64 ? 4 * sms / heads : 64;
     double best = 1e300;
     x.nchunk = 1;
     for (int64_t n = 1; n <= blocks && n <= most; ++n) {
         const int64_t per = (blocks + n - 1) / n;
-        const double cta = x.tiles == 1 ? double(per + 4) : double(per * x.tiles + 6);
+        const double cta = x.tiles == 1 ? double(per + 8) : double(per * x.tiles + 6);
         const double t = double(heads * n) * cta / double(x.tiles == 1 ? 2 * sms : sms) + cta;
         if (t < best) best = t, x.nchunk = int(n);
     }
