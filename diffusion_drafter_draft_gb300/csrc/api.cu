@@ -589,7 +589,7 @@ int check_paged(const dartree_paged_params* p, PagedArgs* a) {
     // row numbers, the rows of q and the launches' CTA counts stay below 2^31
     const int64_t most = int64_t(1) << 31, rows = int64_t(p->max_pages) << lg;
     const int64_t heads = int64_t(p->C) * p->Hkv;
-    if (rows + p->S + 1024 >= most || int64_t(p->C) * p->S >= most || heads >= most ||
+    if (rows + p->S + 1024 >= most || int64_t(p->C) * p->S >= most || heads >= (int64_t(1) << 24) ||
         int64_t(p->C) * p->S * p->Hq >= most || heads * (rows / 128 + 1) >= most)
         return DARTREE_EUNSUPPORTED;
     *a = PagedArgs{};

@@ -312,7 +312,7 @@ DARTREE_API int dartree_tree_attention(const dartree_attn_params* p, const void*
  * only.
  * Workspace of all calls: dartree_paged_workspace_bytes. */
 typedef struct {
-    int C;          /* requests */
+    int C;          /* requests (C * Hkv < 2^24, and C * S * Hq and max_pages * page + S below 2^31) */
     int T;          /* rows of q (C * S without q_start) */
     int S;          /* most new tokens of one request, >= 1 */
     int Hq, Hkv;    /* query heads (a multiple of Hkv, at most 128 per key/value head), key/value heads */
@@ -402,7 +402,7 @@ DARTREE_API int dartree_paged_weights(const dartree_paged_params* p, const void*
  *   keep         [C, Hkv, budget] output: the kept rows, ascending, -1 behind them
  *   n_out        [C] output: min(n_ctx, budget) (may be cache->n_ctx itself)
  *   weights_out  [C, Hkv, dst_pages * page] output: the kept rows' weights (others not
- *                touched), or NULL
+ *                touched), or NULL; not part of weights
  * T, S, Hq and q_start are not used. Pages of either dtype. */
 DARTREE_API int dartree_paged_evict(const dartree_paged_params* p, const dartree_paged_cache* cache,
                                     const float* weights, int budget, int sink, int recent,

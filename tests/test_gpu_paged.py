@@ -422,6 +422,8 @@ EVICT = [
     dict(old=[70], budget=1, sink=0, recent=1, dtype="f32"),
     dict(old=[20000, 3], budget=5000, sink=1, recent=7, page=256, Hkv=1),
     dict(old=[33, 33], budget=32, sink=0, recent=0),                               # one row goes
+    dict(old=[60000], budget=700, sink=3, recent=5, page=256, Hkv=1),              # more rows than fit on chip
+    dict(old=[130, 99], budget=40, sink=13, recent=7),                             # the ranked rows start odd
 ]
 
 
