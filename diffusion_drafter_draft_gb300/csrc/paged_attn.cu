@@ -53,10 +53,11 @@ struct PgSmem {
     static constexpr size_t TOTAL = SLOT_OFF + 16 + 1024;       // (+ alignment of the base to 1024)
     static_assert(TOTAL <= 227 * 1024, "tiles and ring fit in shared memory");
     // merge of a cluster's chunks, over tiles and ring: O of each row in fp32 (a row's 16 extra bytes
-    // keep the rows of a warp in different banks), then (maximum, sum)
+    // keep the rows of a warp in different banks), (maximum, sum), its place
     static constexpr int PITCH = D + 4;
     static constexpr size_t ML_OFF = size_t(NT) * PG_BM * PITCH * 4;
-    static_assert(ML_OFF + NT * PG_BM * 8 <= BAR_OFF, "merge fits in the tiles' place");
+    static constexpr size_t ROW_OFF = ML_OFF + NT * PG_BM * 8;  // int [NT][128]: a row's place in the output
+    static_assert(ROW_OFF + NT * PG_BM * 4 <= BAR_OFF, "merge fits in the tiles' place");
 };
 
 constexpr int PG_CLUSTER = 8;         // chunks that merge through shared memory
@@ -527,7 +528,10 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
             if (nblk > 0) mbar_wait_bounded(&ofull[nact - 1], 0, a.status);
             __syncwarp();
             const int rr = t * PG_BM + row;
+            int* const places = reinterpret_cast<int*>(smem + L::ROW_OFF);
             ml[rr] = has ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
+            // (token * heads + head: below 2^31; -2 - place: a slot without a node; -1: no row)
+            places[rr] = real ? int(orow) : slot_ok && !a.q_start ? -2 - int(orow) : -1;
             if (load)
 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 32) {
@@ -541,44 +545,39 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
                 }
             __syncwarp();
             cluster_sync();
+            // (little code: it runs once, out of a cold instruction cache)
             constexpr int V = D / 32;                            // values of a row per lane
+#pragma unroll 1
             for (int k = chunk + x.nchunk * (warp - 4); k < NT * PG_BM; k += x.nchunk * 4 * NT) {
-                const int kt = k / PG_BM, ki = (k % PG_BM) / x.grp, kh = k % PG_BM - ki * x.grp;
-                const int tok = t0 + kt * x.tt + ki;
-                const bool is_tok = ki < x.tt && tok < r.n_new;
-                if (!is_tok && (ki >= x.tt || tok >= a.S || a.q_start)) continue;
-                float f[PG_CLUSTER], ol[PG_CLUSTER], o[PG_CLUSTER][V], top = -INFINITY, sum = 0.f;
+                const int place = places[k];
+                if (place == -1) continue;
+                float o[PG_CLUSTER][V], mj = -INFINITY, lj = 0.f;
+                if (lane < x.nchunk) ld_dsmem_f32x2(dsmem_addr(ml + k, lane), mj, lj);
 #pragma unroll
-                for (int j = 0; j < PG_CLUSTER; ++j) {
-                    f[j] = -INFINITY, ol[j] = 0.f;
-#pragma unroll
-                    for (int e = 0; e < V; ++e) o[j][e] = 0.f;
-                    if (j < x.nchunk && is_tok) {
-                        ld_dsmem_f32x2(dsmem_addr(ml + k, j), f[j], ol[j]);
+                for (int j = 0; j < PG_CLUSTER; ++j)
+                    if (j < x.nchunk) {
                         const uint32_t src = dsmem_addr(ob + k * L::PITCH + lane * V, j);
                         if (V == 4) ld_dsmem_f32x4(src, o[j][0], o[j][1], o[j][V - 2], o[j][V - 1]);
                         else ld_dsmem_f32x2(src, o[j][0], o[j][1]);
                     }
-                    top = fmaxf(top, f[j]);
-                }
+                const float top = warp_max(mj), w = lj > 0.f ? ex2(mj - top) : 0.f, sum = warp_sum(w * lj);
+                const float inv = sum > 0.f ? 1.0f / sum : 0.f;
                 float acc[V];
 #pragma unroll
                 for (int e = 0; e < V; ++e) acc[e] = 0.f;
 #pragma unroll
                 for (int j = 0; j < PG_CLUSTER; ++j) {
-                    if (!(ol[j] > 0.f)) continue;                // (nothing seen there: O may be anything)
-                    const float w = ex2(f[j] - top);
-                    sum = fmaf(w, ol[j], sum);
+                    const float wj = __shfl_sync(0xffffffffu, w, j);
+                    if (j < x.nchunk && wj > 0.f)                // (nothing seen there: O may be anything)
 #pragma unroll
-                    for (int e = 0; e < V; ++e) acc[e] = fmaf(w, o[j][e], acc[e]);
+                        for (int e = 0; e < V; ++e) acc[e] = fmaf(wj, o[j][e], acc[e]);
                 }
-                const float inv = sum > 0.f ? 1.0f / sum : 0.f;
-                const size_t at = (size_t(r.q0) + tok) * a.Hq + size_t(g) * x.grp + kh;
+                const size_t at = size_t(place >= 0 ? place : -2 - place);
                 uint32_t* dst = reinterpret_cast<uint32_t*>(x.out + at * D) + lane * (V / 2);
 #pragma unroll
                 for (int e = 0; e < V / 2; ++e) dst[e] = pack2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
                 if (x.lse && lane == 0)
-                    x.lse[at] = sum > 0.f ? (top + log2f(sum)) * 0.6931471805599453f : is_tok ? -INFINITY : 0.f;
+                    x.lse[at] = sum > 0.f ? (top + log2f(sum)) * 0.6931471805599453f : place >= 0 ? -INFINITY : 0.f;
             }
             __syncwarp();
             cluster_sync();                                      // (no CTA leaves while its rows are read)
