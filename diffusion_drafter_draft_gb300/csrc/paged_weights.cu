@@ -14,8 +14,9 @@
 //   warp 1      issues S^T into one of two tensor-memory buffers
 //   warps 2..9  two groups of 128 threads, one per buffer: while one adds up a tile the
 //               other's is formed; the groups' sums of a block meet in shared memory
-// Single tokens are bound by reading the keys once; long chunks by the exponentials
-// (one per score) beside one matrix product.
+// Single tokens are bound by reading the keys once (16 tokens over 4096-8192 rows: 45 us,
+// 4.6 TB/s); chunks by the sums, an exponential per score and ~4.5 instructions (two chunks
+// of 256-511 tokens over 4000-8000 rows, 16/4 heads of 64: 32 us, the exponentials alone 12).
 // Every mbarrier wait is bounded; one that runs out records DARTREE_ETIMEOUT.
 #include <cuda.h>
 #include <cuda_bf16.h>

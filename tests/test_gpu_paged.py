@@ -168,6 +168,7 @@ ATTN = [
     # long contexts of few rows: many chunks, merged through memory
     dict(new=[20, 11], old=[6000, 3000], tree=True, S=20, Hq=4, Hkv=1, page=64),
     dict(new=[2, 0, 1], old=[7000, 10, 130], Hq=8, Hkv=1, D=64, page=256, pad=(1, 2)),
+    dict(new=[3], old=[70000], Hq=4, Hkv=1, D=64, page=256),
 ]
 
 
