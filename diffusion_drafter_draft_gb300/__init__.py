@@ -818,7 +818,8 @@ class PagedCache:
 
     def attention(self, q, tree=None, scale=None, out=None, lse=None, stream=None):
         """Attention of the new tokens, already appended, over the pages (dartree_paged_attention):
-        q [T, Hq, D] rotated -> out [T, Hq, D]; lse [T, Hq] float32 is filled when given."""
+        q [T, Hq, D] rotated -> out [T, Hq, D], not q itself; lse [T, Hq] float32 is filled when given.
+        scale: None or 0 for 1 / sqrt(D)."""
         qp = self._need(q, "q", self.dtype, self._shapes["q"])
         if out is None:
             out = self._new(torch.empty, self._shapes["q"], self.dtype, stream)
@@ -839,7 +840,8 @@ class PagedCache:
     def evict(self, weights, budget, dst_table, sink=0, recent=0, keep=None, n_out=None, weights_out=None,
               stream=None):
         """The first `sink`, the last `recent` and the heaviest other rows of every request and key/value
-        head, `budget` in all, copied into the pages of dst_table [C, dst_pages] (dartree_paged_evict) ->
+        head, `budget` in all, copied into the pages of dst_table [C, dst_pages], none of them pages of
+        the cache's table (dartree_paged_evict) ->
         dict(keep [C, Hkv, budget], n [C], weights [C, Hkv, dst_pages * page])."""
         budget = int(budget)
         wp = self._need(weights, "weights", torch.float32, self._shapes["w"])

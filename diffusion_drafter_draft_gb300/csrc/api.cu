@@ -563,6 +563,12 @@ namespace {
 
 bool al16(const void* x) { return x && reinterpret_cast<uintptr_t>(x) % 16 == 0; }
 
+// Whether na bytes from a and nb bytes from b share one.
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + uint64_t(nb) && y < x + uint64_t(na);
+}
+
 // Workspace of the paged calls: status word, the counts of an eviction, the partial
 // results of an attention.
 struct PagedLayout {
@@ -590,7 +596,8 @@ int check_paged(const dartree_paged_params* p, PagedArgs* a) {
     const int64_t most = int64_t(1) << 31, rows = int64_t(p->max_pages) << lg;
     const int64_t heads = int64_t(p->C) * p->Hkv;
     if (rows + p->S + 1024 >= most || int64_t(p->C) * p->S >= most || heads >= (int64_t(1) << 24) ||
-        int64_t(p->C) * p->S * p->Hq >= most || heads * (rows / 128 + 1) >= most)
+        int64_t(p->C) * p->S * p->Hq >= most || int64_t(p->T) * p->Hq >= most ||
+        heads * (rows / 128 + 1) >= most)
         return DARTREE_EUNSUPPORTED;
     *a = PagedArgs{};
     a->C = p->C, a->T = p->T, a->S = p->S, a->Hq = p->Hq, a->Hkv = p->Hkv, a->D = p->D, a->page = p->page;
@@ -639,6 +646,12 @@ int dartree_paged_append(const dartree_paged_params* p, const dartree_paged_toke
         return DARTREE_EINVAL;
     if (x->q == q_out && x->ldq != int64_t(a.Hq) * a.D) return DARTREE_EINVAL;
     if (int e = check_ws(ws, ws_bytes, paged_layout(a).total)) return e;
+    const int64_t es = 16 / vec, out_bytes = int64_t(a.T) * a.Hq * a.D * es;
+    auto in_out = [&](const void* t, int64_t ld, int heads) {
+        return overlap(q_out, out_bytes, t, ((a.T - 1) * ld + int64_t(heads) * a.D) * es);
+    };
+    if ((x->q != q_out && in_out(x->q, x->ldq, a.Hq)) || in_out(x->k, x->ldk, a.Hkv) || in_out(x->v, x->ldv, a.Hkv))
+        return DARTREE_EINVAL;
     a.status = at<int>(ws, 0);
     return launch_paged_append(a, x->q, x->k, x->v, x->ldq, x->ldk, x->ldv, x->gq, x->gk, x->pos_base, x->eps,
                                double(x->theta), q_out, as_stream(stream));
@@ -670,6 +683,9 @@ int dartree_paged_attention(const dartree_paged_params* p, const void* q, const 
     if (!al16(out) || (lse && reinterpret_cast<uintptr_t>(lse) % 4 != 0)) return DARTREE_EINVAL;
     const PagedLayout l = paged_layout(a);
     if (int e = check_ws(ws, ws_bytes, l.total)) return e;
+    const int64_t rows = int64_t(a.T) * a.Hq, bytes = rows * a.D * 2;
+    if (overlap(out, bytes, q, bytes) || (lse && (overlap(lse, rows * 4, q, bytes) || overlap(lse, rows * 4, out, bytes))))
+        return DARTREE_EINVAL;
     a.status = at<int>(ws, 0);
     return launch_paged_attention(a, q, scale, out, lse, at<void>(ws, l.part), as_stream(stream));
 }
@@ -708,6 +724,9 @@ int dartree_paged_evict(const dartree_paged_params* p, const dartree_paged_cache
     if (!weights || !dst_table || !keep || !n_out) return DARTREE_EINVAL;
     const PagedLayout l = paged_layout(a);
     if (int e = check_ws(ws, ws_bytes, l.total)) return e;
+    const int64_t row = int64_t(a.C) * a.Hkv * a.page * 4;  // of weights, per page
+    if (dst_table == cache->table || (weights_out && overlap(weights, row * a.max_pages, weights_out, row * dst_pages)))
+        return DARTREE_EINVAL;
     a.status = at<int>(ws, 0);
     return launch_paged_evict(a, weights, budget, sink, recent, dst_table, dst_pages, keep, n_out, weights_out,
                               at<int32_t>(ws, l.counts), as_stream(stream));

@@ -312,7 +312,7 @@ DARTREE_API int dartree_tree_attention(const dartree_attn_params* p, const void*
  * only.
  * Workspace of all calls: dartree_paged_workspace_bytes. */
 typedef struct {
-    int C;          /* requests (C * Hkv < 2^24, and C * S * Hq and max_pages * page + S below 2^31) */
+    int C;          /* requests (C * Hkv < 2^24; C * S * Hq, T * Hq and max_pages * page + S below 2^31) */
     int T;          /* rows of q (C * S without q_start) */
     int S;          /* most new tokens of one request, >= 1 */
     int Hq, Hkv;    /* query heads (a multiple of Hkv, at most 128 per key/value head), key/value heads */
@@ -345,7 +345,8 @@ DARTREE_API size_t dartree_paged_workspace_bytes(const dartree_paged_params* p);
  *               theta^(-2i/D) as in dartree_tree_attention.
  *   q_out       [T, Hq, D]
  * Norm and rotation in fp32 (angles reduced in double), rounded once to dtype. All
- * pointers 16-byte aligned. q_out may be q itself when ldq = Hq * D. */
+ * pointers 16-byte aligned. q_out may be q itself when ldq = Hq * D and shares no byte
+ * with q, k and v otherwise (DARTREE_EINVAL). */
 typedef struct {
     const void* q;
     const void* k;
@@ -368,6 +369,7 @@ DARTREE_API int dartree_paged_append(const dartree_paged_params* p, const dartre
  *         no context) gives zeros
  *   lse   [T, Hq] float, natural logarithm of the sum of exponentials of a row's scaled
  *         scores (-inf for a token that sees nothing), or NULL
+ * q, out and lse share no byte (DARTREE_EINVAL).
  * bf16 only (DARTREE_EUNSUPPORTED otherwise). Scores and sums in fp32; probabilities
  * are rounded to bf16 for the product with the values. Page rows behind a request's
  * last one (n_ctx + its new tokens) may hold anything, infinities and NaN included; the

@@ -40,7 +40,8 @@ BAD = [(dict(C=-1), "EINVAL"), (dict(S=0), "EINVAL"), (dict(T=-1), "EINVAL"), (d
        (dict(D=256), "EUNSUPPORTED"), (dict(page=8), "EUNSUPPORTED"), (dict(page=48), "EUNSUPPORTED"),
        (dict(page=512), "EUNSUPPORTED"), (dict(Hq=258, Hkv=2), "EUNSUPPORTED"),
        (dict(page=256, max_pages=1 << 23), "EUNSUPPORTED"),   # 2^31 rows
-       (dict(C=1 << 15, S=1 << 16, T=1 << 30), "EUNSUPPORTED")]
+       (dict(C=1 << 15, S=1 << 16, T=1 << 30), "EUNSUPPORTED"),
+       (dict(T=(1 << 31) // 8, Hq=8, Hkv=2), "EUNSUPPORTED")]  # T * Hq = 2^31
 
 
 @pytest.mark.parametrize("kw,err", BAD)
@@ -140,6 +141,42 @@ def test_evict_and_commit_arguments(dd):
     assert cm(Lp=65) == dd.EUNSUPPORTED
     assert cm(n=need - 1) == dd.EWORKSPACE
     assert cm(p=_p(dd, C=0, T=0)) == dd.OK
+
+
+def test_outputs_inside_inputs_are_refused(dd):
+    """Kernels read these inputs while other CTAs write the outputs."""
+    L, p, m = dd.lib(), ctypes.byref(_p(dd)), ctypes.byref(_m(dd))
+    need = L.dartree_paged_workspace_bytes(p)
+    at = lambda n: ctypes.c_void_p((1 << 24) + n)   # one buffer of q rows: T * Hq * D * 2 bytes
+    n = 6 * 8 * 128 * 2
+
+    def app(out, **kw):
+        x = _x(dd, **{**dict(q=1 << 24, k=1 << 28, v=1 << 29), **kw})
+        return L.dartree_paged_append(p, ctypes.byref(x), m, None, out, WS, need, None)
+
+    assert app(at(16)) == dd.EINVAL
+    assert app(at(n - 16)) == dd.EINVAL
+    assert app(at(16 - n)) == dd.EINVAL
+    assert app(at(0), k=(1 << 24) + n - 16) == dd.EINVAL     # in place, keys in its last bytes
+    assert app(at(0), v=(1 << 24) - 6 * 2 * 128 * 2 + 16) == dd.EINVAL
+    assert app(at(0), q=(1 << 24) - 2048, ldq=3 * 1024) == dd.EINVAL
+
+    def att(out, lse=None):
+        return L.dartree_paged_attention(p, at(0), m, None, 0.0, out, lse, WS, need, None)
+
+    for d in (0, 16, n - 16, 16 - n):
+        assert att(at(d)) == dd.EINVAL, d
+    assert att(at(n), at(n - 4)) == dd.EINVAL                # lse in q's last bytes
+    assert att(at(n), at(n + 64)) == dd.EINVAL               # in out
+
+    def ev(dst, w, wo):
+        return L.dartree_paged_evict(p, m, w, 64, 4, 8, dst, 1, FAKE, FAKE, wo, WS, need, None)
+
+    w = 2 * 2 * 4 * 64 * 4                                   # bytes of weights: C, Hkv, max_pages * page floats
+    assert ev(FAKE, at(0), None) == dd.EINVAL                # the cache's own table
+    assert ev(at(-4096), at(0), at(0)) == dd.EINVAL
+    assert ev(at(-4096), at(0), at(w - 4)) == dd.EINVAL
+    assert ev(at(-4096), at(0), at(4 - w // 4)) == dd.EINVAL
 
 
 def test_kernel_families_are_named(dd):
