@@ -271,7 +271,10 @@ int launch_paged_append(const PagedArgs& a, const void* q, const void* k, const 
 // every run its place, and the kept rows are written ascending.
 // paged_move_kernel: PM_U rows' 16-byte vectors per thread, their addresses looked up
 // before the first is read (one vector per thread, a chain of four dependent loads each,
-// took 91 us where this takes 54 for 134 MB each way, 5.0 TB/s; eight rows 67).
+// took 91 us where this takes 48 for 134 MB each way, 5.6 TB/s; eight rows 67). From
+// PM_STREAM bytes on neither side is meant to stay in the L2: with and without that,
+// selection included, 8 MB 15.1 and 14.4 us, 17 MB 17.8 and 18.5, 34 MB 23.9 and 25.1, 134
+// MB 56.7 and 60.8, and an attention over the copies that follows keeps the gain.
 // 128 heads of 8192-16384 rows to 2048: selection 16 us, bound by its passes' latency (one
 // CTA per head), then the copy, bound by memory.
 
@@ -378,10 +381,11 @@ __global__ void __launch_bounds__(PS_NT) paged_select_kernel(PagedArgs a, const 
     }
 }
 
-constexpr int PM_NT = 256;
-constexpr int PM_U = 4;
+constexpr int PM_NT = 128;
+constexpr int PM_U = 3;
+constexpr int64_t PM_STREAM = int64_t(16) << 20;  // bytes copied
 
-template <int VECS>  // 16-byte vectors of a row; a row's keys come first, then its values
+template <int VECS, bool STREAM>  // 16-byte vectors of a row; a row's keys come first, then its values
 __global__ void __launch_bounds__(PM_NT) paged_move_kernel(PagedArgs a, const float* __restrict__ weights, int budget,
                                                            const int32_t* __restrict__ dst_table, int dst_pages,
                                                            const int32_t* __restrict__ keep,
@@ -417,13 +421,17 @@ __global__ void __launch_bounds__(PM_NT) paged_move_kernel(PagedArgs a, const fl
     };
 #pragma unroll
     for (int u = 0; u < PM_U; ++u)
-        if (sp[u] >= 0 && dp[u] >= 0) x[u] = vector(sp[u], src[u]);
+        if (sp[u] >= 0 && dp[u] >= 0) x[u] = STREAM ? __ldcs(&vector(sp[u], src[u])) : vector(sp[u], src[u]);
 #pragma unroll
     for (int u = 0; u < PM_U; ++u) {
         if (src[u] < 0) continue;
         const int r = r0 + u * RP;
-        if (sp[u] >= 0 && dp[u] >= 0) vector(dp[u], r) = x[u];
-        else if (vec == 0) set_status(a.status, DARTREE_EINTERNAL);
+        if (sp[u] >= 0 && dp[u] >= 0) {
+            if (STREAM) __stcs(&vector(dp[u], r), x[u]);
+            else vector(dp[u], r) = x[u];
+        } else if (vec == 0) {
+            set_status(a.status, DARTREE_EINTERNAL);
+        }
         if (vec == 0 && weights_out)
             weights_out[size_t(cg) * (size_t(dst_pages) << a.log2_page) + r] =
                 weights[size_t(cg) * (size_t(a.max_pages) << a.log2_page) + src[u]];
@@ -443,8 +451,9 @@ static cudaError_t launch_move(const PagedArgs& a, const float* weights, int bud
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     KTimer kt_(KID_PAGED_MOVE, stream);
-    return cudaLaunchKernelEx(&cfg, paged_move_kernel<VECS>, a, weights, budget, dst_table, dst_pages, keep, counts,
-                              n_out, weights_out, per);
+    const bool stream_it = int64_t(a.C) * a.Hkv * budget * (2 * VECS * 16) >= PM_STREAM;
+    return cudaLaunchKernelEx(&cfg, stream_it ? paged_move_kernel<VECS, true> : paged_move_kernel<VECS, false>, a,
+                              weights, budget, dst_table, dst_pages, keep, counts, n_out, weights_out, per);
 }
 
 int launch_paged_evict(const PagedArgs& a, const float* weights, int budget, int sink, int recent,

@@ -425,6 +425,10 @@ EVICT = [
     dict(old=[33, 33], budget=32, sink=0, recent=0),                               # one row goes
     dict(old=[60000], budget=700, sink=3, recent=5, page=256, Hkv=1),              # more rows than fit on chip
     dict(old=[130, 99], budget=40, sink=13, recent=7),                             # the ranked rows start odd
+    # copies of 16 MB and more, the last rows of a budget that no CTA's rows divide
+    dict(old=[9000, 4200], budget=4101, sink=4, recent=100, page=64, D=128, Hkv=4),
+    dict(old=[5000, 4097, 17], budget=4097, sink=4, recent=100, page=16, D=128, Hkv=4, dtype="f32"),
+    dict(old=[8300, 8193], budget=8193, sink=0, recent=1, page=128, D=64, Hkv=4),
 ]
 
 
