@@ -549,39 +549,63 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
                 }
             __syncwarp();
             cluster_sync();
-            // (little code: it runs once, out of a cold instruction cache)
+            // this warp's rows are k0 + step i: lane i has row i's place and, from one round of reads, its
+            // factors 2^(m_j - m) / sum (four trees: 27.1 us, 29.9 with a round of reads for every row);
+            // the first row's O is on its way before they are known. One row in hand: two take 26.7,
+            // but a single token then 11.0 instead of 10.7 (more code, run once out of a cold cache)
             constexpr int V = D / 32;                            // values of a row per lane
+            const int k0 = chunk + x.nchunk * (warp - 4), step = x.nchunk * 4 * NT, kl = k0 + step * lane;
+            const int place = kl < NT * PG_BM ? places[kl] : -1; // (at most 16 rows)
+            float f[PG_CLUSTER], lj[PG_CLUSTER], o[PG_CLUSTER][V];
+#pragma unroll
+            for (int j = 0; j < PG_CLUSTER; ++j) {
+                f[j] = -INFINITY, lj[j] = 0.f;
+                if (j < x.nchunk && place != -1) ld_dsmem_f32x2(dsmem_addr(ml + kl, j), f[j], lj[j]);
+            }
+            bool known = false;
+            unsigned left = __ballot_sync(0xffffffffu, place != -1);
 #pragma unroll 1
-            for (int k = chunk + x.nchunk * (warp - 4); k < NT * PG_BM; k += x.nchunk * 4 * NT) {
-                const int place = places[k];
-                if (place == -1) continue;
-                float o[PG_CLUSTER][V], mj = -INFINITY, lj = 0.f;
-                if (lane < x.nchunk) ld_dsmem_f32x2(dsmem_addr(ml + k, lane), mj, lj);
+            while (left) {
+                const int i = __ffs(left) - 1;
+                left &= left - 1;
 #pragma unroll
                 for (int j = 0; j < PG_CLUSTER; ++j)
                     if (j < x.nchunk) {
-                        const uint32_t src = dsmem_addr(ob + k * L::PITCH + lane * V, j);
+                        const uint32_t src = dsmem_addr(ob + (k0 + step * i) * L::PITCH + lane * V, j);
                         if (V == 4) ld_dsmem_f32x4(src, o[j][0], o[j][1], o[j][V - 2], o[j][V - 1]);
                         else ld_dsmem_f32x2(src, o[j][0], o[j][1]);
                     }
-                const float top = warp_max(mj), w = lj > 0.f ? ex2(mj - top) : 0.f, sum = warp_sum(w * lj);
-                const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+                if (!known) {
+                    known = true;
+                    float top = -INFINITY, sum = 0.f;
+#pragma unroll
+                    for (int j = 0; j < PG_CLUSTER; ++j) top = fmaxf(top, f[j]);
+#pragma unroll
+                    for (int j = 0; j < PG_CLUSTER; ++j) {
+                        f[j] = lj[j] > 0.f ? ex2(f[j] - top) : 0.f;
+                        sum = fmaf(f[j], lj[j], sum);
+                    }
+                    const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+#pragma unroll
+                    for (int j = 0; j < PG_CLUSTER; ++j) f[j] *= inv;
+                    if (x.lse && place != -1)
+                        x.lse[place >= 0 ? place : -2 - place] =
+                            sum > 0.f ? (top + log2f(sum)) * 0.6931471805599453f : place >= 0 ? -INFINITY : 0.f;
+                }
                 float acc[V];
 #pragma unroll
                 for (int e = 0; e < V; ++e) acc[e] = 0.f;
 #pragma unroll
                 for (int j = 0; j < PG_CLUSTER; ++j) {
-                    const float wj = __shfl_sync(0xffffffffu, w, j);
-                    if (j < x.nchunk && wj > 0.f)                // (nothing seen there: O may be anything)
+                    const float fj = __shfl_sync(0xffffffffu, f[j], i);
+                    if (j < x.nchunk && fj > 0.f)                // (nothing seen there: O may be anything)
 #pragma unroll
-                        for (int e = 0; e < V; ++e) acc[e] = fmaf(wj, o[j][e], acc[e]);
+                        for (int e = 0; e < V; ++e) acc[e] = fmaf(fj, o[j][e], acc[e]);
                 }
-                const size_t at = size_t(place >= 0 ? place : -2 - place);
-                uint32_t* dst = reinterpret_cast<uint32_t*>(x.out + at * D) + lane * (V / 2);
+                const int to = __shfl_sync(0xffffffffu, place, i);
+                uint32_t* dst = reinterpret_cast<uint32_t*>(x.out + size_t(to >= 0 ? to : -2 - to) * D) + lane * (V / 2);
 #pragma unroll
-                for (int e = 0; e < V / 2; ++e) dst[e] = pack2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-                if (x.lse && lane == 0)
-                    x.lse[at] = sum > 0.f ? (top + log2f(sum)) * 0.6931471805599453f : place >= 0 ? -INFINITY : 0.f;
+                for (int e = 0; e < V / 2; ++e) dst[e] = pack2(acc[2 * e], acc[2 * e + 1]);
             }
             __syncwarp();
             cluster_sync();                                      // (no CTA leaves while its rows are read)
