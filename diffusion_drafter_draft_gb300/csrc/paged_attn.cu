@@ -35,15 +35,13 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
-#include "paged.cuh"
+#include "paged_attn.cuh"
 #include "tc.cuh"
 
 namespace dartree {
 
 constexpr int PG_BM = 128;            // rows of a tile
 constexpr int PG_BN = 128;            // keys of a block
-constexpr float PG_MOST = 16384.0f;    // sum of a block's weights from which a new maximum is taken
-constexpr float LOG2E = 1.4426950408889634f;
 
 template <int D, int NT, int ST>
 struct PgSmem {
@@ -64,28 +62,11 @@ struct PgSmem {
     static_assert(ROW_OFF + NT * PG_BM * 4 <= BAR_OFF, "merge fits in the tiles' place");
 };
 
-constexpr int PG_CLUSTER = 8;         // chunks that merge through shared memory
-
 struct PgPlan {
     int tt, tiles, nt, nchunk, rows;  // tokens per tile, tiles, tiles per CTA, chunks, rows kept per partial tile
-    bool cluster;                     // the chunks merge through shared memory
+    bool cluster, few;                // the chunks merge through shared memory; at most 16 rows
     size_t part_o, part_ml, total;    // workspace (partials): offsets and bytes
 };
-
-struct PgArgs {
-    PagedArgs a;
-    int grp, tt, tiles, nchunk, rows;
-    float sl2;                        // scale * log2(e)
-    bf16_t* out;
-    float* lse;
-    float* part_o;
-    float2* part_ml;
-};
-
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
 
 template <int D, int NT, int ST, bool CL>
 __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
@@ -549,64 +530,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
                 }
             __syncwarp();
             cluster_sync();
-            // this warp's rows are k0 + step i: lane i has row i's place and, from one round of reads, its
-            // factors 2^(m_j - m) / sum (four trees: 27.1 us, 29.9 with a round of reads for every row);
-            // the first row's O is on its way before they are known. One row in hand: two take 26.7,
-            // but a single token then 11.0 instead of 10.7 (more code, run once out of a cold cache)
-            constexpr int V = D / 32;                            // values of a row per lane
-            const int k0 = chunk + x.nchunk * (warp - 4), step = x.nchunk * 4 * NT, kl = k0 + step * lane;
-            const int place = kl < NT * PG_BM ? places[kl] : -1; // (at most 16 rows)
-            float f[PG_CLUSTER], lj[PG_CLUSTER], o[PG_CLUSTER][V];
-#pragma unroll
-            for (int j = 0; j < PG_CLUSTER; ++j) {
-                f[j] = -INFINITY, lj[j] = 0.f;
-                if (j < x.nchunk && place != -1) ld_dsmem_f32x2(dsmem_addr(ml + kl, j), f[j], lj[j]);
-            }
-            bool known = false;
-            unsigned left = __ballot_sync(0xffffffffu, place != -1);
-#pragma unroll 1
-            while (left) {
-                const int i = __ffs(left) - 1;
-                left &= left - 1;
-#pragma unroll
-                for (int j = 0; j < PG_CLUSTER; ++j)
-                    if (j < x.nchunk) {
-                        const uint32_t src = dsmem_addr(ob + (k0 + step * i) * L::PITCH + lane * V, j);
-                        if (V == 4) ld_dsmem_f32x4(src, o[j][0], o[j][1], o[j][V - 2], o[j][V - 1]);
-                        else ld_dsmem_f32x2(src, o[j][0], o[j][1]);
-                    }
-                if (!known) {
-                    known = true;
-                    float top = -INFINITY, sum = 0.f;
-#pragma unroll
-                    for (int j = 0; j < PG_CLUSTER; ++j) top = fmaxf(top, f[j]);
-#pragma unroll
-                    for (int j = 0; j < PG_CLUSTER; ++j) {
-                        f[j] = lj[j] > 0.f ? ex2(f[j] - top) : 0.f;
-                        sum = fmaf(f[j], lj[j], sum);
-                    }
-                    const float inv = sum > 0.f ? 1.0f / sum : 0.f;
-#pragma unroll
-                    for (int j = 0; j < PG_CLUSTER; ++j) f[j] *= inv;
-                    if (x.lse && place != -1)
-                        x.lse[place >= 0 ? place : -2 - place] =
-                            sum > 0.f ? (top + log2f(sum)) * 0.6931471805599453f : place >= 0 ? -INFINITY : 0.f;
-                }
-                float acc[V];
-#pragma unroll
-                for (int e = 0; e < V; ++e) acc[e] = 0.f;
-#pragma unroll
-                for (int j = 0; j < PG_CLUSTER; ++j) {
-                    const float fj = __shfl_sync(0xffffffffu, f[j], i);
-                    if (j < x.nchunk && fj > 0.f)                // (nothing seen there: O may be anything)
-#pragma unroll
-                        for (int e = 0; e < V; ++e) acc[e] = fmaf(fj, o[j][e], acc[e]);
-                }
-                const int to = __shfl_sync(0xffffffffu, place, i);
-                uint32_t* dst = reinterpret_cast<uint32_t*>(x.out + size_t(to >= 0 ? to : -2 - to) * D) + lane * (V / 2);
-#pragma unroll
-                for (int e = 0; e < V / 2; ++e) dst[e] = pack2(acc[2 * e], acc[2 * e + 1]);
-            }
+            paged_merge<D>(x, ob, L::PITCH, ml, places, NT * PG_BM, chunk, warp - 4, 4 * NT);
             __syncwarp();
             cluster_sync();                                      // (no CTA leaves while its rows are read)
         } else {
@@ -730,7 +654,21 @@ static PgPlan paged_plan(const PagedArgs& a) {
     const int64_t blocks = (((int64_t(a.max_pages) << a.log2_page)) + PG_BN - 1) / PG_BN;
     p.nt = 1, p.nchunk = 1;
     double best = 1e300;
-    for (int nt = 1; nt <= (p.tiles > 1 ? 2 : 1) && heads > 0; ++nt) {
+    if (a.S * grp <= 16) {
+        p.few = true, p.tt = a.S;
+        const int64_t sms = num_sms();
+        const double tile = 2.0 * PG_BN * a.D * 2 * double(sms) / 6.5e6;   // us to stream a block into one SM
+        for (int64_t n = 1; n <= blocks && n <= 64 && heads > 0; ++n) {
+            const double per = double((blocks + n - 1) / n), load = double(heads * n) / double(sms);
+            auto consider = [&](double t, bool cluster) {
+                if (t < best) best = t, p.nchunk = int(n), p.cluster = cluster;
+            };
+            const double cta = 3.0 + per * fmax(0.7, tile * fmin(load, 2.0));
+            consider(cta * (1.0 + fmax(load / 2.0 - 1.0, 0.0)) + (n > 1 ? 4.0 : 0.0), false);
+            if (n > 1 && n <= PG_CLUSTER && heads * n <= sms) consider(cta + 2.0, true);
+        }
+    }
+    for (int nt = 1; !p.few && nt <= (p.tiles > 1 ? 2 : 1) && heads > 0; ++nt) {
         const int64_t base = heads * ((p.tiles + nt - 1) / nt), slots = int64_t(num_sms()) * (nt == 1 ? 2 : 1);
         const int64_t most = slots / base > 16 ? slots / base : 16;
         for (int64_t n = 1; n <= blocks && n <= most; ++n) {
@@ -804,6 +742,7 @@ int launch_paged_attention(const PagedArgs& a, const void* q, float scale, void*
     PgArgs x{a, a.Hq / a.Hkv, p.tt, p.tiles, p.nchunk, p.rows, scale * LOG2E, static_cast<bf16_t*>(out), lse,
              reinterpret_cast<float*>(w), reinterpret_cast<float2*>(w + p.part_ml)};
     auto run = [&](auto two, auto one, auto cluster) {
+        if (p.few) return launch_paged_few(x, p.cluster, tq, tk, tv, stream);
         return (p.nt == 2 ? two : p.cluster ? cluster : one)(tq, tk, tv, x, stream);
     };
     const int e = a.D == 64 ? run(launch_attn_t<64, 2, 8>, launch_attn_t<64, 1, 4>, launch_attn_t<64, 1, 4, true>)

@@ -24,7 +24,7 @@ __device__ __forceinline__ uint64_t desc_sw128_kmajor(uint32_t smem_addr) {
     return DESC_SW128_KMAJOR | uint64_t((smem_addr >> 4) & 0x3fffu);  // start address
 }
 
-// MN-major B operand staged with 128-byte swizzle: K rows of 64 bf16 (128 B) along N,
+// MN-major operand (said for B) staged with 128-byte swizzle: K rows of 64 bf16 (128 B) along N,
 // 8-row groups 1024 B apart; `lead` bytes lead to the next 64 of N. Moving 16 rows
 // along K adds 128 to the encoded start address.
 __host__ __device__ constexpr uint64_t desc_sw128_mnmajor_base(uint32_t lead) {  // (start address: low 14 bits)
@@ -32,7 +32,11 @@ __host__ __device__ constexpr uint64_t desc_sw128_mnmajor_base(uint32_t lead) { 
            | (uint64_t(1024u >> 4) << 32)           // stride byte offset: 8 rows of K
            | (uint64_t(1u) << 46) | (uint64_t(2u) << 61);
 }
-constexpr uint32_t IDESC_B_MNMAJOR = 1u << 16;          // added to idesc_bf16_f32
+constexpr uint32_t IDESC_A_MNMAJOR = 1u << 15, IDESC_B_MNMAJOR = 1u << 16;  // added to idesc_bf16_f32
+// The same for 16 of N with 32-byte swizzle (16-byte halves exchanged in rows 4..7 of 8): K rows of
+// 32 B, 8-row groups 256 B apart. Moving 16 rows along K adds 32 to the encoded start address.
+constexpr uint64_t DESC_SW32_MNMAJOR = (uint64_t(256u >> 4) << 16) | (uint64_t(256u >> 4) << 32) |
+                                       (uint64_t(1u) << 46) | (uint64_t(6u) << 61);
 
 // Instruction descriptor, kind::f16: bf16 A and B (K-major), fp32 accumulate.
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
