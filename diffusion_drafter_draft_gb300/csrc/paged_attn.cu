@@ -64,7 +64,7 @@ struct PgSmem {
 
 struct PgPlan {
     int tt, tiles, nt, nchunk, rows;  // tokens per tile, tiles, tiles per CTA, chunks, rows kept per partial tile
-    bool cluster, few;                // the chunks merge through shared memory; at most 16 rows
+    bool cluster, few, alone;         // the chunks merge through shared memory; at most 16 rows; a CTA per SM
     size_t part_o, part_ml, total;    // workspace (partials): offsets and bytes
 };
 
@@ -654,19 +654,27 @@ static PgPlan paged_plan(const PagedArgs& a) {
     const int64_t blocks = (((int64_t(a.max_pages) << a.log2_page)) + PG_BN - 1) / PG_BN;
     p.nt = 1, p.nchunk = 1;
     double best = 1e300;
+    // whether clusters of n all run at once: each of the eight groups of SMs may have n - 1 places over
+    auto fits = [](int64_t ctas, int64_t n, int64_t slots) { return n <= PG_CLUSTER && ctas <= slots - 8 * (n - 1); };
     if (a.S * grp <= 16) {
         p.few = true, p.tt = a.S;
         const int64_t sms = num_sms();
-        const double tile = 2.0 * PG_BN * a.D * 2 * double(sms) / 6.5e6;   // us to stream a block into one SM
+        // In us: start and end of a CTA 3, a block 0.9 alone on its SM and 1.25 beside another, or its share of
+        // the memory (a wave of two per SM; the last one's part); a second launch 4.5, the merge in a
+        // cluster 2. (Equal clusters: the more chunks, since requests may be shorter than their tables.)
+        const double tile = 2.0 * PG_BN * a.D * 2 * double(sms) / 6.7e6;   // a block per SM, at the memory's rate
         for (int64_t n = 1; n <= blocks && n <= 64 && heads > 0; ++n) {
             const double per = double((blocks + n - 1) / n), load = double(heads * n) / double(sms);
-            auto consider = [&](double t, bool cluster) {
-                if (t < best) best = t, p.nchunk = int(n), p.cluster = cluster;
-            };
-            const double cta = 3.0 + per * fmax(0.7, tile * fmin(load, 2.0));
-            consider(cta * (1.0 + fmax(load / 2.0 - 1.0, 0.0)) + (n > 1 ? 4.0 : 0.0), false);
-            if (n > 1 && n <= PG_CLUSTER && heads * n <= sms) consider(cta + 2.0, true);
+            const double waves = floor(load / 2.0), rest = load - 2.0 * waves;
+            const double shared = double(heads) * double(blocks) * tile / double(sms);
+            double t = n > 1 ? 4.5 : 0.0;
+            if (load <= 2.0) t += 3.0 + fmax(per * (load <= 1.0 ? 0.9 : 1.25), shared);
+            else t += waves * (3.0 + per * 2.0 * tile) + (rest > 0.0 ? 3.0 + per * fmax(1.25, rest * tile) : 0.0);
+            if (t < best) best = t, p.nchunk = int(n), p.cluster = false;
+            const double tc = 5.0 + fmax(per * 0.9, shared);
+            if (n > 1 && fits(heads * n, n, sms) && tc <= best) best = tc, p.nchunk = int(n), p.cluster = true;
         }
+        p.alone = heads * p.nchunk <= sms;
     }
     for (int nt = 1; !p.few && nt <= (p.tiles > 1 ? 2 : 1) && heads > 0; ++nt) {
         const int64_t base = heads * ((p.tiles + nt - 1) / nt), slots = int64_t(num_sms()) * (nt == 1 ? 2 : 1);
@@ -683,7 +691,7 @@ static PgPlan paged_plan(const PagedArgs& a) {
             }
             consider(run + 1.5 * nt * p.rows / PG_BM,
                      4.0 + double(heads) * p.tiles * double(n) * p.rows * a.D * 4.0 / 1e7, false);
-            if (nt == 1 && n <= PG_CLUSTER && base * n <= slots) consider(run + 1.0 * p.rows / PG_BM, 1.5, true);
+            if (nt == 1 && fits(base * n, n, slots)) consider(run + 1.0 * p.rows / PG_BM, 1.5, true);
         }
     }
     if (p.nchunk > 1 && !p.cluster) {
@@ -742,7 +750,7 @@ int launch_paged_attention(const PagedArgs& a, const void* q, float scale, void*
     PgArgs x{a, a.Hq / a.Hkv, p.tt, p.tiles, p.nchunk, p.rows, scale * LOG2E, static_cast<bf16_t*>(out), lse,
              reinterpret_cast<float*>(w), reinterpret_cast<float2*>(w + p.part_ml)};
     auto run = [&](auto two, auto one, auto cluster) {
-        if (p.few) return launch_paged_few(x, p.cluster, tq, tk, tv, stream);
+        if (p.few) return launch_paged_few(x, p.cluster, p.alone, tq, tk, tv, stream);
         return (p.nt == 2 ? two : p.cluster ? cluster : one)(tq, tk, tv, x, stream);
     };
     const int e = a.D == 64 ? run(launch_attn_t<64, 2, 8>, launch_attn_t<64, 1, 4>, launch_attn_t<64, 1, 4, true>)

@@ -98,7 +98,7 @@ __device__ __forceinline__ void paged_merge(const PgArgs& x, const float* ob, in
 }
 
 // Few rows (paged_few.cu): tiles of 16 rows, one per request and key/value head.
-int launch_paged_few(const PgArgs& x, bool cluster, const CUtensorMap& tq, const CUtensorMap& tk,
-                     const CUtensorMap& tv, cudaStream_t stream);
+int launch_paged_few(const PgArgs& x, bool cluster, bool alone, const CUtensorMap& tq,
+                     const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream);
 
 }  // namespace dartree

@@ -438,14 +438,15 @@ static int launch_few_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
     return cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, x) == cudaSuccess ? DARTREE_OK : DARTREE_ECUDA;
 }
 
-// Alone on its SM (a cluster: few CTAs) a CTA has room for three blocks' keys and values, else two
-// CTAs share the SM with three tiles of 128 x 128 each.
-int launch_paged_few(const PgArgs& x, bool cluster, const CUtensorMap& tq, const CUtensorMap& tk,
+// Alone on its SM a CTA has room for three blocks' keys and values (heads of 64: six), else two share the SM with half of that.
+int launch_paged_few(const PgArgs& x, bool cluster, bool alone, const CUtensorMap& tq, const CUtensorMap& tk,
                      const CUtensorMap& tv, cudaStream_t stream) {
     if (x.a.D == 64)
-        return cluster ? launch_few_t<64, 6, true>(tq, tk, tv, x, stream)
+        return cluster ? launch_few_t<64, 12, true>(tq, tk, tv, x, stream)
+               : alone ? launch_few_t<64, 12, false>(tq, tk, tv, x, stream)
                        : launch_few_t<64, 6, false>(tq, tk, tv, x, stream);
     return cluster ? launch_few_t<128, 6, true>(tq, tk, tv, x, stream)
+           : alone ? launch_few_t<128, 6, false>(tq, tk, tv, x, stream)
                    : launch_few_t<128, 3, false>(tq, tk, tv, x, stream);
 }
 
