@@ -169,6 +169,18 @@ ATTN = [
     dict(new=[20, 11], old=[6000, 3000], tree=True, S=20, Hq=4, Hkv=1, page=64),
     dict(new=[2, 0, 1], old=[7000, 10, 130], Hq=8, Hkv=1, D=64, page=256, pad=(1, 2)),
     dict(new=[3], old=[70000], Hq=4, Hkv=1, D=64, page=256),
+    # at most 16 rows of a key/value head: causal and tree masks inside them, empty requests, both head sizes
+    dict(new=[4, 0, 2, 3], old=[700, 5, 0, 127], Hq=8, Hkv=2, page=32, pad=(3, 2)),
+    dict(new=[16, 3, 0], old=[250, 1000, 4], S=16, Hq=2, Hkv=2, D=64, tree=True),
+    dict(new=[8, 8], old=[120, 1], Hq=4, Hkv=2, page=16, ragged=False, spare=2000),
+    dict(new=[2], old=[9000], Hq=16, Hkv=2, D=64, page=128, ragged=False),
+    dict(new=[1], old=[4000], Hq=16, Hkv=1, page=16, ragged=False),
+    dict(new=[5], old=[0], Hq=3, Hkv=1, D=64, page=256),
+    dict(new=[1] * 40, old=[37 * c for c in range(40)], Hq=16, Hkv=8, D=64, page=32, ragged=False),
+    dict(new=[1, 2] * 10, old=[100 * c for c in range(20)], Hq=8, Hkv=8, page=64),
+    # single tokens of more heads than that
+    dict(new=[1, 1], old=[3000, 50], Hq=32, Hkv=1, page=64, ragged=False),
+    dict(new=[1] * 20, old=[60 * c for c in range(20)], Hq=68, Hkv=4, D=64, page=16, ragged=False),
 ]
 
 
@@ -260,6 +272,81 @@ def test_attention_a_key_far_above_the_others(dd, at):
     out = x.cache.attention(x.q, lse=lse)
     x.ok()
     _check_attention(x, out, lse)
+
+
+# one request (its blocks spread over a cluster), a batch (a CTA has all of a head's blocks)
+FEW = [dict(new=[1], old=[1500], Hq=4, Hkv=1), dict(new=[2] * 22, old=[1400 - 3 * c for c in range(22)], Hq=16, Hkv=8),
+       dict(new=[3], old=[1100], Hq=8, Hkv=2, D=64), dict(new=[1] * 40, old=[900] * 40, Hq=8, Hkv=8, D=64)]
+
+
+@pytest.mark.parametrize("i", range(len(FEW)))
+@pytest.mark.parametrize("fall", [False, True])
+def test_few_rows_maximum_that_keeps_growing(dd, i, fall):
+    """Scores that rise (or fall) block by block, by more than the weights may carry."""
+    x = Case(dd, page=32, seed=130 + i, **FEW[i]).fill()
+    for c in range(x.C):
+        n = x.old[c] + x.new[c]
+        p, r = op.place(x.np_table, c, np.arange(n), x.page)
+        ramp = torch.linspace(-1, 1, n, device="cuda")[:, None, None] * (-6 if fall else 6)
+        x.k[torch.from_numpy(p.astype(np.int64)).cuda(), :, torch.from_numpy(r).cuda()] = \
+            (x.rand(n, x.Hkv, x.D).float() * 0.2 + ramp).to(torch.bfloat16)
+    x.q.copy_((x.q.float() * 0.2 + 1).to(torch.bfloat16))
+    lse = torch.empty(x.T, x.Hq, device="cuda")
+    out = x.cache.attention(x.q, lse=lse)
+    x.ok()
+    _check_attention(x, out, lse)
+
+
+@pytest.mark.parametrize("i", range(len(FEW)))
+@pytest.mark.parametrize("at", [0, 127, 128, 500, 895])
+def test_few_rows_a_key_far_above_the_others(dd, i, at):
+    x = Case(dd, page=64, seed=140 + at, **FEW[i]).fill()
+    x.q.copy_((x.q.float() * 0.1 + 1).to(torch.bfloat16))
+    for c in range(x.C):
+        p, r = op.place(x.np_table, c, [at], x.page)
+        x.k[int(p[0]), :, int(r[0])] = 9.0
+    lse = torch.empty(x.T, x.Hq, device="cuda")
+    out = x.cache.attention(x.q, lse=lse)
+    x.ok()
+    _check_attention(x, out, lse)
+
+
+@pytest.mark.parametrize("scale,scaleq", [(1.0, 8.0), (0.02, 1.0)])
+def test_few_rows_scales(dd, scale, scaleq):
+    x = Case(dd, [3, 1], [900, 64], Hq=8, Hkv=2, seed=151, scaleq=scaleq).fill()
+    lse = torch.empty(x.T, x.Hq, device="cuda")
+    out = x.cache.attention(x.q, scale=scale, lse=lse)
+    x.ok()
+    _check_attention(x, out, lse, scale=scale)
+
+
+def test_few_rows_that_see_nothing_for_a_block(dd):
+    """Tree slots whose mask is empty, without a context and behind one, in batches small and large."""
+    for C in (1, 90):
+        x = Case(dd, [6] * C, [0, 130][:C] + [0] * (C - 2), S=6, tree=True, seed=153).fill()
+        for m in x.masks:
+            m[3] = 0
+            m[5, :5] = 0
+        x.tree["mask"] = torch.from_numpy(np.stack(x.masks)).cuda()
+        lse = torch.empty(x.T, x.Hq, device="cuda")
+        out = x.cache.attention(x.q, tree=x.tree, lse=lse)
+        x.ok()
+        _check_attention(x, out, lse)
+        assert (out[3] == 0).all() and torch.isinf(lse[3]).all()
+
+
+def test_equal_inputs_give_equal_outputs(dd):
+    """Every way the chunks are merged, called again and again."""
+    for kw in (FEW[0], FEW[1], dict(new=[1], old=[9000], Hq=4, Hkv=1), dict(new=[20], old=[2000], Hq=8, Hkv=2),
+               dict(new=[300], old=[700], Hq=8, Hkv=2)):
+        x = Case(dd, page=64, seed=157, **kw).fill()
+        lse = torch.empty(x.T, x.Hq, device="cuda")
+        want = x.cache.attention(x.q, lse=lse).clone()
+        want_lse = lse.clone()
+        for _ in range(20):
+            lse.fill_(7.0)
+            assert torch.equal(x.cache.attention(x.q, lse=lse), want) and torch.equal(lse, want_lse)
+        x.ok()
 
 
 # ------------------------------------------------------------------------------ append
@@ -564,6 +651,33 @@ def test_lengths_that_do_not_fit_are_reported(dd):
     x.q_start.copy_(was)
     x.cache.append(x.q, k, v)
     assert _status(dd, x) == 0
+
+
+@pytest.mark.parametrize("Hq", [4, 64, 200])   # rows of a head: few, two tiles, four
+def test_attention_of_bad_tables_and_lengths(dd, Hq):
+    x = Case(dd, [3, 4], [40, 300], Hq=Hq, seed=85).fill()
+    lse = torch.empty(x.T, x.Hq, device="cuda")
+    good = int(x.table[0, 1])
+    for bad in (-1, 10 ** 6, 2 ** 31 - 1, -2 ** 31):
+        x.table[0, 1] = bad
+        out = x.cache.attention(x.q, lse=lse)
+        assert _status(dd, x) == dd.EINTERNAL
+        assert torch.isfinite(out.float()).all()
+    x.table[0, 1] = good
+    for ctx in (x.cache.rows - 1, x.cache.rows + 5, -1, 2 ** 31 - 1, -2 ** 31):
+        x.n_ctx[0] = ctx
+        x.cache.attention(x.q)
+        assert _status(dd, x) == dd.EINTERNAL
+    x.n_ctx[0] = 40
+    was = x.q_start.clone()
+    for st in ([0, 9, 8], [-3, 3, 7], [0, 3, 50], [5, 2, 7], [2 ** 31 - 1, -2 ** 31, 7]):
+        x.q_start.copy_(torch.tensor(st, dtype=torch.int32))
+        x.cache.attention(x.q)
+        assert _status(dd, x) == dd.EINTERNAL
+    x.q_start.copy_(was)
+    out = x.cache.attention(x.q, lse=lse)
+    x.ok()
+    _check_attention(x, out, lse)
 
 
 def test_paths_that_name_no_slot_are_reported(dd):
