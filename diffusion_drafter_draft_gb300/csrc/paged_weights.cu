@@ -14,8 +14,8 @@
 //   warp 1      issues S^T into one of two tensor-memory buffers
 //   warps 2..9  two groups of 128 threads, one per buffer: while one adds up a tile the
 //               other's is formed; the groups' sums of a block meet in shared memory
-// Single tokens are bound by reading the keys once (16 tokens over 4096-8192 rows: 42 us,
-// 5.0 TB/s); chunks by the sums, an exponential per score and ~4.5 instructions (two chunks
+// Single tokens are bound by reading the keys once (16 tokens over 4096-8192 rows: 39 us,
+// 5.4 TB/s); chunks by the sums, an exponential per score and ~4.5 instructions (two chunks
 // of 256-511 tokens over 4000-8000 rows, 16/4 heads of 64: 32 us, the exponentials alone 12).
 // Every mbarrier wait is bounded; one that runs out records DARTREE_ETIMEOUT.
 #include <cuda.h>
@@ -371,18 +371,25 @@ int launch_paged_weights(const PagedArgs& a, const void* q, const float* lse, fl
     x.tiles = (a.S + x.tt - 1) / x.tt;
     const int64_t heads = int64_t(a.C) * a.Hkv;
     const int64_t blocks = ((int64_t(a.max_pages) << a.log2_page) + PW_BM - 1) / PW_BM;
-    // Chunks of key blocks: the least of (all CTAs' time / CTAs in flight + one CTA's time), which
-    // bounds any order of CTAs of different lengths. One query tile: in block times of reading keys
-    // (two CTAs an SM), a CTA's start and end counted as eight; more: in tiles (an SM's CTAs share its
-    // arithmetic), counted as six.
+    // Chunks of key blocks. More query tiles than one, in tiles (an SM's CTAs share its arithmetic; a CTA's
+    // start and end counted as six): the least of (all CTAs' time / SMs + one CTA's time), which bounds any
+    // order of CTAs of different lengths. One query tile, in us: start and end of a CTA 2, a block 0.56 alone
+    // on its SM and 0.75 beside another, or its share of the memory (a wave of two per SM; the last one's
+    // part). Of equals the more chunks, since requests may be shorter than their tables: 16 requests of 8192
+    // rows, 8 heads: two chunks 43.0 us, one 49.5, five 51.1.
     const int64_t sms = num_sms(), most = 4 * sms / heads > 64 ? 4 * sms / heads : 64;
+    const double tile = double(PW_BM) * a.D * 2 * double(sms) / 6.7e6;     // a block per SM, at the memory's rate
+    const double shared = double(heads) * double(blocks) * tile / double(sms);
     double best = 1e300;
     x.nchunk = 1;
     for (int64_t n = 1; n <= blocks && n <= most; ++n) {
-        const int64_t per = (blocks + n - 1) / n;
-        const double cta = x.tiles == 1 ? double(per + 8) : double(per * x.tiles + 6);
-        const double t = double(heads * n) * cta / double(x.tiles == 1 ? 2 * sms : sms) + cta;
-        if (t < best) best = t, x.nchunk = int(n);
+        const double per = double((blocks + n - 1) / n), load = double(heads * n) / double(sms);
+        const double waves = floor(load / 2.0), rest = load - 2.0 * waves, cta = per * x.tiles + 6.0;
+        double t;
+        if (x.tiles > 1) t = load * cta + cta;
+        else if (load <= 2.0) t = 2.0 + fmax(per * (load <= 1.0 ? 0.56 : 0.75), shared);
+        else t = waves * (2.0 + per * 2.0 * tile) + (rest > 0.0 ? 2.0 + per * fmax(0.75, rest * tile) : 0.0);
+        if (x.tiles > 1 ? t < best : t <= best) best = t, x.nchunk = int(n);
     }
     CUtensorMap tq, tk;
     // (a batch without tokens has no queries: its map is never used)
