@@ -28,8 +28,9 @@
 // their partial rows go through memory to a second launch.
 //
 // Long chunks are bound by the tensor cores (8192 tokens over 8192 rows, 32/8 heads of 128:
-// 1.0 ms, 1.66 PFLOP/s), single tokens by reading the cache once (64 tokens over 4096-8192
-// rows: 261 us, 6.2 TB/s), few rows by latency (one token over 2048 rows: 10.7 us).
+// 1.0 ms, 1.66 PFLOP/s), trees by the chain of a block (scores, weights, product: ~1.6 us) and the
+// merge (four trees of 65 slots over 1024-2048 rows: 26.4 us). At most 16 rows of a key/value head
+// (single tokens) have a kernel of their own, paged_few.cu.
 // Every mbarrier wait is bounded; one that runs out records DARTREE_ETIMEOUT.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -64,7 +65,7 @@ struct PgSmem {
 
 struct PgPlan {
     int tt, tiles, nt, nchunk, rows;  // tokens per tile, tiles, tiles per CTA, chunks, rows kept per partial tile
-    bool cluster, few, alone;         // the chunks merge through shared memory; at most 16 rows; a CTA per SM
+    bool cluster, few, alone;         // the chunks merge through shared memory; at most 16 rows; a CTA per SM and tile
     size_t part_o, part_ml, total;    // workspace (partials): offsets and bytes
 };
 
@@ -114,11 +115,12 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
     griddep_launch_dependents();
     griddep_wait();
 
-    // the last tiles (the most keys of a causal batch) first
+    // the last tiles (the most keys of a causal batch) first, of all heads or (x.inner) head by head
     const int ntile = (x.tiles + NT - 1) / NT;
     const int chunk = int(blockIdx.x % x.nchunk);
-    const unsigned rest = blockIdx.x / x.nchunk;
-    const int heads = a.C * a.Hkv, cg = int(rest % heads), tp = ntile - 1 - int(rest / heads);
+    const unsigned rest = blockIdx.x / x.nchunk, heads = a.C * a.Hkv, in = x.inner ? ntile : heads;
+    const int high = int(rest / in), low = int(rest - high * in);
+    const int cg = x.inner ? high : low, tp = ntile - 1 - (x.inner ? low : high);
     const int c = cg / a.Hkv, g = cg - c * a.Hkv;
     bool bad;
     const PagedRequest r = paged_request(a, c, bad);
@@ -636,14 +638,14 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
 
 // ----------------------------------------------------------------------------- host
 
-// Tiles per CTA and chunks of a tile's key blocks: the least of (all CTAs' time / CTAs in
-// flight + one CTA's time), which bounds any order of CTAs of different lengths. In units
-// of a block's time (~1.6 us at D = 128): a block 1 (two tiles, one CTA an SM) or 1.15
-// (two CTAs of one tile, each reading the block), a CTA's start and end 2. Merging through
-// memory: 1.5 for a whole tile's partial result, 4 for the second launch, and the bytes;
-// within a cluster of one-tile CTAs, 1 for a whole tile and 1.5, where all CTAs run at
-// once (in several waves the CTAs that wait for their cluster's last hold up the next:
-// 64 tokens over 6144 rows 293 us in clusters, 261 us through memory).
+// Tiles per CTA and chunks of a tile's key blocks: the least time, in us, fitted to sweeps of
+// 18 shapes with caches that were not in the L2. A CTA's start and end, then a block: two
+// tiles 6 and 1.7 (D = 128); one tile beside another CTA, with a ring of one block, 5 and
+// 2.5; alone on its SM with two and a half blocks in flight 4 and 1.55 (both less where many
+// tiles read the same keys). Merging in a cluster, where all CTAs run at once, 2 and 3 for
+// a whole tile; through memory 6 and the partial results' bytes at 4 TB/s.
+// Against the best of all ways: one tree of 65 slots over 2048 rows 18.9 -> 13.9 us with
+// CTAs alone, 16 over 4096 rows 120 us with two tiles a CTA (169 with one).
 static PgPlan paged_plan(const PagedArgs& a) {
     PgPlan p{};
     const int grp = a.Hq / a.Hkv;
@@ -676,22 +678,24 @@ static PgPlan paged_plan(const PagedArgs& a) {
         }
         p.alone = heads * p.nchunk <= sms;
     }
-    for (int nt = 1; !p.few && nt <= (p.tiles > 1 ? 2 : 1) && heads > 0; ++nt) {
-        const int64_t base = heads * ((p.tiles + nt - 1) / nt), slots = int64_t(num_sms()) * (nt == 1 ? 2 : 1);
+    const double shared = double(heads) * double(blocks) * 4.0 * PG_BN * a.D / 6.7e6;   // the memory's share
+    for (int way = 0; way < 3 && heads > 0 && !p.few; ++way) {
+        if (way == 2 && p.tiles == 1) break;
+        const int nt = way == 2 ? 2 : 1;
+        const bool alone = way == 1, many = p.tiles >= 4;
+        const int64_t base = heads * ((p.tiles + nt - 1) / nt), slots = int64_t(num_sms()) * (way == 0 ? 2 : 1);
+        const double ends = way == 0 ? 5.0 : alone ? 4.0 : 6.0;
+        const double block = a.D == 128 ? (way == 0 ? (many ? 2.1 : 2.5) : alone ? (many ? 1.36 : 1.55) : 1.7)
+                                        : (way == 0 ? 1.4 : alone ? 1.5 : 1.45);
         const int64_t most = slots / base > 16 ? slots / base : 16;
         for (int64_t n = 1; n <= blocks && n <= most; ++n) {
-            const double run = double((blocks + n - 1) / n) * (nt == 1 ? 1.15 : 1.0) + 2.0;
-            auto consider = [&](double cta, double merge, bool cluster) {
-                const double t = double(base * n) * cta / double(slots) + cta + merge;
-                if (t < best) best = t, p.nt = nt, p.nchunk = int(n), p.cluster = cluster;
-            };
-            if (n == 1) {
-                consider(run, 0.0, false);
-                continue;
-            }
-            consider(run + 1.5 * nt * p.rows / PG_BM,
-                     4.0 + double(heads) * p.tiles * double(n) * p.rows * a.D * 4.0 / 1e7, false);
-            if (nt == 1 && fits(base * n, n, slots)) consider(run + 1.0 * p.rows / PG_BM, 1.5, true);
+            const double load = double(base * n) / double(slots);
+            const double waves = load <= 1.0 ? 1.0 : load < 3.0 ? ceil(load) : load + 0.5;
+            const bool cluster = n > 1 && nt == 1 && fits(base * n, n, slots);
+            const double merge = n == 1 ? 0.0 : cluster ? 2.0 + 3.0 * p.rows / PG_BM
+                                 : 6.0 + double(heads) * p.tiles * double(n) * p.rows * a.D * 8.0 / 4e6;
+            const double t = fmax(waves * (ends + block * double((blocks + n - 1) / n)), shared + 3.0) + merge;
+            if (t < best) best = t, p.nt = nt, p.nchunk = int(n), p.cluster = cluster, p.alone = alone;
         }
     }
     if (p.nchunk > 1 && !p.cluster) {
@@ -747,14 +751,26 @@ int launch_paged_attention(const PagedArgs& a, const void* q, float scale, void*
     if (!make_query_map(&tq, a, q, p.tt) || !make_page_map(&tk, a, a.k) || !make_page_map(&tv, a, a.v))
         return DARTREE_ECUDA;
     uint8_t* w = static_cast<uint8_t*>(part);
-    PgArgs x{a, a.Hq / a.Hkv, p.tt, p.tiles, p.nchunk, p.rows, scale * LOG2E, static_cast<bf16_t*>(out), lse,
+    // Tiles of nearly the same length (few new tokens beside the table's rows) follow one another head by
+    // head and find their keys and values in the L2 (16 trees of 65 slots over 4096 rows, three tiles: 170 us
+    // against 197); tiles of very different lengths go by length, the longest first. (Not for a grid that runs
+    // at once: 28 against 27 us for four trees over 2048 rows.)
+    const int64_t ctas = int64_t(a.C) * a.Hkv * ((p.tiles + p.nt - 1) / p.nt) * p.nchunk;
+    const bool inner = 4 * int64_t(a.S) <= int64_t(a.max_pages) << a.log2_page &&
+                       ctas > num_sms() * (p.nt == 1 && !p.alone ? 2 : 1);
+    PgArgs x{a, a.Hq / a.Hkv, p.tt, p.tiles, p.nchunk, p.rows, inner, scale * LOG2E, static_cast<bf16_t*>(out), lse,
              reinterpret_cast<float*>(w), reinterpret_cast<float2*>(w + p.part_ml)};
-    auto run = [&](auto two, auto one, auto cluster) {
-        if (p.few) return launch_paged_few(x, p.cluster, p.alone, tq, tk, tv, stream);
-        return (p.nt == 2 ? two : p.cluster ? cluster : one)(tq, tk, tv, x, stream);
-    };
-    const int e = a.D == 64 ? run(launch_attn_t<64, 2, 8>, launch_attn_t<64, 1, 4>, launch_attn_t<64, 1, 4, true>)
-                            : run(launch_attn_t<128, 2, 5>, launch_attn_t<128, 1, 2>, launch_attn_t<128, 1, 2, true>);
+    int e;
+    if (p.few)
+        e = launch_paged_few(x, p.cluster, p.alone, tq, tk, tv, stream);
+    else if (a.D == 64)
+        e = (p.nt == 2 ? launch_attn_t<64, 2, 8>
+             : p.alone ? (p.cluster ? launch_attn_t<64, 1, 8, true> : launch_attn_t<64, 1, 8>)
+                       : (p.cluster ? launch_attn_t<64, 1, 4, true> : launch_attn_t<64, 1, 4>))(tq, tk, tv, x, stream);
+    else
+        e = (p.nt == 2 ? launch_attn_t<128, 2, 5>
+             : p.alone ? (p.cluster ? launch_attn_t<128, 1, 5, true> : launch_attn_t<128, 1, 5>)
+                       : (p.cluster ? launch_attn_t<128, 1, 2, true> : launch_attn_t<128, 1, 2>))(tq, tk, tv, x, stream);
     if (e != DARTREE_OK || p.nchunk == 1 || p.cluster) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned((size_t(a.C) * a.S * a.Hq + 7) / 8));

@@ -17,6 +17,7 @@ constexpr int PG_CLUSTER = 8;         // chunks that merge through shared memory
 struct PgArgs {
     PagedArgs a;
     int grp, tt, tiles, nchunk, rows;
+    int inner;                        // a head's tiles follow one another
     float sl2;                        // scale * log2(e)
     bf16_t* out;
     float* lse;

@@ -178,6 +178,11 @@ ATTN = [
     dict(new=[5], old=[0], Hq=3, Hkv=1, D=64, page=256),
     dict(new=[1] * 40, old=[37 * c for c in range(40)], Hq=16, Hkv=8, D=64, page=32, ragged=False),
     dict(new=[1, 2] * 10, old=[100 * c for c in range(20)], Hq=8, Hkv=8, page=64),
+    # several tiles of many heads, more CTAs than run at once; a tile alone on its SM
+    dict(new=[65] * 20, old=[45 * c for c in range(20)], tree=True, Hq=16, Hkv=8, page=64),
+    dict(new=[130] * 22, old=[600 - 20 * c for c in range(22)], Hq=8, Hkv=8, D=64, page=32, spare=100),
+    dict(new=[100], old=[100], Hq=32, Hkv=8, page=16, ragged=False),
+    dict(new=[17, 9], old=[500, 333], S=17, tree=True, Hq=16, Hkv=2, D=64, page=16),
     # single tokens of more heads than that
     dict(new=[1, 1], old=[3000, 50], Hq=32, Hkv=1, page=64, ragged=False),
     dict(new=[1] * 20, old=[60 * c for c in range(20)], Hq=68, Hkv=4, D=64, page=16, ragged=False),
