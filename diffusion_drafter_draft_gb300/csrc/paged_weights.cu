@@ -265,6 +265,26 @@ __global__ void __launch_bounds__(PW_NT, 2)
                         next_t = first_tile(b + 1) + (((n + ntile - t) & 1) != group ? 1 : 0);
                     if (next_t < ntile) next_lse = lse_of(next_t);
                 }
+                // a tree's new rows: bit i of tok, whether the tile's token i sees this key (a batch of loads is
+                // independent and on its way at once: loads by need took a block of 33 slots 18 us longer)
+                uint32_t tok[4] = {0, 0, 0, 0};
+                const bool tree = a.mask && __any_sync(0xffffffffu, j >= r.n_old);
+                if (tree) {
+                    const int s = j - r.n_old, nt = min(r.n_new - t * x.tt, x.tt);
+                    const uint8_t* row = a.mask + (size_t(c) * a.S + t * x.tt) * a.S + (s >= 0 && s < r.n_new ? s : 0);
+#pragma unroll
+                    for (int w = 0; w < 4; ++w)
+#pragma unroll 1
+                        for (int q = 0; q < 32 && 32 * w + q < nt; q += 8) {
+                            uint8_t m[8];
+#pragma unroll
+                            for (int u = 0; u < 8; ++u) m[u] = row[size_t(min(32 * w + q + u, nt - 1)) * a.S];
+#pragma unroll
+                            for (int u = 0; u < 8; ++u) tok[w] |= m[u] ? 1u << (q + u) : 0u;
+                        }
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) tok[w] = s < 0 ? 0xffffffffu : s < r.n_new ? tok[w] : 0u;
+                }
                 ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&sfull[group], uint32_t(n >> 1) & 1u, a.status));
                 if (ok) {
                     tc::fence_after_sync();
@@ -287,7 +307,7 @@ __global__ void __launch_bounds__(PW_NT, 2)
                         }
                     };
                     // hidden columns get a score of -inf (what lies behind the last token may be anything)
-                    if (__all_sync(0xffffffffu, cols == 128 && from <= 0 && !(a.mask && s >= 0))) {
+                    if (__all_sync(0xffffffffu, cols == 128 && from <= 0 && !tree)) {
 #pragma unroll
                         for (int c0 = 0; c0 < 128; c0 += 32) {
                             uint32_t v[32];
@@ -295,7 +315,7 @@ __global__ void __launch_bounds__(PW_NT, 2)
                             add(v, c0);
                             add(v + 16, c0 + 16);
                         }
-                    } else if (__all_sync(0xffffffffu, !(a.mask && s >= 0))) {
+                    } else if (!tree) {
 #pragma unroll 1
                         for (int c0 = 0; c0 < cols; c0 += 16) {
                             uint32_t v[16];
@@ -306,19 +326,20 @@ __global__ void __launch_bounds__(PW_NT, 2)
                             add(v, c0);
                         }
                     } else {
-                        // a tree's rows: token by token (`row`: the mask's byte of this key, if it is a new row's)
-                        const uint8_t* row = a.mask + (size_t(c) * a.S + t0) * a.S + (s >= 0 && s < r.n_new ? s : 0);
-                        int ti = 0, hg = 0;
+                        // a tree's rows: bit i of `see` is token c0 / grp + i's
 #pragma unroll 1
                         for (int c0 = 0; c0 < cols; c0 += 16) {
                             uint32_t v[16];
-                            __syncwarp();
+                            const int ti = c0 / x.grp, w = ti >> 5;
+                            const uint32_t lo = w == 0 ? tok[0] : w == 1 ? tok[1] : w == 2 ? tok[2] : tok[3];
+                            const uint32_t up = w == 0 ? tok[1] : w == 1 ? tok[2] : w == 2 ? tok[3] : 0u;
+                            uint32_t see = __funnelshift_r(lo, up, ti & 31);
+                            int hg = c0 - ti * x.grp;
                             tc::tmem_ld16(trow + uint32_t(c0), v);
 #pragma unroll
                             for (int e = 0; e < 16; ++e) {
-                                const bool seen = c0 + e < cols && (s < 0 || (s < r.n_new && row[size_t(ti) * a.S] != 0));
-                                if (!seen) v[e] = 0xff800000u;
-                                if (++hg == x.grp) hg = 0, ++ti;
+                                if (!(see & 1u) || c0 + e >= cols) v[e] = 0xff800000u;
+                                if (++hg == x.grp) hg = 0, see >>= 1;
                             }
                             add(v, c0);
                         }
@@ -371,26 +392,29 @@ int launch_paged_weights(const PagedArgs& a, const void* q, const float* lse, fl
     x.tiles = (a.S + x.tt - 1) / x.tt;
     const int64_t heads = int64_t(a.C) * a.Hkv;
     const int64_t blocks = ((int64_t(a.max_pages) << a.log2_page) + PW_BM - 1) / PW_BM;
-    // Chunks of key blocks. More query tiles than one, in tiles (an SM's CTAs share its arithmetic; a CTA's
-    // start and end counted as six): the least of (all CTAs' time / SMs + one CTA's time), which bounds any
-    // order of CTAs of different lengths. One query tile, in us: start and end of a CTA 2, a block 0.56 alone
-    // on its SM and 0.75 beside another, or its share of the memory (a wave of two per SM; the last one's
-    // part). Of equals the more chunks, since requests may be shorter than their tables: 16 requests of 8192
-    // rows, 8 heads: two chunks 43.0 us, one 49.5, five 51.1.
+    // Chunks of key blocks, in us. More query tiles than one: two CTAs an SM hardly slow each other, and a CTA
+    // takes 3 and 1.4 (heads of 64: 1.2) for each tile of each of its blocks; so many waves. One query tile: start
+    // and end of a CTA 2, a block 0.56 alone on its SM and 0.75 beside another, or its share of the memory (a
+    // wave of two per SM; the last one's part). Of equals (several tiles: of those within 8 %) the most chunks,
+    // since requests may be shorter than their tables: two chunks of 256-511 tokens, 32 us with 67 chunks and 38
+    // with 34, where equal lengths take 41.8 and 40.3. 16 requests of 8192 rows, 8 heads: two chunks 43.0 us, one
+    // 49.5, five 51.1; 16 trees of 65 slots over 4096 rows: seven 74 us, three 102.
     const int64_t sms = num_sms(), most = 4 * sms / heads > 64 ? 4 * sms / heads : 64;
     const double tile = double(PW_BM) * a.D * 2 * double(sms) / 6.7e6;     // a block per SM, at the memory's rate
     const double shared = double(heads) * double(blocks) * tile / double(sms);
-    double best = 1e300;
-    x.nchunk = 1;
-    for (int64_t n = 1; n <= blocks && n <= most; ++n) {
+    auto time = [&](int64_t n) -> double {
         const double per = double((blocks + n - 1) / n), load = double(heads * n) / double(sms);
-        const double waves = floor(load / 2.0), rest = load - 2.0 * waves, cta = per * x.tiles + 6.0;
-        double t;
-        if (x.tiles > 1) t = load * cta + cta;
-        else if (load <= 2.0) t = 2.0 + fmax(per * (load <= 1.0 ? 0.56 : 0.75), shared);
-        else t = waves * (2.0 + per * 2.0 * tile) + (rest > 0.0 ? 2.0 + per * fmax(0.75, rest * tile) : 0.0);
-        if (x.tiles > 1 ? t < best : t <= best) best = t, x.nchunk = int(n);
-    }
+        const double waves = floor(load / 2.0), rest = load - 2.0 * waves;
+        if (x.tiles > 1)
+            return (load <= 8.0 ? ceil(load / 2.0) : load / 2.0 + 0.5) * (3.0 + per * x.tiles * (a.D == 64 ? 1.2 : 1.4));
+        if (load <= 2.0) return 2.0 + fmax(per * (load <= 1.0 ? 0.56 : 0.75), shared);
+        return waves * (2.0 + per * 2.0 * tile) + (rest > 0.0 ? 2.0 + per * fmax(0.75, rest * tile) : 0.0);
+    };
+    double best = 1e300;
+    for (int64_t n = 1; n <= blocks && n <= most; ++n) best = fmin(best, time(n));
+    x.nchunk = 1;
+    for (int64_t n = 1; n <= blocks && n <= most; ++n)
+        if (time(n) <= best * (x.tiles > 1 ? 1.08 : 1.0)) x.nchunk = int(n);
     CUtensorMap tq, tk;
     // (a batch without tokens has no queries: its map is never used)
     if (!make_query_map(&tq, a, a.T > 0 ? q : a.k, x.tt) || !make_page_map(&tk, a, a.k)) return DARTREE_ECUDA;

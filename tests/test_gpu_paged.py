@@ -431,6 +431,10 @@ WEIGHTS = [
     dict(new=[3, 2], old=[140, 0], Hq=200, Hkv=2, page=16),
     dict(new=[65, 20], old=[200, 7], S=65, tree=True, Hq=8, Hkv=2, page=64, D=64),
     dict(new=[200], old=[0], Hq=4, Hkv=4, ragged=False),
+    # trees: more than 32 slots in a tile, heads that 16 columns do not divide, slots over a block's end
+    dict(new=[100, 40], old=[200, 7], S=100, tree=True, Hq=2, Hkv=2, page=32),
+    dict(new=[50, 33], old=[100, 127], S=50, tree=True, Hq=6, Hkv=2, page=16, D=64),
+    dict(new=[300], old=[90], S=300, tree=True, Hq=1, Hkv=1, page=64),
 ]
 
 
