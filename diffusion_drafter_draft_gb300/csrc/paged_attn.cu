@@ -29,7 +29,7 @@
 //
 // Long chunks are bound by the tensor cores (8192 tokens over 8192 rows, 32/8 heads of 128:
 // 1.0 ms, 1.66 PFLOP/s), trees by the chain of a block (scores, weights, product: ~1.6 us) and the
-// merge (four trees of 65 slots over 1024-2048 rows: 26.4 us). At most 16 rows of a key/value head
+// merge (four trees of 65 slots over 1024-2048 rows: 24.9 us). At most 16 rows of a key/value head
 // (single tokens) have a kernel of their own, paged_few.cu.
 // Every mbarrier wait is bounded; one that runs out records DARTREE_ETIMEOUT.
 #include <cuda.h>
@@ -342,24 +342,23 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
             const int sl = key + lane - r.n_old;
 #pragma unroll
             for (int w = 0; w < 4; ++w) bits[w] = 0;
+            // (every load is in range by its clamped indices and needs no other's outcome: a tree of 64 slots
+            // of one head 15.2 us, 25.0 with loads by need)
             for (int q0 = tok0; q0 <= tok1; q0 += 8) {
-                bool v[8][4];
+                uint8_t v[8][4];
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
-                    const int q = q0 + u, i_q = t0 + t * x.tt + q;
+                    const int i_q = min(t0 + t * x.tt + q0 + u, r.n_new - 1);
                     const uint8_t* mrow = a.mask + (size_t(c) * a.S + i_q) * a.S;
-                    const bool tok = q <= tok1 && q < x.tt && i_q < r.n_new;
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const int j = sl + 32 * w;
-                        v[u][w] = j < 0 || (tok && j < r.n_new && mrow[j] != 0);
-                    }
+                    for (int w = 0; w < 4; ++w) v[u][w] = mrow[min(max(sl + 32 * w, 0), r.n_new - 1)];
                 }
 #pragma unroll
                 for (int u = 0; u < 8; ++u)
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
-                        const uint32_t word = __ballot_sync(0xffffffffu, v[u][w]);
+                        const int j = sl + 32 * w;
+                        const uint32_t word = __ballot_sync(0xffffffffu, j < 0 || (j < r.n_new && v[u][w] != 0));
                         if (q0 + u == ti) bits[w] = word;
                     }
             }

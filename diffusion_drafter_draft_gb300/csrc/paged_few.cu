@@ -222,9 +222,14 @@ __global__ void __launch_bounds__(PF_NT, 2)
                 if (!a.mask) {
                     seen &= ~((1u << s * x.grp) - 1u);               // (s < n_new)
                 } else {
+                    const uint8_t* col = a.mask + size_t(c) * a.S * a.S + s;
+                    uint8_t v[PF_N];
+#pragma unroll
+                    for (int t = 0; t < PF_N; ++t) v[t] = col[size_t(min(t, r.n_new - 1)) * a.S];
                     seen = 0;
-                    for (int t = 0; t < r.n_new; ++t)
-                        if (a.mask[(size_t(c) * a.S + t) * a.S + s]) seen |= head1 << t * x.grp;
+#pragma unroll
+                    for (int t = 0; t < PF_N; ++t)
+                        if (t < r.n_new && v[t]) seen |= head1 << t * x.grp;
                 }
             }
             ok = ok && mbar_wait_bounded(&sfull[i & 1], uint32_t(i >> 1) & 1u, a.status);
