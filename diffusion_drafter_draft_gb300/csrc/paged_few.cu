@@ -262,8 +262,7 @@ __global__ void __launch_bounds__(PF_NT, 2)
                 uint32_t pk[PF_N / 2];
 #pragma unroll
                 for (int n = 0; n < PF_N; ++n) {
-                    const float off = m[n] > -INFINITY ? -m[n] : 1e30f;
-                    p[n] = (seen >> n) & 1u ? ex2(fmaf(__uint_as_float(sc[n]), x.sl2, off)) : 0.f;
+                    p[n] = (seen >> n) & 1u ? ex2(fmaf(__uint_as_float(sc[n]), x.sl2, -m[n])) : 0.f;
                     big = fmaxf(big, p[n]);
                     if (n & 1) pk[n / 2] = pack2(p[n - 1], p[n]);
                 }
