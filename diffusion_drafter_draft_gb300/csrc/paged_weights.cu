@@ -8,7 +8,8 @@
 // a row of its own: no reduction across threads, no atomics, a fixed order of addition.
 //
 // CTA = (chunk of key blocks, (request, key/value head)), over all query tiles of TT
-// tokens x grp heads (columns token * grp + head):
+// tokens x grp heads (columns token * grp + head), or (SPLIT: few key blocks under many
+// query tiles) over a part of them, the parts' CTAs a cluster that adds its sums:
 //   warp 0      producer: key blocks and query tiles by TMA through two rings (a single
 //               query tile is fetched once)
 //   warp 1      issues S^T into one of two tensor-memory buffers
@@ -55,12 +56,13 @@ struct PwSmem {
 struct PwArgs {
     PagedArgs a;
     int grp, tt, tiles, nchunk;
+    int split;                // CTAs of a cluster that share a chunk's query tiles
     float sl2, decay;
     const float* lse;
     float* weights;
 };
 
-template <int D>
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(PW_NT, 2)
     paged_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ PwArgs x) {
@@ -98,7 +100,9 @@ __global__ void __launch_bounds__(PW_NT, 2)
     griddep_launch_dependents();
     griddep_wait();
 
-    const int chunk = int(blockIdx.x % x.nchunk), cg = int(blockIdx.x / x.nchunk);
+    const unsigned split = SPLIT ? x.split : 1u, rest = blockIdx.x / split;
+    const int part = int(blockIdx.x % split);                // (rank in the cluster)
+    const int chunk = int(rest % x.nchunk), cg = int(rest / x.nchunk);
     const int c = cg / a.Hkv, g = cg - c * a.Hkv;
     bool bad;
     const PagedRequest r = paged_request(a, c, bad);
@@ -113,11 +117,17 @@ __global__ void __launch_bounds__(PW_NT, 2)
     uint8_t* const kring = smem;
     uint8_t* const qring = few ? smem + L::FEW_OFF : smem + ks_n * L::TILE;
     const uint32_t qpanel = uint32_t(few ? L::FEW_PANEL : L::PANEL);
-    // the first tile that sees a row of block b
+    // the tiles that see a row of block b, this CTA's part of them
     auto first_tile = [&](int b) -> int {
-        const int ahead = b * PW_BM - r.n_old;
-        return a.mask || ahead <= 0 ? 0 : ahead / x.tt;
+        const int ahead = b * PW_BM - r.n_old, first = a.mask || ahead <= 0 ? 0 : ahead / x.tt;
+        return SPLIT ? first + max(ntile - first, 0) * part / int(split) : first;
     };
+    auto last_tile = [&](int b) -> int {                     // one behind it
+        if (!SPLIT) return ntile;
+        const int ahead = b * PW_BM - r.n_old, first = a.mask || ahead <= 0 ? 0 : ahead / x.tt;
+        return first + max(ntile - first, 0) * (part + 1) / int(split);
+    };
+    float total = 0.f, kept = 0.f;                           // (split: a key's sum here, its weight before)
 
     if (warp == 0) {
         // ---------------------------------------------------------------- producer
@@ -161,7 +171,7 @@ __global__ void __launch_bounds__(PW_NT, 2)
                 }
                 ++nk;
                 if (lane == 0 && !(once && nq > 0))
-                    for (int t = first_tile(b); t < ntile && ok; ++t) {
+                    for (int t = first_tile(b), end = last_tile(b); t < end && ok; ++t) {
                         const int qs = nq % qs_n;
                         if (nq >= qs_n)
                             ok = mbar_wait_bounded(&qempty[qs], uint32_t((nq / qs_n) & 1) ^ 1u, a.status);
@@ -200,7 +210,7 @@ __global__ void __launch_bounds__(PW_NT, 2)
             bool ok = true;
             for (int b = u0; b < u1 && ok; ++b) {
                 ok = mbar_wait_bounded(&kfull[ks], kp, a.status);
-                for (int t = first_tile(b); t < n_t && ok; ++t, ++n) {
+                for (int t = first_tile(b), end = last_tile(b); t < end && ok; ++t, ++n) {
                     if (!once || n == 0) ok = mbar_wait_bounded(&qfull[qs], qp, a.status);
                     if (ok && n >= 2) ok = mbar_wait_bounded(&sfree[n & 1], uint32_t((n >> 1) - 1) & 1u, a.status);
                     if (!ok) break;
@@ -216,7 +226,7 @@ __global__ void __launch_bounds__(PW_NT, 2)
                         tc::mma_commit(&qempty[qs]);
                         if (++qs == qs_n) qs = 0, qp ^= 1u;
                     }
-                    if (t + 1 == n_t) tc::mma_commit(&kempty[ks]);
+                    if (t + 1 == end) tc::mma_commit(&kempty[ks]);
                     tc::mma_commit(&sfull[n & 1]);
                 }
                 if (++ks == ks_n) ks = 0, kp ^= 1u;
@@ -248,7 +258,8 @@ __global__ void __launch_bounds__(PW_NT, 2)
             float before = 0.f;
             if (owner && j < r.n_old) before = wrow[j];
             float sum = 0.f;
-            for (int t = first_tile(b); t < ntile; ++t, ++n) {
+            const int end = last_tile(b);
+            for (int t = first_tile(b); t < end; ++t, ++n) {
                 if ((n & 1) != group) continue;
                 const float mine = next_t == t ? next_lse : lse_of(t);
                 if (ntile > 1 || next_t != t) {                               // (a lone tile's stay)
@@ -261,9 +272,9 @@ __global__ void __launch_bounds__(PW_NT, 2)
                 next_lse = mine;
                 if (ntile > 1) {
                     next_t = t + 2;
-                    if (next_t >= ntile && b + 1 < b1)
-                        next_t = first_tile(b + 1) + (((n + ntile - t) & 1) != group ? 1 : 0);
-                    if (next_t < ntile) next_lse = lse_of(next_t);
+                    if (next_t >= end && b + 1 < b1)                          // (then no split: end = ntile)
+                        next_t = first_tile(b + 1) + (((n + end - t) & 1) != group ? 1 : 0);
+                    if (next_t < end) next_lse = lse_of(next_t);
                 }
                 // a tree's new rows: bit i of tok, whether the tile's token i sees this key (a batch of loads is
                 // independent and on its way at once: loads by need took a block of 33 slots 18 us longer)
@@ -357,8 +368,25 @@ __global__ void __launch_bounds__(PW_NT, 2)
                 asm volatile("bar.sync 1, 256;" ::: "memory");
                 if (group == 0) sum += ssum[(b & 1) * 128 + key];
             }
-            if (owner && j < r.n_keys && ok) wrow[j] = j < r.n_old ? fmaf(x.decay, before, sum) : sum;
+            if (SPLIT) total = ok ? sum : 0.f, kept = before;
+            else if (owner && j < r.n_keys && ok) wrow[j] = j < r.n_old ? fmaf(x.decay, before, sum) : sum;
         }
+    }
+    if constexpr (SPLIT) {
+        // (one block: its sums, group 0's, go to shared memory, and the first CTA adds the parts in their order)
+        const int key = (warp & 3) * 32 + lane, j = b0 * PW_BM + key;
+        float* const xs = reinterpret_cast<float*>(smem + L::SUM_OFF) + ((b0 & 1) ^ 1) * 128;
+        const bool mine = warp >= 2 && warp < 6;
+        if (mine) xs[key] = total;
+        __syncwarp();
+        cluster_sync();
+        if (mine && part == 0 && b0 < b1 && j < r.n_keys) {
+            float sum = 0.f;
+            for (int q = 0; q < int(split); ++q) sum += __uint_as_float(ld_dsmem_u32(dsmem_addr(xs + key, q)));
+            x.weights[size_t(cg) * (size_t(a.max_pages) << a.log2_page) + j] = j < r.n_old ? fmaf(x.decay, kept, sum) : sum;
+        }
+        __syncwarp();
+        cluster_sync();                                      // (no CTA leaves while its sums are read)
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -367,27 +395,30 @@ __global__ void __launch_bounds__(PW_NT, 2)
 
 // ----------------------------------------------------------------------------- host
 
-template <int D>
+template <int D, bool SPLIT>
 static int launch_weights_t(const CUtensorMap& tq, const CUtensorMap& tk, const PwArgs& x, cudaStream_t stream) {
-    auto kern = paged_weights_kernel<D>;
+    auto kern = paged_weights_kernel<D, SPLIT>;
     const size_t smem = PwSmem<D>::TOTAL;
     static std::atomic<uint64_t> raised{0};
     if (!raise_smem(kern, int(smem), raised)) return DARTREE_ECUDA;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned(x.nchunk) * unsigned(x.a.C) * x.a.Hkv);
+    cfg.gridDim = dim3(unsigned(x.split) * x.nchunk * unsigned(x.a.C) * x.a.Hkv);
     cfg.blockDim = dim3(PW_NT);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1] = {pdl_attribute()};
+    cudaLaunchAttribute attr[2] = {pdl_attribute()};
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(x.split);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = SPLIT ? 2 : 1;
     KTimer kt_(KID_PAGED_WEIGHTS, stream);
     return cudaLaunchKernelEx(&cfg, kern, tq, tk, x) == cudaSuccess ? DARTREE_OK : DARTREE_ECUDA;
 }
 
 int launch_paged_weights(const PagedArgs& a, const void* q, const float* lse, float scale, float decay,
                          float* weights, cudaStream_t stream) {
-    PwArgs x{a, a.Hq / a.Hkv, 0, 0, 0, scale * 1.4426950408889634f, decay, lse, weights};
+    PwArgs x{a, a.Hq / a.Hkv, 0, 0, 0, 1, scale * 1.4426950408889634f, decay, lse, weights};
     x.tt = 128 / x.grp < a.S ? 128 / x.grp : a.S;
     x.tiles = (a.S + x.tt - 1) / x.tt;
     const int64_t heads = int64_t(a.C) * a.Hkv;
@@ -415,10 +446,28 @@ int launch_paged_weights(const PagedArgs& a, const void* q, const float* lse, fl
     x.nchunk = 1;
     for (int64_t n = 1; n <= blocks && n <= most; ++n)
         if (time(n) <= best * (x.tiles > 1 ? 1.08 : 1.0)) x.nchunk = int(n);
+    // Few key blocks under many query tiles (prompts with little before them): a block to a CTA, and two, four or
+    // eight CTAs, a cluster, share its tiles; start, end and merge 5 then. The longest CTA, or all waves and half
+    // of the longest (of new rows only the tokens from their own on see them). A prompt of 512 tokens 20.9 -> 9.1
+    // us, 2048 76 -> 42, 378 of three requests, 16 heads of a group, 53 -> 16; over more waves than its tiles are
+    // worth it loses (two chunks of 511 tokens over 8000 rows: 42 us whole, 50 by two).
+    if (x.tiles > 1) {
+        const double seen = double(x.tiles) * (a.mask ? 1.0 : 1.0 - 0.5 * fmin(1.0, a.S / double(blocks * PW_BM)));
+        const double tile_us = a.D == 64 ? 1.2 : 1.4;
+        auto shared_time = [&](int64_t q, double ends) -> double {
+            const double part = ceil(double(x.tiles) / double(q)), w = double(heads * blocks * q) / double(2 * sms);
+            return fmax(ends + part * tile_us, w * (ends + seen / double(q) * tile_us) + 0.5 * part * tile_us);
+        };
+        best = fmin(best, shared_time(1, 3.0));
+        for (int64_t q = 2; q <= 8; q *= 2)
+            if (shared_time(q, 5.0) < 0.95 * best) best = shared_time(q, 5.0), x.nchunk = int(blocks), x.split = int(q);
+    }
     CUtensorMap tq, tk;
     // (a batch without tokens has no queries: its map is never used)
     if (!make_query_map(&tq, a, a.T > 0 ? q : a.k, x.tt) || !make_page_map(&tk, a, a.k)) return DARTREE_ECUDA;
-    return a.D == 64 ? launch_weights_t<64>(tq, tk, x, stream) : launch_weights_t<128>(tq, tk, x, stream);
+    if (x.split > 1)
+        return a.D == 64 ? launch_weights_t<64, true>(tq, tk, x, stream) : launch_weights_t<128, true>(tq, tk, x, stream);
+    return a.D == 64 ? launch_weights_t<64, false>(tq, tk, x, stream) : launch_weights_t<128, false>(tq, tk, x, stream);
 }
 
 }  // namespace dartree

@@ -435,6 +435,10 @@ WEIGHTS = [
     dict(new=[100, 40], old=[200, 7], S=100, tree=True, Hq=2, Hkv=2, page=32),
     dict(new=[50, 33], old=[100, 127], S=50, tree=True, Hq=6, Hkv=2, page=16, D=64),
     dict(new=[300], old=[90], S=300, tree=True, Hq=1, Hkv=1, page=64),
+    # many query tiles over few key blocks: CTAs share a block's tiles
+    dict(new=[300, 3, 0, 130], old=[27, 300, 50, 0], Hq=16, Hkv=1, page=64),
+    dict(new=[260], old=[1], Hq=8, Hkv=1, D=64, page=16, ragged=False),
+    dict(new=[200, 90], old=[60, 3], S=200, tree=True, Hq=8, Hkv=2, page=32),
 ]
 
 
