@@ -92,6 +92,21 @@ __global__ void __launch_bounds__(PW_NT, 2)
         }
         fence_mbar_init();
     }
+    const bool once = x.tiles == 1;                       // one query tile: it stays in stage 0
+    const bool few = once && x.tt * x.grp <= L::FEW;
+    const int ks_n = few ? L::ALL : once ? L::LONG : L::SHORT, qs_n = few ? 1 : once ? L::SHORT : L::LONG;
+    uint8_t* const kring = smem;
+    uint8_t* const qring = few ? smem + L::FEW_OFF : smem + ks_n * L::TILE;
+    const uint32_t qpanel = uint32_t(few ? L::FEW_PANEL : L::PANEL);
+    // columns that pad a tile to 16 are rows of zeros (no copy writes them): their scores are 0 and, with an lse of
+    // -inf, add nothing, so a tile whose tokens are all there needs no masks
+    const int used = x.tt * x.grp, pad = (16 - used % 16) % 16;
+    for (int e = threadIdx.x; e < pad * qs_n * L::PANELS * 8; e += PW_NT) {
+        const int row = e / 8 % pad, pnl = e / 8 / pad;        // (panel of all stages)
+        uint8_t* const at = qring + (pnl / L::PANELS) * L::TILE + (pnl % L::PANELS) * qpanel;
+        reinterpret_cast<uint4*>(at + size_t(used + row) * 128)[e % 8] = make_uint4(0, 0, 0, 0);
+    }
+    fence_proxy_async_smem();
     if (warp == 1) tc::tmem_alloc(slot, 256);
     tc::fence_before_sync();
     __syncthreads();
@@ -111,12 +126,6 @@ __global__ void __launch_bounds__(PW_NT, 2)
     const int per = (blocks + x.nchunk - 1) / x.nchunk;
     const int b0 = chunk * per, b1 = min(blocks, b0 + per);
     const int ntile = (r.n_new + x.tt - 1) / x.tt;
-    const bool once = x.tiles == 1;                       // one query tile: it stays in stage 0
-    const bool few = once && x.tt * x.grp <= L::FEW;
-    const int ks_n = few ? L::ALL : once ? L::LONG : L::SHORT, qs_n = few ? 1 : once ? L::SHORT : L::LONG;
-    uint8_t* const kring = smem;
-    uint8_t* const qring = few ? smem + L::FEW_OFF : smem + ks_n * L::TILE;
-    const uint32_t qpanel = uint32_t(few ? L::FEW_PANEL : L::PANEL);
     // the tiles that see a row of block b, this CTA's part of them
     auto first_tile = [&](int b) -> int {
         const int ahead = b * PW_BM - r.n_old, first = a.mask || ahead <= 0 ? 0 : ahead / x.tt;
@@ -318,7 +327,7 @@ __global__ void __launch_bounds__(PW_NT, 2)
                         }
                     };
                     // hidden columns get a score of -inf (what lies behind the last token may be anything)
-                    if (__all_sync(0xffffffffu, cols == 128 && from <= 0 && !tree)) {
+                    if (__all_sync(0xffffffffu, used > 112 && cols == used && from <= 0 && !tree)) {
 #pragma unroll
                         for (int c0 = 0; c0 < 128; c0 += 32) {
                             uint32_t v[32];

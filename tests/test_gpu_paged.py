@@ -351,6 +351,8 @@ def test_equal_inputs_give_equal_outputs(dd):
         for _ in range(20):
             lse.fill_(7.0)
             assert torch.equal(x.cache.attention(x.q, lse=lse), want) and torch.equal(lse, want_lse)
+        sums = [x.cache.weights(x.q, lse, torch.zeros(x.C, x.Hkv, x.cache.rows, device="cuda")) for _ in range(20)]
+        assert all(torch.equal(w, sums[0]) for w in sums)
         x.ok()
 
 
@@ -435,6 +437,9 @@ WEIGHTS = [
     dict(new=[100, 40], old=[200, 7], S=100, tree=True, Hq=2, Hkv=2, page=32),
     dict(new=[50, 33], old=[100, 127], S=50, tree=True, Hq=6, Hkv=2, page=16, D=64),
     dict(new=[300], old=[90], S=300, tree=True, Hq=1, Hkv=1, page=64),
+    # tiles that 16 columns do not divide, whole ones and their last
+    dict(new=[150, 18], old=[2100, 300], Hq=28, Hkv=4, page=64),
+    dict(new=[60], old=[1500], Hq=10, Hkv=2, D=64, page=32, ragged=False),
     # many query tiles over few key blocks: CTAs share a block's tiles
     dict(new=[300, 3, 0, 130], old=[27, 300, 50, 0], Hq=16, Hkv=1, page=64),
     dict(new=[260], old=[1], Hq=8, Hkv=1, D=64, page=16, ragged=False),
