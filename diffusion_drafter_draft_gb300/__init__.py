@@ -33,7 +33,7 @@ EXPORTS = ("dartree_head_init", "dartree_workspace_bytes", "dartree_topk", "dart
            "dartree_lm_head_topk", "dartree_tree_attention_workspace_bytes", "dartree_tree_attention", "dartree_host_session_create",
            "dartree_host_session_destroy", "dartree_host_stage", "dartree_host_round", "dartree_host_input_bytes",
            "dartree_paged_workspace_bytes", "dartree_paged_append", "dartree_paged_attention",
-           "dartree_paged_weights", "dartree_paged_evict", "dartree_paged_commit")
+           "dartree_paged_weights", "dartree_paged_evict", "dartree_paged_commit", "dartree_paged_commit_weights")
 
 
 class DartreeError(RuntimeError):
@@ -147,6 +147,7 @@ def lib() -> ctypes.CDLL:
                                       ctypes.c_float, vp, vp, sz, vp]),
         "dartree_paged_evict": (i, [P(PagedParams), P(PagedCacheDesc), vp, i, i, i, vp, i, vp, vp, vp, vp, sz, vp]),
         "dartree_paged_commit": (i, [P(PagedParams), P(PagedCacheDesc), vp, vp, i, vp, vp, sz, vp]),
+        "dartree_paged_commit_weights": (i, [P(PagedParams), P(PagedCacheDesc), vp, vp, i, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -737,7 +738,8 @@ class PagedCache:
         self._wsp = (ws.data_ptr(), ws.numel())
         self.rows = self.max_pages * self.page
         L = lib()
-        self._fn = {n: getattr(L, "dartree_paged_" + n) for n in ("append", "attention", "weights", "evict", "commit")}
+        self._fn = {n: getattr(L, "dartree_paged_" + n)
+                    for n in ("append", "attention", "weights", "evict", "commit", "commit_weights")}
         self._pp, self._mp = ctypes.byref(self.p), ctypes.byref(self._m)
         self._t = Tree()
         self._tp = ctypes.byref(self._t)
@@ -830,7 +832,9 @@ class PagedCache:
 
     def weights(self, q, lse, weights, tree=None, scale=None, decay=1.0, stream=None):
         """weights [C, Hkv, max_pages * page] float32 decayed and increased by the attention weight each
-        cached row receives from the new tokens (dartree_paged_weights)."""
+        cached row receives from the new tokens (dartree_paged_weights). The new rows' weights start from 0;
+        rows that were appended without this call keep what lay there. A tree's rows move with the
+        accepted path when commit is given the weights."""
         qp = self._need(q, "q", self.dtype, self._shapes["q"])
         lp = self._need(lse, "lse", torch.float32, self._shapes["lse"])
         wp = self._need(weights, "weights", torch.float32, self._shapes["w"])
@@ -864,9 +868,11 @@ class PagedCache:
                   n_out.data_ptr(), weights_out.data_ptr())
         return dict(keep=keep, n=n_out, weights=weights_out)
 
-    def commit(self, path, accepted_len, n_out=None, stream=None):
+    def commit(self, path, accepted_len, n_out=None, stream=None, weights=None):
         """The accepted path [C, L] of each request's tree moved behind the root's row
-        (dartree_paged_commit) -> rows cached then [C] (n_out may be the cache's n_ctx)."""
+        (dartree_paged_commit) -> rows cached then [C] (n_out may be the cache's n_ctx).
+        weights [C, Hkv, max_pages * page], when given, moves with the rows
+        (dartree_paged_commit_weights)."""
         if not isinstance(path, torch.Tensor) or path.dim() != 2:
             raise ValueError("path must be [C, L]")
         L = path.shape[1]
@@ -874,6 +880,10 @@ class PagedCache:
         ap = self._need(accepted_len, "accepted_len", torch.int32, self._shapes["C"])
         if n_out is None:
             n_out = self._new(torch.empty, (self.C,), torch.int32, stream)
-        self._run("commit", stream, self._pp, self._mp, pp, ap, L,
-                  self._need(n_out, "n_out", torch.int32, self._shapes["C"]))
+        op = self._need(n_out, "n_out", torch.int32, self._shapes["C"])
+        if weights is None:
+            self._run("commit", stream, self._pp, self._mp, pp, ap, L, op)
+        else:
+            wp = self._need(weights, "weights", torch.float32, self._shapes["w"])
+            self._run("commit_weights", stream, self._pp, self._mp, pp, ap, L, wp, op)
         return n_out

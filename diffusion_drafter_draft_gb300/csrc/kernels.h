@@ -295,8 +295,8 @@ int launch_paged_weights(const PagedArgs& a, const void* q, const float* lse, fl
 int launch_paged_evict(const PagedArgs& a, const float* weights, int budget, int sink, int recent,
                        const int32_t* dst_table, int dst_pages, int32_t* keep, int32_t* n_out, float* weights_out,
                        int32_t* counts, cudaStream_t stream);
-int launch_paged_commit(const PagedArgs& a, const int32_t* path, const int32_t* accepted_len, int L, int32_t* n_out,
-                        cudaStream_t stream);
+int launch_paged_commit(const PagedArgs& a, const int32_t* path, const int32_t* accepted_len, int L, float* weights,
+                        int32_t* n_out, cudaStream_t stream);
 
 // Bounded-wait self-test (which = 0: mbarrier, 1: grid barrier on ctr).
 int launch_selftest_wait(int which, unsigned* ctr, int* status, uint64_t limit_ns, cudaStream_t stream);

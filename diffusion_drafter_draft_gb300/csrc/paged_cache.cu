@@ -489,7 +489,8 @@ int launch_paged_evict(const PagedArgs& a, const float* weights, int budget, int
 //
 // One CTA per request. A destination row may be the source of another row, so all rows
 // of a batch of heads are read into registers before any is written: a batch holds
-// PC_NT * PC_V 16-byte vectors and whole heads only. Bound by four dependent loads and the
+// PC_NT * PC_V 16-byte vectors and whole heads only. The rows' accumulated weights, when given,
+// go with them the same way, PC_NT of them a batch. Bound by four dependent loads and the
 // launch: one request 5.7 us, 64 requests 7.1.
 
 constexpr int PC_NT = 512;
@@ -497,7 +498,9 @@ constexpr int PC_V = 8;
 
 template <int VECS>  // 16-byte vectors of a row
 __global__ void __launch_bounds__(PC_NT) paged_commit_kernel(PagedArgs a, const int32_t* __restrict__ path,
-                                                             const int32_t* accepted_len, int L, int32_t* n_out) {
+                                                             const int32_t* accepted_len, int L,
+                                                             float* __restrict__ weights, int32_t* n_out) {
+    __shared__ int s_row[DARTREE_MAX_L];                              // cached row that moves to n_ctx + 1 + i
     __shared__ long long s_src[DARTREE_MAX_L], s_dst[DARTREE_MAX_L];  // element offsets of head 0, -1: not moved
     griddep_launch_dependents();
     griddep_wait();
@@ -524,6 +527,7 @@ __global__ void __launch_bounds__(PC_NT) paged_commit_kernel(PagedArgs a, const 
                 d_o = (long long)paged_offset(a, dp, 0, int(dst));
             }
         }
+        s_row[threadIdx.x] = int(src);
         s_src[threadIdx.x] = so;
         s_dst[threadIdx.x] = d_o;
     }
@@ -558,16 +562,27 @@ __global__ void __launch_bounds__(PC_NT) paged_commit_kernel(PagedArgs a, const 
             if (to[u]) *to[u] = x[u];
         // (the next batch holds other heads: no row of this one)
     }
+    if (weights) {
+        const int hb = PC_NT / acc, hq = int(threadIdx.x) / acc, r = int(threadIdx.x) - hq * acc;  // heads of a batch
+        for (int g0 = 0; g0 < a.Hkv; g0 += hb) {
+            const bool move = hq < hb && g0 + hq < a.Hkv && s_src[r] >= 0;
+            float* const w = weights + (size_t(c) * a.Hkv + g0 + hq) * size_t(cap);
+            float x = 0.f;
+            if (move) x = w[s_row[r]];
+            __syncthreads();
+            if (move) w[old + 1 + r] = x;
+        }
+    }
 }
 
 template <int VECS>
 static cudaError_t launch_commit_t(const cudaLaunchConfig_t& cfg, const PagedArgs& a, const int32_t* path,
-                                   const int32_t* accepted_len, int L, int32_t* n_out) {
-    return cudaLaunchKernelEx(&cfg, paged_commit_kernel<VECS>, a, path, accepted_len, L, n_out);
+                                   const int32_t* accepted_len, int L, float* weights, int32_t* n_out) {
+    return cudaLaunchKernelEx(&cfg, paged_commit_kernel<VECS>, a, path, accepted_len, L, weights, n_out);
 }
 
-int launch_paged_commit(const PagedArgs& a, const int32_t* path, const int32_t* accepted_len, int L, int32_t* n_out,
-                        cudaStream_t stream) {
+int launch_paged_commit(const PagedArgs& a, const int32_t* path, const int32_t* accepted_len, int L, float* weights,
+                        int32_t* n_out, cudaStream_t stream) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned(a.C));
     cfg.blockDim = dim3(PC_NT);
@@ -578,7 +593,7 @@ int launch_paged_commit(const PagedArgs& a, const int32_t* path, const int32_t* 
     KTimer kt_(KID_PAGED_COMMIT, stream);
     const int vecs = a.D * (a.dtype == DARTREE_BF16 ? 2 : 4) / 16;
     const auto f = vecs == 8 ? launch_commit_t<8> : vecs == 16 ? launch_commit_t<16> : launch_commit_t<32>;
-    return f(cfg, a, path, accepted_len, L, n_out) == cudaSuccess ? DARTREE_OK : DARTREE_ECUDA;
+    return f(cfg, a, path, accepted_len, L, weights, n_out) == cudaSuccess ? DARTREE_OK : DARTREE_ECUDA;
 }
 
 }  // namespace dartree

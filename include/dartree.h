@@ -383,7 +383,10 @@ DARTREE_API int dartree_paged_attention(const dartree_paged_params* p, const voi
  * c holds (new ones included)
  *   weights[c, g, j] = decay * weights[c, g, j] + sum exp(scale <q, k_j> - lse)
  * over the tokens that see j; a new row starts from 0 instead of weights[c, g, j].
- * Rows past the new ones are not touched.
+ * Rows past the new ones are not touched. The weights belong to rows, not to tokens: the slots
+ * of a tree are new rows n_ctx + slot, and dartree_paged_commit_weights takes the accepted
+ * ones' weights along. A step without this call gives its rows no weight: the next call takes
+ * what lies there for theirs, so the caller fills those rows first (with 0, say).
  *   lse     [T, Hq] from dartree_paged_attention with the same arguments
  *   weights [C, Hkv, N] float, in and out; decay in [0, 1]
  * The sums are taken in a fixed order: equal inputs give equal results. bf16 only. */
@@ -419,10 +422,17 @@ DARTREE_API int dartree_paged_evict(const dartree_paged_params* p, const dartree
  *   accepted_len  [C], 0..L (clamped to it, and to S - 1)
  *   L             1..DARTREE_MAX_L
  *   n_out         [C] (may be cache->n_ctx itself)
- * T, Hq and q_start are not used. Pages of either dtype. */
+ * T, Hq and q_start are not used. Pages of either dtype.
+ * dartree_paged_commit_weights moves the rows' accumulated weights, too (a row that is not
+ * moved keeps its own): the form for a cache whose tree step was counted by
+ * dartree_paged_weights.
+ *   weights       [C, Hkv, max_pages * page] float, in and out (not NULL) */
 DARTREE_API int dartree_paged_commit(const dartree_paged_params* p, const dartree_paged_cache* cache,
                                      const int32_t* path, const int32_t* accepted_len, int L, int32_t* n_out,
                                      void* ws, size_t ws_bytes, void* stream);
+DARTREE_API int dartree_paged_commit_weights(const dartree_paged_params* p, const dartree_paged_cache* cache,
+                                             const int32_t* path, const int32_t* accepted_len, int L, float* weights,
+                                             int32_t* n_out, void* ws, size_t ws_bytes, void* stream);
 
 /* Node budget and width for a batch of C concurrent requests (DARTree blog post,
  * section 4.4: at concurrency 4 the budget B shrinks from 64 to 32 and the width W

@@ -607,6 +607,78 @@ def test_commit_matches_oracle(dd, i, alias):
     np.testing.assert_array_equal(x.host(x.v), bv)
 
 
+@pytest.mark.parametrize("i", range(len(COMMIT)))
+def test_commit_moves_the_weights_with_the_rows(dd, i):
+    """Every row's weight goes where its key goes; all others stay (weights NaN behind the rows held)."""
+    kw = dict(COMMIT[i])
+    paths, L, S = kw.pop("paths"), kw.pop("L"), kw.pop("S")
+    old = [30 + 7 * c for c in range(len(paths))]
+    x = Case(dd, [S] * len(paths), old, S=S, seed=170 + i, ragged=False, Hq=kw.get("Hkv", 2), spare=3, **kw).fill()
+    path = np.full((x.C, L), -1, np.int32)
+    for c, p in enumerate(paths):
+        path[c, :len(p)] = p
+    w = torch.rand(x.C, x.Hkv, x.cache.rows, generator=x.gen, device="cuda")
+    for c in range(x.C):
+        w[c, :, old[c] + S:] = float("nan")
+    want, plain = w.cpu().numpy().copy(), (x.k.clone(), x.v.clone())
+    acc = torch.tensor([len(p) for p in paths], dtype=torch.int32).cuda()
+    n = x.cache.commit(torch.from_numpy(path).cuda(), acc, weights=w)
+    x.ok()
+    moved = x.host(x.k), x.host(x.v)
+    for c, p in enumerate(paths):
+        src, dst, end = op.commit_moves(path[c], len(p), old[c])
+        assert int(n[c]) == end
+        want[c][:, dst] = want[c][:, src].copy()
+    np.testing.assert_array_equal(w.cpu().numpy(), want)
+    x.k.copy_(plain[0]), x.v.copy_(plain[1])             # keys and values as without weights
+    assert torch.equal(x.cache.commit(torch.from_numpy(path).cuda(), acc), n)
+    np.testing.assert_array_equal(x.host(x.k), moved[0])
+    np.testing.assert_array_equal(x.host(x.v), moved[1])
+
+
+def test_weights_follow_a_committed_tree(dd):
+    """Two tree steps and a token, each counted, against sums kept row by row for the tokens that stayed."""
+    S, C = 17, 2
+    x = Case(dd, [17, 9], [140, 33], S=S, tree=True, Hq=8, Hkv=2, page=32, seed=181, spare=40).fill(new_too=False)
+    scale = 1 / math.sqrt(x.D)
+    w = torch.rand(C, x.Hkv, x.cache.rows, generator=x.gen, device="cuda")
+    for c in range(C):
+        w[c, :, x.old[c]:] = float("nan")
+    kept = [w[c, :, :x.old[c]].cpu().numpy().astype(np.float64) for c in range(C)]
+    token = dd.PagedCache(x.k, x.v, x.table, x.n_ctx, x.Hq, 1)
+    lse = torch.empty(x.T, x.Hq, device="cuda")
+    for last in (False, False, True):
+        cache, T, new = (token, C, [1, 1]) if last else (x.cache, x.T, x.new)
+        tree, first = (None, [0, 1]) if last else (x.tree, x.first)
+        q, z = x.rand(T, x.Hq, x.D), lse[:T]
+        qr = cache.append(q, x.rand(T, x.Hkv, x.D), x.rand(T, x.Hkv, x.D), tree=tree)
+        cache.attention(qr, tree=tree, lse=z)
+        cache.weights(qr, z, w, tree=tree, decay=0.75)
+        old = x.n_ctx.tolist()
+        path, acc = np.full((C, 16), -1, np.int32), [0, 0]
+        hz, hq = z.cpu().numpy().astype(np.float64), x.host(qr).astype(np.float64)
+        for c in range(C):
+            n, r = old[c] + new[c], slice(first[c], first[c] + new[c])
+            seen = op.sees(old[c], new[c], None if last else x.masks[c])
+            kc = x.rows(x.k, c, n)
+            kept[c] = op.weights(hq[r], kc, seen, hz[r], scale, kept[c], old[c], 0.75)
+            if not last:
+                slots = np.flatnonzero(x.masks[c][int(np.argmax(x.depth[c]))])[1:]
+                path[c, :len(slots)], acc[c] = slots, len(slots)
+                kept[c] = kept[c][:, list(range(old[c] + 1)) + [old[c] + int(s) for s in slots]]
+        if not last:
+            cache.commit(torch.from_numpy(path).cuda(), torch.tensor(acc, dtype=torch.int32).cuda(), n_out=x.n_ctx,
+                         weights=w)
+        assert dd.read_status(cache.ws) == 0
+        for c in range(C):
+            m = kept[c].shape[1]
+            assert m == old[c] + 1 + acc[c]
+            # scale * sum |q_d k_d|, |score| and |lse| lie below 64: a term is off by 128 * 2^-23 * 64 = 2^-10 for
+            # the products, 2 * 64 * 2^-22 for the argument, 2^-20 for the exponential, and the sums of at most
+            # 3 * 17 * 4 positive ones by 204 * 2^-24 of themselves: together below 2^-9
+            np.testing.assert_allclose(w[c, :, :m].cpu().numpy(), kept[c], rtol=2.0 ** -9, atol=0)
+
+
 # ------------------------------------------------------------------------------ what the device checks
 
 def _status(dd, x):

@@ -143,6 +143,22 @@ def test_evict_and_commit_arguments(dd):
     assert cm(p=_p(dd, C=0, T=0)) == dd.OK
 
 
+def test_commit_with_weights_arguments(dd):
+    L = dd.lib()
+    need = L.dartree_paged_workspace_bytes(ctypes.byref(_p(dd)))
+
+    def cm(p=None, m=None, path=FAKE, acc=FAKE, Lp=16, w=FAKE, n_out=FAKE, n=None):
+        return L.dartree_paged_commit_weights(ctypes.byref(p or _p(dd)), ctypes.byref(m or _m(dd)), path, acc, Lp, w,
+                                              n_out, WS, need if n is None else n, None)
+
+    for kw in (dict(w=None), dict(path=None), dict(acc=None), dict(Lp=0), dict(n_out=None),
+               dict(m=_m(dd, table=None))):
+        assert cm(**kw) == dd.EINVAL, kw
+    assert cm(Lp=65) == dd.EUNSUPPORTED
+    assert cm(n=need - 1) == dd.EWORKSPACE
+    assert cm(p=_p(dd, C=0, T=0)) == dd.OK
+
+
 def test_outputs_inside_inputs_are_refused(dd):
     """Kernels read these inputs while other CTAs write the outputs."""
     L, p, m = dd.lib(), ctypes.byref(_p(dd)), ctypes.byref(_m(dd))
