@@ -32,8 +32,8 @@ EXPORTS = ("dartree_head_init", "dartree_workspace_bytes", "dartree_topk", "dart
            "dartree_verify_sample", "dartree_adaptive_budget", "dartree_lm_head_workspace_bytes",
            "dartree_lm_head_topk", "dartree_tree_attention_workspace_bytes", "dartree_tree_attention", "dartree_host_session_create",
            "dartree_host_session_destroy", "dartree_host_stage", "dartree_host_round", "dartree_host_input_bytes",
-           "dartree_paged_workspace_bytes", "dartree_paged_append", "dartree_paged_attention",
-           "dartree_paged_weights", "dartree_paged_evict", "dartree_paged_commit", "dartree_paged_commit_weights")
+           "dartree_paged_workspace_bytes", "dartree_paged_attention_plan", "dartree_paged_append",
+           "dartree_paged_attention", "dartree_paged_weights", "dartree_paged_evict", "dartree_paged_commit", "dartree_paged_commit_weights")
 
 
 class DartreeError(RuntimeError):
@@ -72,6 +72,11 @@ class PagedParams(ctypes.Structure):
 
 class PagedCacheDesc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "table", "n_ctx", "q_start")]
+
+
+class PagedPlan(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("few", "tiles_per_cta", "chunks", "cluster", "alone")] + \
+        [("part_bytes", ctypes.c_size_t)]
 
 
 class PagedTokens(ctypes.Structure):
@@ -140,6 +145,7 @@ def lib() -> ctypes.CDLL:
         "dartree_host_round": (i, [vp, P(HostOutputs), vp]),
         "dartree_host_input_bytes": (sz, [vp, i]),
         "dartree_paged_workspace_bytes": (sz, [P(PagedParams)]),
+        "dartree_paged_attention_plan": (i, [P(PagedParams), P(PagedPlan)]),
         "dartree_paged_append": (i, [P(PagedParams), P(PagedTokens), P(PagedCacheDesc), P(Tree), vp, vp, sz, vp]),
         "dartree_paged_attention": (i, [P(PagedParams), vp, P(PagedCacheDesc), P(Tree), ctypes.c_float, vp, vp, vp, sz,
                                         vp]),
@@ -691,7 +697,7 @@ class PagedCache:
       q_start           [C + 1] int32 first rows of q (T rows in all); None: S tokens of
                         every request, or a tree's S slots
       ws                a workspace to use (shared by calls that follow one another on
-                        the device); allocated when None
+                        the device; the one of a larger batch will do); allocated when None
 
     The tensors are read at every call: a serving loop changes table, n_ctx and q_start
     in place. Nothing is allocated by a call that is given its outputs, so it can be
@@ -731,7 +737,8 @@ class PagedCache:
         if n == 0:
             raise DartreeError(EUNSUPPORTED, "dartree_paged_workspace_bytes")
         if ws is None:
-            ws = new_workspace(n, self.device)
+            ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+            ws[:256].zero_()                            # (the status word; the calls fill the rest themselves)
         else:
             self._need(ws, "ws", torch.uint8)
         self.ws = ws

@@ -569,16 +569,15 @@ bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
     return x < y + uint64_t(nb) && y < x + uint64_t(na);
 }
 
-// Workspace of the paged calls: status word, the counts of an eviction, the partial
-// results of an attention.
+// Workspace of the paged calls: status word, the counts of an eviction, and from `part` on the
+// partial results of an attention. The other calls use what lies before them.
 struct PagedLayout {
-    size_t counts, part, total;
+    size_t counts, part;
 };
 PagedLayout paged_layout(const PagedArgs& a) {
     PagedLayout l{};
     l.counts = kAlign;
     l.part = l.counts + up(size_t(a.C) * 4);
-    l.total = l.part + up(paged_attention_part_bytes(a));
     return l;
 }
 
@@ -627,7 +626,16 @@ extern "C" {
 size_t dartree_paged_workspace_bytes(const dartree_paged_params* p) {
     PagedArgs a;
     if (check_paged(p, &a) != DARTREE_OK) return 0;
-    return paged_layout(a).total;
+    return paged_layout(a).part + up(paged_attention_part_bytes(a, true));
+}
+
+int dartree_paged_attention_plan(const dartree_paged_params* p, dartree_paged_plan* plan) {
+    PagedArgs a;
+    if (!plan) return DARTREE_EINVAL;
+    if (int e = check_paged(p, &a)) return e;
+    if (a.dtype != DARTREE_BF16) return DARTREE_EUNSUPPORTED;
+    paged_attention_plan(a, plan);
+    return DARTREE_OK;
 }
 
 int dartree_paged_append(const dartree_paged_params* p, const dartree_paged_tokens* x, const dartree_paged_cache* cache,
@@ -645,7 +653,7 @@ int dartree_paged_append(const dartree_paged_params* p, const dartree_paged_toke
         x->ldq < int64_t(a.Hq) * a.D || x->ldk < int64_t(a.Hkv) * a.D || x->ldv < int64_t(a.Hkv) * a.D)
         return DARTREE_EINVAL;
     if (x->q == q_out && x->ldq != int64_t(a.Hq) * a.D) return DARTREE_EINVAL;
-    if (int e = check_ws(ws, ws_bytes, paged_layout(a).total)) return e;
+    if (int e = check_ws(ws, ws_bytes, paged_layout(a).part)) return e;
     const int64_t es = 16 / vec, out_bytes = int64_t(a.T) * a.Hq * a.D * es;
     auto in_out = [&](const void* t, int64_t ld, int heads) {
         return overlap(q_out, out_bytes, t, ((a.T - 1) * ld + int64_t(heads) * a.D) * es);
@@ -682,7 +690,7 @@ int dartree_paged_attention(const dartree_paged_params* p, const void* q, const 
     if (empty) return DARTREE_OK;
     if (!al16(out) || (lse && reinterpret_cast<uintptr_t>(lse) % 4 != 0)) return DARTREE_EINVAL;
     const PagedLayout l = paged_layout(a);
-    if (int e = check_ws(ws, ws_bytes, l.total)) return e;
+    if (int e = check_ws(ws, ws_bytes, l.part + paged_attention_part_bytes(a, false))) return e;
     const int64_t rows = int64_t(a.T) * a.Hq, bytes = rows * a.D * 2;
     if (overlap(out, bytes, q, bytes) || (lse && (overlap(lse, rows * 4, q, bytes) || overlap(lse, rows * 4, out, bytes))))
         return DARTREE_EINVAL;
@@ -704,7 +712,7 @@ int dartree_paged_weights(const dartree_paged_params* p, const void* q, const fl
         a.q_start = cache->q_start;
     }
     if (!weights || (!empty && !lse)) return DARTREE_EINVAL;
-    if (int e = check_ws(ws, ws_bytes, paged_layout(a).total)) return e;
+    if (int e = check_ws(ws, ws_bytes, paged_layout(a).part)) return e;
     a.status = at<int>(ws, 0);
     return launch_paged_weights(a, q, lse, scale, decay, weights, as_stream(stream));
 }
@@ -723,7 +731,7 @@ int dartree_paged_evict(const dartree_paged_params* p, const dartree_paged_cache
     if (int e = check_paged_cache(cache, nullptr, false, &a)) return e;
     if (!weights || !dst_table || !keep || !n_out) return DARTREE_EINVAL;
     const PagedLayout l = paged_layout(a);
-    if (int e = check_ws(ws, ws_bytes, l.total)) return e;
+    if (int e = check_ws(ws, ws_bytes, l.part)) return e;
     const int64_t row = int64_t(a.C) * a.Hkv * a.page * 4;  // of weights, per page
     if (dst_table == cache->table || (weights_out && overlap(weights, row * a.max_pages, weights_out, row * dst_pages)))
         return DARTREE_EINVAL;
@@ -742,7 +750,7 @@ static int paged_commit(const dartree_paged_params* p, const dartree_paged_cache
     if (a.C == 0) return DARTREE_OK;
     if (int e = check_paged_cache(cache, nullptr, false, &a)) return e;
     if (!path || !accepted_len || !n_out) return DARTREE_EINVAL;
-    if (int e = check_ws(ws, ws_bytes, paged_layout(a).total)) return e;
+    if (int e = check_ws(ws, ws_bytes, paged_layout(a).part)) return e;
     a.status = at<int>(ws, 0);
     return launch_paged_commit(a, path, accepted_len, L, weights, n_out, as_stream(stream));
 }

@@ -8,6 +8,8 @@
 #include <mutex>
 #include <stdint.h>
 
+#include "dartree.h"
+
 namespace dartree {
 
 // Side streams for forks inside one call (0: target-row maxima of a round, 1: the
@@ -287,7 +289,9 @@ bool make_page_map(CUtensorMap* m, const PagedArgs& a, const void* pool);
 int launch_paged_append(const PagedArgs& a, const void* q, const void* k, const void* v, int64_t ldq, int64_t ldk,
                         int64_t ldv, const void* gq, const void* gk, const int32_t* pos_base, float eps, double theta,
                         void* q_out, cudaStream_t stream);
-size_t paged_attention_part_bytes(const PagedArgs& a);
+// Bytes of partial results: of this call, or (most) a bound for every batch of at most these sizes.
+size_t paged_attention_part_bytes(const PagedArgs& a, bool most);
+void paged_attention_plan(const PagedArgs& a, dartree_paged_plan* out);
 int launch_paged_attention(const PagedArgs& a, const void* q, float scale, void* out, float* lse, void* part,
                            cudaStream_t stream);
 int launch_paged_weights(const PagedArgs& a, const void* q, const float* lse, float scale, float decay,

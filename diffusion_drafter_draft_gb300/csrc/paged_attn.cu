@@ -66,7 +66,9 @@ struct PgSmem {
 struct PgPlan {
     int tt, tiles, nt, nchunk, rows;  // tokens per tile, tiles, tiles per CTA, chunks, rows kept per partial tile
     bool cluster, few, alone;         // the chunks merge through shared memory; at most 16 rows; a CTA per SM and tile
-    size_t part_o, part_ml, total;    // workspace (partials): offsets and bytes
+    size_t part_ml, total;            // workspace (partials): offset of the maxima and sums, bytes
+    int64_t most_rows;                // partial rows of any plan for at most these sizes, their bytes
+    size_t most;
 };
 
 template <int D, int NT, int ST, bool CL>
@@ -645,6 +647,26 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
 // a whole tile; through memory 6 and the partial results' bytes at 4 TB/s.
 // Against the best of all ways: one tree of 65 slots over 2048 rows 18.9 -> 13.9 us with
 // CTAs alone, 16 over 4096 rows 120 us with two tiles a CTA (169 with one).
+// Chunks that meet in memory are for tables of PG_PART_BLOCKS blocks on (their launch costs more than a
+// few blocks) and keep within PG_PART_BYTES of partial rows, part_rows of them at most: so a workspace's
+// size grows with batch, tokens and table, and one that serves a batch serves every smaller one. (Tables
+// of up to 16384 rows are planned as without these limits; of random batches over up to 131072 rows 3 in
+// 100 lose 1.4 % by the same times, 7 % at most.)
+constexpr int PG_PART_BLOCKS = 8;
+constexpr int64_t PG_PART_BYTES = int64_t(128) << 20;
+
+// Most chunks of `ctas` tiles that are worth their merge: enough to fill the SMs, or 16.
+static int64_t most_chunks(int64_t ctas, int64_t slots) { return slots / ctas > 16 ? slots / ctas : 16; }
+
+// Upper bound of the partial rows (chunks times rows) of any plan for these tiles: grows with each argument.
+// (`tiles` of all heads; two tiles a CTA, on half the slots, have the same bound.)
+static int64_t part_rows(int64_t tiles, int64_t blocks, int64_t rows, int D) {
+    if (tiles == 0 || blocks < PG_PART_BLOCKS) return 0;
+    const int64_t fill = 2 * int64_t(num_sms()), ways = 16 * tiles > fill ? 16 * tiles : fill;
+    const int64_t all = (ways < tiles * blocks ? ways : tiles * blocks) * rows, cap = PG_PART_BYTES / (4 * D);
+    return all < cap ? all : cap;
+}
+
 static PgPlan paged_plan(const PagedArgs& a) {
     PgPlan p{};
     const int grp = a.Hq / a.Hkv;
@@ -655,6 +677,8 @@ static PgPlan paged_plan(const PagedArgs& a) {
     const int64_t blocks = (((int64_t(a.max_pages) << a.log2_page)) + PG_BN - 1) / PG_BN;
     p.nt = 1, p.nchunk = 1;
     double best = 1e300;
+    p.most_rows = part_rows(heads * p.tiles, blocks, p.rows, a.D);
+    auto stored = [&](int64_t n) { return n == 1 || heads * p.tiles * n * p.rows <= p.most_rows; };
     // whether clusters of n all run at once: each of the eight groups of SMs may have n - 1 places over
     auto fits = [](int64_t ctas, int64_t n, int64_t slots) { return n <= PG_CLUSTER && ctas <= slots - 8 * (n - 1); };
     if (a.S * grp <= 16) {
@@ -664,14 +688,14 @@ static PgPlan paged_plan(const PagedArgs& a) {
         // the memory (a wave of two per SM; the last one's part); a second launch 4.5, the merge in a
         // cluster 2. (Equal clusters: the more chunks, since requests may be shorter than their tables.)
         const double tile = 2.0 * PG_BN * a.D * 2 * double(sms) / 6.7e6;   // a block per SM, at the memory's rate
-        for (int64_t n = 1; n <= blocks && n <= 64 && heads > 0; ++n) {
+        for (int64_t n = 1; n <= blocks && n <= 64 && heads > 0 && n <= most_chunks(heads, 2 * sms); ++n) {
             const double per = double((blocks + n - 1) / n), load = double(heads * n) / double(sms);
             const double waves = floor(load / 2.0), rest = load - 2.0 * waves;
             const double shared = double(heads) * double(blocks) * tile / double(sms);
             double t = n > 1 ? 4.5 : 0.0;
             if (load <= 2.0) t += 3.0 + fmax(per * (load <= 1.0 ? 0.9 : 1.25), shared);
             else t += waves * (3.0 + per * 2.0 * tile) + (rest > 0.0 ? 3.0 + per * fmax(1.25, rest * tile) : 0.0);
-            if (t < best) best = t, p.nchunk = int(n), p.cluster = false;
+            if (t < best && stored(n)) best = t, p.nchunk = int(n), p.cluster = false;
             const double tc = 5.0 + fmax(per * 0.9, shared);
             if (n > 1 && fits(heads * n, n, sms) && tc <= best) best = tc, p.nchunk = int(n), p.cluster = true;
         }
@@ -686,27 +710,38 @@ static PgPlan paged_plan(const PagedArgs& a) {
         const double ends = way == 0 ? 5.0 : alone ? 4.0 : 6.0;
         const double block = a.D == 128 ? (way == 0 ? (many ? 2.1 : 2.5) : alone ? (many ? 1.36 : 1.55) : 1.7)
                                         : (way == 0 ? 1.4 : alone ? 1.5 : 1.45);
-        const int64_t most = slots / base > 16 ? slots / base : 16;
-        for (int64_t n = 1; n <= blocks && n <= most; ++n) {
+        for (int64_t n = 1; n <= blocks && n <= most_chunks(base, slots); ++n) {
             const double load = double(base * n) / double(slots);
             const double waves = load <= 1.0 ? 1.0 : load < 3.0 ? ceil(load) : load + 0.5;
             const bool cluster = n > 1 && nt == 1 && fits(base * n, n, slots);
             const double merge = n == 1 ? 0.0 : cluster ? 2.0 + 3.0 * p.rows / PG_BM
                                  : 6.0 + double(heads) * p.tiles * double(n) * p.rows * a.D * 8.0 / 4e6;
             const double t = fmax(waves * (ends + block * double((blocks + n - 1) / n)), shared + 3.0) + merge;
-            if (t < best) best = t, p.nt = nt, p.nchunk = int(n), p.cluster = cluster, p.alone = alone;
+            if (t < best && (cluster || stored(n)))
+                best = t, p.nt = nt, p.nchunk = int(n), p.cluster = cluster, p.alone = alone;
         }
     }
-    if (p.nchunk > 1 && !p.cluster) {
+    auto bytes = [&](int64_t rows, size_t* ml) {
         auto up = [](size_t b) { return (b + 255) / 256 * 256; };
-        const size_t rows = size_t(a.C) * a.Hkv * p.tiles * p.nchunk * p.rows;
-        p.part_ml = up(rows * a.D * 4);
-        p.total = p.part_ml + up(rows * 8);
-    }
+        *ml = up(size_t(rows) * a.D * 4);
+        return *ml + up(size_t(rows) * 8);
+    };
+    size_t most_ml;
+    p.most = bytes(p.most_rows, &most_ml);
+    if (p.nchunk > 1 && !p.cluster) p.total = bytes(heads * p.tiles * p.nchunk * p.rows, &p.part_ml);
     return p;
 }
 
-size_t paged_attention_part_bytes(const PagedArgs& a) { return a.dtype == DARTREE_BF16 ? paged_plan(a).total : 0; }
+size_t paged_attention_part_bytes(const PagedArgs& a, bool most) {
+    if (a.dtype != DARTREE_BF16) return 0;
+    const PgPlan p = paged_plan(a);
+    return most ? p.most : p.total;
+}
+
+void paged_attention_plan(const PagedArgs& a, dartree_paged_plan* out) {
+    const PgPlan p = paged_plan(a);
+    *out = dartree_paged_plan{p.few, p.few ? 1 : p.nt, p.nchunk, p.cluster, p.alone, p.total};
+}
 
 bool make_page_map(CUtensorMap* m, const PagedArgs& a, const void* pool) {
     const uint64_t d[4] = {uint64_t(a.D), uint64_t(a.page), uint64_t(a.Hkv), uint64_t(a.n_pages)};

@@ -310,7 +310,9 @@ DARTREE_API int dartree_tree_attention(const dartree_attn_params* p, const void*
  * such a page; results that needed it are finite but unspecified). Two rows of the
  * batch's new tokens never share a page row: pages that requests share hold cached rows
  * only.
- * Workspace of all calls: dartree_paged_workspace_bytes. */
+ * Workspace of all calls: dartree_paged_workspace_bytes, which never shrinks as C, S or max_pages
+ * grow, so one made for the largest batch serves every smaller one. (The attention may store
+ * partial results in it, at most 140 MB; the other calls use 256 bytes and 4 for each request.) */
 typedef struct {
     int C;          /* requests (C * Hkv < 2^24; C * S * Hq, T * Hq and max_pages * page + S below 2^31) */
     int T;          /* rows of q (C * S without q_start) */
@@ -332,6 +334,18 @@ typedef struct {
 } dartree_paged_cache;
 
 DARTREE_API size_t dartree_paged_workspace_bytes(const dartree_paged_params* p);
+
+/* How dartree_paged_attention takes these sizes on the current device (host only, no GPU work; for tests
+ * and tuning). Errors as for the attention's own sizes. */
+typedef struct {
+    int few;           /* 1: at most 16 rows of a key/value head, transposed products */
+    int tiles_per_cta; /* 128-row query tiles of a CTA: 1 or 2 */
+    int chunks;        /* parts of a tile's keys, each a CTA's */
+    int cluster;       /* 1: the chunks merge through shared memory; 0 with chunks > 1: through the workspace */
+    int alone;         /* 1: one CTA to an SM */
+    size_t part_bytes; /* partial results in the workspace */
+} dartree_paged_plan;
+DARTREE_API int dartree_paged_attention_plan(const dartree_paged_params* p, dartree_paged_plan* plan);
 
 /* Head norms, position rotation and store of a layer's new tokens in one pass.
  *   q, k, v     rows of Hq, Hkv and Hkv heads of D values; consecutive tokens lie ldq,

@@ -356,6 +356,36 @@ def test_equal_inputs_give_equal_outputs(dd):
         x.ok()
 
 
+def test_one_workspace_for_batches_of_every_size(dd):
+    """Made for the largest batch and the most tokens: smaller ones, some with more partial results than the
+    largest, run in it, and the other calls, too."""
+    rows, Hq, Hkv, page = 4096, 32, 8, 64
+    p = dd.PagedParams(64, 64 * 65, 65, Hq, Hkv, 128, page, 1, rows // page, dd.BF16)
+    n = dd.lib().dartree_paged_workspace_bytes(dd.ctypes.byref(p))
+    ws = dd.new_workspace(n)
+    stored = 0
+    for C, S, old in ((8, 33, 500), (8, 65, 300), (1, 1, 4000), (12, 9, 200), (3, 20, 4000), (1, 64, 2000), (20, 2, 60)):
+        x = Case(dd, [S] * C, [old - c for c in range(C)], Hq=Hq, Hkv=Hkv, page=page, ragged=False, seed=C + S,
+                 spare=rows - old - S).fill()
+        x.cache = dd.PagedCache(x.k, x.v, x.table, x.n_ctx, Hq, S, ws=ws)
+        plan = dd.PagedPlan()
+        assert dd.lib().dartree_paged_attention_plan(dd.ctypes.byref(x.cache.p), dd.ctypes.byref(plan)) == 0
+        stored += plan.part_bytes > 0
+        lse = torch.empty(x.T, Hq, device="cuda")
+        out = x.cache.attention(x.q, lse=lse)
+        w = torch.zeros(C, Hkv, x.cache.rows, device="cuda")
+        x.cache.weights(x.q, lse, w)
+        x.ok()
+        _check_attention(x, out, lse, most=4)
+        path, acc = torch.full((C, 4), -1, dtype=torch.int32), torch.zeros(C, dtype=torch.int32)
+        if S > 2:
+            path[:, 0], acc[:] = 2, 1
+        n_out = x.cache.commit(path.cuda(), acc.cuda(), weights=w)
+        x.ok()
+        assert n_out.tolist() == [o + 1 + int(S > 2) for o in x.old]
+    assert stored                                        # (eight requests of 33 tokens, on 148 and on 152 SMs)
+
+
 # ------------------------------------------------------------------------------ append
 
 APPEND = [

@@ -195,6 +195,51 @@ def test_outputs_inside_inputs_are_refused(dd):
     assert ev(at(-4096), at(0), at(4 - w // 4)) == dd.EINVAL
 
 
+PLAN_SIZES = dict(C=64, T=64, S=1, Hq=32, Hkv=8, D=128, page=64, n_pages=1 << 20, max_pages=128, dtype=1)
+
+
+def _plan(dd, **kw):
+    p, out = dd.PagedParams(**{**PLAN_SIZES, **kw}), dd.PagedPlan()
+    assert dd.lib().dartree_paged_attention_plan(ctypes.byref(p), ctypes.byref(out)) == dd.OK
+    return out
+
+
+def _bytes(dd, **kw):
+    n = dd.lib().dartree_paged_workspace_bytes(ctypes.byref(dd.PagedParams(**{**PLAN_SIZES, **kw})))
+    assert n > 0
+    return n
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hkv,grp", [(8, 4), (1, 8), (2, 16), (8, 1), (4, 7), (1, 128), (32, 1)])
+def test_a_workspace_serves_every_smaller_batch(dd, Hkv, grp, D):
+    """The bytes grow with C, S and the table's width, and cover what each batch's own plan stores."""
+    heads = dict(Hq=Hkv * grp, Hkv=Hkv, D=D)
+    Cs, Ss = (0, 1, 2, 3, 5, 8, 16, 31, 48, 64, 200), (1, 2, 3, 4, 16, 17, 33, 65, 128, 500, 2048)
+    pages = (1, 7, 8, 9, 16, 64, 128, 500, 1024, 4096)
+    need = {}
+    for C in Cs:
+        for S in Ss:
+            for m in pages:
+                b = need[C, S, m] = _bytes(dd, C=C, S=S, T=C * S, max_pages=m, **heads)
+                plan = _plan(dd, C=C, S=S, T=C * S, max_pages=m, **heads)
+                assert 256 + 4 * C + plan.part_bytes <= b <= 256 + 4 * C + 256 + (140 << 20), (C, S, m)
+                for C2, S2, m2 in ((Cs[max(Cs.index(C) - 1, 0)], S, m), (C, Ss[max(Ss.index(S) - 1, 0)], m),
+                                   (C, S, pages[max(pages.index(m) - 1, 0)])):
+                    assert need[C2, S2, m2] <= b, (C, S, m)
+
+
+def test_plan_arguments(dd):
+    L, out = dd.lib(), dd.PagedPlan()
+    ok = _p(dd)
+    assert L.dartree_paged_attention_plan(ctypes.byref(ok), None) == dd.EINVAL
+    assert L.dartree_paged_attention_plan(None, ctypes.byref(out)) == dd.EINVAL
+    assert L.dartree_paged_attention_plan(ctypes.byref(_p(dd, dtype=0)), ctypes.byref(out)) == dd.EUNSUPPORTED
+    for kw, err in BAD:
+        assert L.dartree_paged_attention_plan(ctypes.byref(_p(dd, **kw)), ctypes.byref(out)) == getattr(dd, err)
+    assert _plan(dd).few == 1 and _plan(dd, S=2048, C=1, T=2048).few == 0
+
+
 def test_kernel_families_are_named(dd):
     names = [dd.lib().dartree_kernel_name(i).decode() for i in range(dd.num_kernel_ids())]
     for n in ("append", "attn", "weights", "select", "move", "commit"):
