@@ -701,11 +701,13 @@ class PagedCache:
 
     The tensors are read at every call: a serving loop changes table, n_ctx and q_start
     in place. Nothing is allocated by a call that is given its outputs, so it can be
-    captured into a CUDA graph. read_status(cache.ws) tells what the kernels found wrong
-    in lengths and tables. Calls run on `stream` (default: the current stream of the
-    pages' device) and outputs they allocate belong to it; the workspace is made on the
-    stream that is current when the object is. An object is used by one host thread at
-    a time.
+    captured into a CUDA graph (the object is kept as long as the graph). read_status(cache.ws)
+    tells what the kernels found wrong in lengths and tables. Calls run on `stream` (default:
+    the current stream of the pages' device) and outputs they allocate belong to it; the
+    workspace is made on the stream that is current when the object is, and the first call on
+    another stream waits for that and keeps the memory until the work there is done (calls
+    that are captured on another stream do not wait: torch.cuda.graph has waited for the
+    device). An object is used by one host thread at a time.
     """
 
     def __init__(self, k_pages, v_pages, table, n_ctx, Hq, S, T=None, q_start=None, ws=None):
@@ -736,9 +738,14 @@ class PagedCache:
         n = lib().dartree_paged_workspace_bytes(ctypes.byref(self.p))
         if n == 0:
             raise DartreeError(EUNSUPPORTED, "dartree_paged_workspace_bytes")
+        self._made, self._known = None, None            # end of the workspace's fill, streams that know it
         if ws is None:
             ws = torch.empty(n, dtype=torch.uint8, device=self.device)
             ws[:256].zero_()                            # (the status word; the calls fill the rest themselves)
+            here = torch.cuda.current_stream(self.device)
+            self._known = {here.cuda_stream}
+            if not self._capturing(here):
+                self._made = here.record_event()
         else:
             self._need(ws, "ws", torch.uint8)
         self.ws = ws
@@ -768,9 +775,26 @@ class PagedCache:
             raise ValueError(f"{name} must be on {self.device}, got {t.device}")
         return ptr
 
+    @staticmethod
+    def _capturing(stream) -> bool:
+        with torch.cuda.stream(stream):
+            return torch.cuda.is_current_stream_capturing()
+
+    def _meet(self, stream):
+        """A stream other than the one that filled the workspace is about to use it."""
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        self.ws.record_stream(stream)
+        if not self._capturing(stream):
+            if self._made is not None:
+                stream.wait_event(self._made)
+            self._known.add(stream.cuda_stream)
+
     def _run(self, name, stream, *args):
         # (the current stream as its handle: a torch.cuda.Stream object costs more than the launch)
         s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(self.device.index)
+        if self._known is not None and s not in self._known:
+            self._meet(stream)
         if torch.cuda.current_device() == self.device.index:
             rc = self._fn[name](*args, *self._wsp, s)
         else:

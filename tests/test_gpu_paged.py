@@ -969,6 +969,42 @@ def test_streams_and_graphs(dd):
         assert ((w.sum(-1) - (i + 2) * 4).abs() < 1e-2).all()
 
 
+@pytest.mark.parametrize("current", [False, True])
+def test_a_workspace_is_filled_before_another_stream_uses_it(dd, current):
+    """The fill waits behind work of the stream it was made on; a status word that a call on a side stream
+    writes meanwhile must not be cleared by it."""
+    x = Case(dd, [2], [40], seed=191).fill()
+    x.table[0, 0] = -1
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(50_000_000)                        # some 25 ms on the current stream
+    cache = dd.PagedCache(x.k, x.v, x.table, x.n_ctx, x.Hq, x.S, T=x.T, q_start=x.q_start)
+    if current:
+        with torch.cuda.stream(side):
+            cache.attention(x.q)
+    else:
+        cache.attention(x.q, stream=side)
+    torch.cuda.synchronize()
+    assert dd.read_status(cache.ws) == dd.EINTERNAL
+
+
+def test_a_workspace_outlives_its_object_on_a_side_stream(dd):
+    """Its memory is not given away while a call on a side stream may still use it."""
+    x = Case(dd, [2], [40], seed=193).fill()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    cache = dd.PagedCache(x.k, x.v, x.table, x.n_ctx, x.Hq, x.S, T=x.T, q_start=x.q_start)
+    at, n = cache.ws.data_ptr(), cache.ws.numel()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)
+    out = cache.attention(x.q, stream=side)
+    del cache
+    assert all(t.data_ptr() != at for t in [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in range(8)])
+    side.synchronize()
+    assert torch.isfinite(out.float()).all()
+
+
 def test_binding_refuses_what_it_can_see(dd):
     x = Case(dd, [2, 3], [5, 9], seed=97).fill()
     k = x.rand(x.T, x.Hkv, x.D)
