@@ -641,10 +641,11 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
 
 // Tiles per CTA and chunks of a tile's key blocks: the least time, in us, fitted to sweeps of
 // 18 shapes with caches that were not in the L2. A CTA's start and end, then a block: two
-// tiles 6 and 1.7 (D = 128); one tile beside another CTA, with a ring of one block, 5 and
-// 2.5; alone on its SM with two and a half blocks in flight 4 and 1.55 (both less where many
-// tiles read the same keys). Merging in a cluster, where all CTAs run at once, 2 and 3 for
-// a whole tile; through memory 6 and the partial results' bytes at 4 TB/s.
+// tiles 6 and 1.7 (heads of 128; of 64, 6 and 1.45, which two CTAs of one tile, 5 and 1.4,
+// always beat); one tile beside another CTA, with a ring of one block, 5 and 2.5; alone on
+// its SM with two and a half blocks in flight 4 and 1.55 (both less where many tiles read
+// the same keys). Merging in a cluster, where all CTAs run at once, 2 and 3 for a whole
+// tile; through memory 6 and the partial results' bytes at 4 TB/s.
 // Against the best of all ways: one tree of 65 slots over 2048 rows 18.9 -> 13.9 us with
 // CTAs alone, 16 over 4096 rows 120 us with two tiles a CTA (169 with one).
 // Chunks that meet in memory are for tables of PG_PART_BLOCKS blocks on (their launch costs more than a
@@ -703,13 +704,13 @@ static PgPlan paged_plan(const PagedArgs& a) {
     }
     const double shared = double(heads) * double(blocks) * 4.0 * PG_BN * a.D / 6.7e6;   // the memory's share
     for (int way = 0; way < 3 && heads > 0 && !p.few; ++way) {
-        if (way == 2 && p.tiles == 1) break;
+        if (way == 2 && (p.tiles == 1 || a.D == 64)) break;
         const int nt = way == 2 ? 2 : 1;
         const bool alone = way == 1, many = p.tiles >= 4;
         const int64_t base = heads * ((p.tiles + nt - 1) / nt), slots = int64_t(num_sms()) * (way == 0 ? 2 : 1);
         const double ends = way == 0 ? 5.0 : alone ? 4.0 : 6.0;
         const double block = a.D == 128 ? (way == 0 ? (many ? 2.1 : 2.5) : alone ? (many ? 1.36 : 1.55) : 1.7)
-                                        : (way == 0 ? 1.4 : alone ? 1.5 : 1.45);
+                                        : (way == 0 ? 1.4 : 1.5);
         for (int64_t n = 1; n <= blocks && n <= most_chunks(base, slots); ++n) {
             const double load = double(base * n) / double(slots);
             const double waves = load <= 1.0 ? 1.0 : load < 3.0 ? ceil(load) : load + 0.5;
@@ -798,9 +799,8 @@ int launch_paged_attention(const PagedArgs& a, const void* q, float scale, void*
     if (p.few)
         e = launch_paged_few(x, p.cluster, p.alone, tq, tk, tv, stream);
     else if (a.D == 64)
-        e = (p.nt == 2 ? launch_attn_t<64, 2, 8>
-             : p.alone ? (p.cluster ? launch_attn_t<64, 1, 8, true> : launch_attn_t<64, 1, 8>)
-                       : (p.cluster ? launch_attn_t<64, 1, 4, true> : launch_attn_t<64, 1, 4>))(tq, tk, tv, x, stream);
+        e = (p.alone ? (p.cluster ? launch_attn_t<64, 1, 8, true> : launch_attn_t<64, 1, 8>)
+                     : (p.cluster ? launch_attn_t<64, 1, 4, true> : launch_attn_t<64, 1, 4>))(tq, tk, tv, x, stream);
     else
         e = (p.nt == 2 ? launch_attn_t<128, 2, 5>
              : p.alone ? (p.cluster ? launch_attn_t<128, 1, 5, true> : launch_attn_t<128, 1, 5>)

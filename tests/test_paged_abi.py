@@ -240,6 +240,24 @@ def test_plan_arguments(dd):
     assert _plan(dd).few == 1 and _plan(dd, S=2048, C=1, T=2048).few == 0
 
 
+def test_every_way_of_the_attention_is_taken(dd):
+    """(few, tiles per CTA, chunks through memory, cluster, alone): what is compiled for a head size is
+    what its plans choose."""
+    import random
+    rng, taken = random.Random(3), {64: set(), 128: set()}
+    for _ in range(6000):
+        C, S = int(2 ** rng.uniform(0, 8)), rng.choice([1, int(2 ** rng.uniform(0, 13))])
+        Hkv, grp = rng.choice([(1, 8), (2, 5), (4, 4), (8, 4), (8, 1), (4, 7), (2, 16), (1, 1)])
+        for D, seen in taken.items():
+            p = _plan(dd, C=C, S=S, T=C * S, Hq=Hkv * grp, Hkv=Hkv, D=D, max_pages=int(2 ** rng.uniform(0, 11)))
+            seen.add((p.few, p.tiles_per_cta, int(p.part_bytes > 0), p.cluster, p.alone))
+            assert (p.part_bytes > 0) == (p.chunks > 1 and not p.cluster)
+    few = {(1, 1, m, c, a) for m, c, a in ((0, 0, 0), (0, 0, 1), (1, 0, 0), (1, 0, 1), (0, 1, 1))}
+    one = {(0, 1, m, c, a) for m, c in ((0, 0), (1, 0), (0, 1)) for a in (0, 1)}
+    assert taken[64] == few | one
+    assert taken[128] == few | one | {(0, 2, 0, 0, 0), (0, 2, 1, 0, 0)}
+
+
 def test_kernel_families_are_named(dd):
     names = [dd.lib().dartree_kernel_name(i).decode() for i in range(dd.num_kernel_ids())]
     for n in ("append", "attn", "weights", "select", "move", "commit"):
