@@ -741,15 +741,15 @@ int dartree_paged_evict(const dartree_paged_params* p, const dartree_paged_cache
 }
 
 static int paged_commit(const dartree_paged_params* p, const dartree_paged_cache* cache, const int32_t* path,
-                        const int32_t* accepted_len, int L, float* weights, int32_t* n_out, void* ws, size_t ws_bytes,
-                        void* stream) {
+                        const int32_t* accepted_len, int L, bool weighted, float* weights, int32_t* n_out, void* ws,
+                        size_t ws_bytes, void* stream) {
     PagedArgs a;
     if (int e = check_paged(p, &a)) return e;
     if (L < 1) return DARTREE_EINVAL;
     if (L > DARTREE_MAX_L) return DARTREE_EUNSUPPORTED;
     if (a.C == 0) return DARTREE_OK;
     if (int e = check_paged_cache(cache, nullptr, false, &a)) return e;
-    if (!path || !accepted_len || !n_out) return DARTREE_EINVAL;
+    if (!path || !accepted_len || !n_out || (weighted && !weights)) return DARTREE_EINVAL;
     if (int e = check_ws(ws, ws_bytes, paged_layout(a).part)) return e;
     a.status = at<int>(ws, 0);
     return launch_paged_commit(a, path, accepted_len, L, weights, n_out, as_stream(stream));
@@ -757,14 +757,13 @@ static int paged_commit(const dartree_paged_params* p, const dartree_paged_cache
 
 int dartree_paged_commit(const dartree_paged_params* p, const dartree_paged_cache* cache, const int32_t* path,
                          const int32_t* accepted_len, int L, int32_t* n_out, void* ws, size_t ws_bytes, void* stream) {
-    return paged_commit(p, cache, path, accepted_len, L, nullptr, n_out, ws, ws_bytes, stream);
+    return paged_commit(p, cache, path, accepted_len, L, false, nullptr, n_out, ws, ws_bytes, stream);
 }
 
 int dartree_paged_commit_weights(const dartree_paged_params* p, const dartree_paged_cache* cache, const int32_t* path,
                                  const int32_t* accepted_len, int L, float* weights, int32_t* n_out, void* ws,
                                  size_t ws_bytes, void* stream) {
-    if (!weights) return DARTREE_EINVAL;
-    return paged_commit(p, cache, path, accepted_len, L, weights, n_out, ws, ws_bytes, stream);
+    return paged_commit(p, cache, path, accepted_len, L, true, weights, n_out, ws, ws_bytes, stream);
 }
 
 int dartree_adaptive_budget(int C, int* B, int* W) {

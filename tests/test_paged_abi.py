@@ -157,6 +157,7 @@ def test_commit_with_weights_arguments(dd):
     assert cm(Lp=65) == dd.EUNSUPPORTED
     assert cm(n=need - 1) == dd.EWORKSPACE
     assert cm(p=_p(dd, C=0, T=0)) == dd.OK
+    assert cm(p=_p(dd, C=0, T=0), path=None, acc=None, w=None, n_out=None) == dd.OK    # empty tensors
 
 
 def test_outputs_inside_inputs_are_refused(dd):
