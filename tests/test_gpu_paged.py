@@ -395,6 +395,11 @@ APPEND = [
     dict(new=[65, 20], old=[100, 31], S=65, tree=True, Hq=32, Hkv=8, page=64),
     dict(new=[700], old=[5], ragged=False, Hq=3, Hkv=1, D=64),          # four rows per CTA, an odd tail
     dict(new=[701, 2], old=[5, 9], Hq=3, Hkv=3, D=128),
+    # a warp per row, eight rows a CTA and an odd tail (from 16 rows an SM on; those above have a CTA each):
+    # more heads than a warp has in hand, requests without tokens, rows outside the batch
+    dict(new=[1200, 0, 901, 437], old=[3, 9, 60, 0], Hq=20, Hkv=10, D=128, page=32, pad=(3, 2)),
+    dict(new=[1200, 0, 901, 437], old=[3, 9, 60, 0], Hq=40, Hkv=20, D=64, pad=(3, 2)),
+    dict(new=[65 - c for c in range(39)], old=[11 * c for c in range(39)], S=65, tree=True, Hq=3, Hkv=1, page=64),
 ]
 
 
