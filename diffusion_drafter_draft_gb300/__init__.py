@@ -740,12 +740,11 @@ class PagedCache:
             raise DartreeError(EUNSUPPORTED, "dartree_paged_workspace_bytes")
         self._made, self._known = None, None            # end of the workspace's fill, streams that know it
         if ws is None:
+            # (only its status word has to start at zero; the calls fill the rest themselves)
             ws = torch.empty(n, dtype=torch.uint8, device=self.device)
-            ws[:256].zero_()                            # (the status word; the calls fill the rest themselves)
-            here = torch.cuda.current_stream(self.device)
-            self._known = {here.cuda_stream}
-            if not self._capturing(here):
-                self._made = here.record_event()
+            s = torch._C._cuda_getCurrentRawStream(self.device.index)
+            self._known = {s}
+            self._made = self._on_device(lambda: self._clear(ws, s))
         else:
             self._need(ws, "ws", torch.uint8)
         self.ws = ws
@@ -775,20 +774,34 @@ class PagedCache:
             raise ValueError(f"{name} must be on {self.device}, got {t.device}")
         return ptr
 
-    @staticmethod
-    def _capturing(stream) -> bool:
-        with torch.cuda.stream(stream):
-            return torch.cuda.is_current_stream_capturing()
+    def _on_device(self, f):
+        if torch.cuda.current_device() == self.device.index:
+            return f()
+        with torch.cuda.device(self.device):
+            return f()
+
+    _cleared = {}   # (device, stream): an event behind the last workspace cleared there
+
+    def _clear(self, ws, s):
+        """Clears the workspace's status word on the current stream s; an event behind that, None while s is
+        captured (others cannot wait for that)."""
+        _call("dartree_clear_status", ctypes.c_void_p(ws.data_ptr()), ctypes.c_void_p(s))
+        if torch.cuda.is_current_stream_capturing():
+            return None
+        e = self._cleared.setdefault((self.device.index, s), torch.cuda.Event())
+        e.record(torch.cuda.current_stream(self.device))
+        return e
 
     def _meet(self, stream):
         """A stream other than the one that filled the workspace is about to use it."""
         if stream is None:
             stream = torch.cuda.current_stream(self.device)
-        self.ws.record_stream(stream)
-        if not self._capturing(stream):
-            if self._made is not None:
-                stream.wait_event(self._made)
-            self._known.add(stream.cuda_stream)
+        with torch.cuda.stream(stream):
+            self.ws.record_stream(stream)
+            if not torch.cuda.is_current_stream_capturing():
+                if self._made is not None:
+                    stream.wait_event(self._made)
+                self._known.add(stream.cuda_stream)
 
     def _run(self, name, stream, *args):
         # (the current stream as its handle: a torch.cuda.Stream object costs more than the launch)
