@@ -18,7 +18,7 @@ namespace dartree {
 // pairs (16-byte loads and stores, the mean square by shuffles). Everything in fp32,
 // rounded once when stored. Bound by memory once there are rows enough: 13.5 k rows of 48
 // heads of 128 (150 MB each way) take 58 us, a plain copy 52; one head in hand per lane
-// instead of four took 68 (24 KB in flight an SM). A few rows are latency (65 rows 5.8 us).
+// instead of four took 68 (24 KB in flight an SM). A few rows are latency (65 rows 5.6 us).
 
 constexpr int PA_NT = 256;
 
@@ -275,7 +275,7 @@ int launch_paged_append(const PagedArgs& a, const void* q, const void* k, const 
 // PM_STREAM bytes on neither side is meant to stay in the L2: with and without that,
 // selection included, 8 MB 15.1 and 14.4 us, 17 MB 17.8 and 18.5, 34 MB 23.9 and 25.1, 134
 // MB 56.7 and 60.8, and an attention over the copies that follows keeps the gain.
-// 128 heads of 8192-16384 rows to 2048: selection 16 us, bound by its passes' latency (one
+// 128 heads of 8192-16384 rows to 2048, 61 us: selection 14-16 us, bound by its passes' latency (one
 // CTA per head), then the copy, bound by memory.
 
 constexpr int PS_NT = 1024;
@@ -491,16 +491,16 @@ int launch_paged_evict(const PagedArgs& a, const float* weights, int budget, int
 // of a batch of heads are read into registers before any is written: a batch holds
 // PC_NT * PC_V 16-byte vectors and whole heads only. The rows' accumulated weights, when given,
 // go with them the same way, PC_NT of them a batch. Bound by four dependent loads and the
-// launch: one request 5.7 us, 64 requests 7.1.
+// launch: one request 4.8 us, 64 requests 6.9; with weights, kernels of their own, 5.6 and 7.6.
 
 constexpr int PC_NT = 512;
 constexpr int PC_V = 8;
 
-template <int VECS>  // 16-byte vectors of a row
+template <int VECS, bool WEIGHTS>  // 16-byte vectors of a row
 __global__ void __launch_bounds__(PC_NT) paged_commit_kernel(PagedArgs a, const int32_t* __restrict__ path,
                                                              const int32_t* accepted_len, int L,
                                                              float* __restrict__ weights, int32_t* n_out) {
-    __shared__ int s_row[DARTREE_MAX_L];                              // cached row that moves to n_ctx + 1 + i
+    __shared__ int s_row[WEIGHTS ? DARTREE_MAX_L : 1];                // cached row that moves to n_ctx + 1 + i
     __shared__ long long s_src[DARTREE_MAX_L], s_dst[DARTREE_MAX_L];  // element offsets of head 0, -1: not moved
     griddep_launch_dependents();
     griddep_wait();
@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(PC_NT) paged_commit_kernel(PagedArgs a, const 
                 d_o = (long long)paged_offset(a, dp, 0, int(dst));
             }
         }
-        s_row[threadIdx.x] = int(src);
+        if constexpr (WEIGHTS) s_row[threadIdx.x] = int(src);
         s_src[threadIdx.x] = so;
         s_dst[threadIdx.x] = d_o;
     }
@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(PC_NT) paged_commit_kernel(PagedArgs a, const 
             if (to[u]) *to[u] = x[u];
         // (the next batch holds other heads: no row of this one)
     }
-    if (weights) {
+    if constexpr (WEIGHTS) {
         const int hb = PC_NT / acc, hq = int(threadIdx.x) / acc, r = int(threadIdx.x) - hq * acc;  // heads of a batch
         for (int g0 = 0; g0 < a.Hkv; g0 += hb) {
             const bool move = hq < hb && g0 + hq < a.Hkv && s_src[r] >= 0;
@@ -575,10 +575,10 @@ __global__ void __launch_bounds__(PC_NT) paged_commit_kernel(PagedArgs a, const 
     }
 }
 
-template <int VECS>
+template <int VECS, bool WEIGHTS>
 static cudaError_t launch_commit_t(const cudaLaunchConfig_t& cfg, const PagedArgs& a, const int32_t* path,
                                    const int32_t* accepted_len, int L, float* weights, int32_t* n_out) {
-    return cudaLaunchKernelEx(&cfg, paged_commit_kernel<VECS>, a, path, accepted_len, L, weights, n_out);
+    return cudaLaunchKernelEx(&cfg, paged_commit_kernel<VECS, WEIGHTS>, a, path, accepted_len, L, weights, n_out);
 }
 
 int launch_paged_commit(const PagedArgs& a, const int32_t* path, const int32_t* accepted_len, int L, float* weights,
@@ -592,7 +592,12 @@ int launch_paged_commit(const PagedArgs& a, const int32_t* path, const int32_t* 
     cfg.numAttrs = 1;
     KTimer kt_(KID_PAGED_COMMIT, stream);
     const int vecs = a.D * (a.dtype == DARTREE_BF16 ? 2 : 4) / 16;
-    const auto f = vecs == 8 ? launch_commit_t<8> : vecs == 16 ? launch_commit_t<16> : launch_commit_t<32>;
+    const auto f = weights ? (vecs == 8    ? launch_commit_t<8, true>
+                              : vecs == 16 ? launch_commit_t<16, true>
+                                           : launch_commit_t<32, true>)
+                           : (vecs == 8    ? launch_commit_t<8, false>
+                              : vecs == 16 ? launch_commit_t<16, false>
+                                           : launch_commit_t<32, false>);
     return f(cfg, a, path, accepted_len, L, weights, n_out) == cudaSuccess ? DARTREE_OK : DARTREE_ECUDA;
 }
 
