@@ -5,8 +5,9 @@
 //   S^T = K Q^T  (128 keys x 16 rows),   O^T += V^T P^T  (D x 16 rows),
 //
 // so that a block costs the tensor cores and the softmax 16 rows, not 128: there a block of
-// a lone CTA takes 1.5 us however few rows live. One token over 2048 rows: 9.2 us (10.5 there), 64
-// tokens over 4096-8192 rows: 236 us (260), 6.8 TB/s.
+// a lone CTA takes 1.5 us however few rows live. One token over 2048 rows: 9.0 us (10.5 there), 64
+// tokens over 4096-8192 rows: 236 us (260), 6.8 TB/s. P is rounded to bf16 as there: a token's
+// output has the same bound whichever kernel its batch goes to.
 //
 // CTA = (chunk of key blocks, (request, key/value head)):
 //   warps 0..3  softmax, one thread per key: its 16 scores, P in bf16 to shared memory (an

@@ -109,8 +109,8 @@ def test_two_tiles_maximum_that_keeps_growing(dd, i, fall):  # noqa: F811
     _attend(x)
 
 
-@pytest.mark.parametrize("i", [0, 1, 2, 4])
-@pytest.mark.parametrize("at", [0, 63, 64, 100, 127, 128, 200, 255, 299])
+@pytest.mark.parametrize("i", [1, 2, 4])
+@pytest.mark.parametrize("at", [0, 63, 64, 127, 200])
 def test_two_tiles_a_key_far_above_the_others(dd, i, at):  # noqa: F811
     """Both halves of a block of keys; a second key as far above the first."""
     x = _pairs(dd, i, 230 + at)
