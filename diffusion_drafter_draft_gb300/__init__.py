@@ -697,7 +697,8 @@ class PagedCache:
       q_start           [C + 1] int32 first rows of q (T rows in all); None: S tokens of
                         every request, or a tree's S slots
       ws                a workspace to use (shared by calls that follow one another on
-                        the device; the one of a larger batch will do); allocated when None
+                        the device; the one of a larger batch will do; cleared, and ordered
+                        between streams, by the caller); allocated when None
 
     The tensors are read at every call: a serving loop changes table, n_ctx and q_start
     in place. Nothing is allocated by a call that is given its outputs, so it can be

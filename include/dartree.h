@@ -358,7 +358,8 @@ DARTREE_API int dartree_paged_attention_plan(const dartree_paged_params* p, dart
  *               tree at base + tree->pos[c, j]; pairs (i, i + D/2) turn by position *
  *               theta^(-2i/D) as in dartree_tree_attention.
  *   q_out       [T, Hq, D]
- * Norm and rotation in fp32 (angles reduced in double), rounded once to dtype. All
+ * Norm and rotation in fp32 (a normed head's squares add up to less than 2^128; angles
+ * reduced in double), rounded once to dtype. All
  * pointers 16-byte aligned. q_out may be q itself when ldq = Hq * D and shares no byte
  * with q, k and v otherwise (DARTREE_EINVAL). */
 typedef struct {
@@ -378,7 +379,7 @@ DARTREE_API int dartree_paged_append(const dartree_paged_params* p, const dartre
 
 /* Attention of the new tokens (their keys and values already stored) over the pages.
  *   q     [T, Hq, D] rotated queries; query head h reads key/value head h / (Hq / Hkv)
- *   scale factor of the scores, > 0 and finite (0: 1 / sqrt(D))
+ *   scale factor of the scores, > 0 and finite (0: 1 / sqrt(D)); scaled scores stay below 2^126
  *   out   [T, Hq, D]; a token that sees no row (a tree slot with an empty mask row and
  *         no context) gives zeros
  *   lse   [T, Hq] float, natural logarithm of the sum of exponentials of a row's scaled

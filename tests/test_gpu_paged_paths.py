@@ -390,6 +390,40 @@ def test_eviction_and_commit_on_a_side_stream(dd):  # noqa: F811
     np.testing.assert_array_equal(y.host(y.v), bv)
 
 
+def test_caches_on_streams_at_once(dd):  # noqa: F811
+    """Trees in clusters, single tokens, a prompt's weights shared by clusters and a chunk through memory, each
+    with a workspace of its own on a stream of its own, give what they give alone."""
+    cases = [dict(new=[65] * 4, old=[1900, 1500, 1000, 700], S=65, tree=True, Hq=32, Hkv=8, page=64),
+             dict(new=[1] * 3, old=[2000, 900, 50], Hq=32, Hkv=8, page=64, ragged=False),
+             dict(new=[500], old=[1], Hq=32, Hkv=8, page=64, ragged=False),
+             dict(new=[33] * 8, old=[4063] * 8, Hq=32, Hkv=8, page=64)]
+    xs = [Case(dd, seed=380 + i, **kw).fill() for i, kw in enumerate(cases)]
+    ways = [_plan(dd, x) for x in xs]
+    assert ways[0].cluster and ways[1].few and ways[3].part_bytes > 0
+
+    def step(x, stream=None):
+        lse = torch.empty(x.T, x.Hq, device="cuda") if stream is None else x.lse
+        w = torch.zeros(x.C, x.Hkv, x.cache.rows, device="cuda") if stream is None else x.w
+        out = x.cache.attention(x.q, tree=x.tree, out=None if stream is None else x.out, lse=lse, stream=stream)
+        x.cache.weights(x.q, lse, w, tree=x.tree, decay=0.0 if stream is not None else 1.0, stream=stream)
+        return out, lse, w
+
+    alone = [step(x) for x in xs]
+    for x, a in zip(xs, alone):
+        x.ok()
+        _check_attention(x, a[0], a[1], most=4)
+        x.out, x.lse, x.w = (torch.zeros_like(t) for t in a)
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(40):
+        for x, s in zip(xs, streams):
+            step(x, s)
+    torch.cuda.synchronize()
+    for x, a in zip(xs, alone):
+        x.ok()
+        assert torch.equal(x.out, a[0]) and torch.equal(x.lse, a[1]) and torch.equal(x.w, a[2])
+
+
 def test_a_captured_commit_and_eviction(dd):  # noqa: F811
     """Captured together, the commit's lengths feeding the eviction; replayed on other paths, weights, lengths
     and rows."""
