@@ -17,7 +17,7 @@ __all__ = [
     "workspace_bytes", "new_workspace", "topk", "expand", "prune", "tree_mask", "build_tree",
     "verify", "read_status", "clear_status", "Round", "EXPORTS", "heap_build", "HeapRound",
     "verify_sample", "adaptive_budget", "lm_head_topk", "tree_attention", "AttnParams", "HostRounds",
-    "HostInputs", "HostOutputs", "PagedCache",
+    "HostInputs", "HostOutputs", "PagedCache", "sample", "verify_filtered",
 ]
 
 F32, BF16 = 0, 1
@@ -33,7 +33,8 @@ EXPORTS = ("dartree_head_init", "dartree_workspace_bytes", "dartree_topk", "dart
            "dartree_lm_head_topk", "dartree_tree_attention_workspace_bytes", "dartree_tree_attention", "dartree_host_session_create",
            "dartree_host_session_destroy", "dartree_host_stage", "dartree_host_round", "dartree_host_input_bytes",
            "dartree_paged_workspace_bytes", "dartree_paged_attention_plan", "dartree_paged_append",
-           "dartree_paged_attention", "dartree_paged_weights", "dartree_paged_evict", "dartree_paged_commit", "dartree_paged_commit_weights")
+           "dartree_paged_attention", "dartree_paged_weights", "dartree_paged_evict", "dartree_paged_commit", "dartree_paged_commit_weights",
+           "dartree_paged_reserve", "dartree_paged_release", "dartree_sample", "dartree_verify_filtered")
 
 
 class DartreeError(RuntimeError):
@@ -83,6 +84,17 @@ class PagedTokens(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("ldq", ctypes.c_int64),
                 ("ldk", ctypes.c_int64), ("ldv", ctypes.c_int64), ("gq", ctypes.c_void_p), ("gk", ctypes.c_void_p),
                 ("pos_base", ctypes.c_void_p), ("eps", ctypes.c_float), ("theta", ctypes.c_float)]
+
+
+class PagedStep(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("table", "n_ctx", "n_new", "free_pages", "n_free", "n_free_out", "granted",
+                                               "q_start", "slot", "pos", "request")]
+
+
+class Filter(ctypes.Structure):
+    _fields_ = [("temperature", ctypes.c_float), ("top_k", ctypes.c_int), ("top_p", ctypes.c_float),
+                ("min_p", ctypes.c_float)] + [(n, ctypes.c_void_p) for n in ("temperatures", "top_ks", "top_ps",
+                                                                             "min_ps")]
 
 
 class Tree(ctypes.Structure):
@@ -153,6 +165,10 @@ def lib() -> ctypes.CDLL:
                                       ctypes.c_float, vp, vp, sz, vp]),
         "dartree_paged_evict": (i, [P(PagedParams), P(PagedCacheDesc), vp, i, i, i, vp, i, vp, vp, vp, vp, sz, vp]),
         "dartree_paged_commit": (i, [P(PagedParams), P(PagedCacheDesc), vp, vp, i, vp, vp, sz, vp]),
+        "dartree_paged_reserve": (i, [P(PagedParams), P(PagedStep), vp, sz, vp]),
+        "dartree_paged_release": (i, [P(PagedParams), vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "dartree_sample": (i, [vp, i, i, ctypes.c_int64, i, P(Filter), vp, vp, vp, sz, vp]),
+        "dartree_verify_filtered": (i, [P(Params), P(Tree), vp, i, i, i, P(Filter), vp, vp, vp, vp, vp, sz, vp]),
         "dartree_paged_commit_weights": (i, [P(PagedParams), P(PagedCacheDesc), vp, vp, i, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
@@ -423,6 +439,93 @@ def verify_sample(tree, target, rows: int, L: int, temperature: float, seed: int
           int(V), _dtype_code(target), float(temperature), int(seed) & 0xFFFFFFFFFFFFFFFF,
           ctypes.c_void_p(out["accepted_len"].data_ptr()), ctypes.c_void_p(out["path"].data_ptr()),
           ctypes.c_void_p(out["bonus"].data_ptr()), ctypes.c_void_p(ws.data_ptr()), ws.numel(), _stream(stream))
+    return out
+
+
+def _filter(n, device, temperature, top_k, top_p, min_p) -> Filter:
+    """Settings of n requests: numbers, or tensors [n] on the device."""
+    f = Filter(1.0, 0, 1.0, 0.0)
+    for name, v, dt in (("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
+                        ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
+        if isinstance(v, torch.Tensor):
+            setattr(f, name + "s", _need(v, name, dt, (n,)) if n else None)
+            if v.device != device:
+                raise ValueError(f"{name} must be on {device}, got {v.device}")
+        elif dt is torch.int32:
+            if int(v) != v or not -2 ** 31 <= v < 2 ** 31:
+                raise ValueError(f"{name} must be a whole number")
+            f.top_k = int(v)
+        else:
+            setattr(f, name, float(v))
+    return f
+
+
+def _same_device(device, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None, ws=None, stream=None):
+    """A token for each row of logits [rows, V] (rows may lie further apart) under temperature, top-k, top-p and
+    min-p, from one uniform number u [rows] (float32 in [0, 1)) a row (dartree_sample) -> int32 [rows]; -1 for a
+    row of -inf. Settings are numbers or tensors [rows]. read_status(ws) tells of entries that are no settings."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2 or not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor [rows, V]")
+    rows, V = logits.shape
+    ld = logits.stride(0) if rows > 1 else V
+    if logits.stride(1) != 1 and V > 1:
+        raise ValueError("the logits of a row must be contiguous")
+    dev = logits.device
+    _need(u, "u", torch.float32, (rows,))
+    with torch.cuda.device(dev):
+        with torch.cuda.stream(stream):
+            if out is None:
+                out = torch.empty((rows,), dtype=torch.int32, device=dev)
+            if ws is None:
+                ws = new_workspace(256, dev)
+        _need(out, "out", torch.int32, (rows,))
+        _need(ws, "ws", torch.uint8)
+        _same_device(dev, u=u, out=out, ws=ws)
+        f = _filter(rows, dev, temperature, top_k, top_p, min_p)
+        _call("dartree_sample", logits.data_ptr(), rows, V, ld, _dtype_code(logits), ctypes.byref(f), u.data_ptr(),
+              out.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
+    return out
+
+
+def verify_filtered(tree, target, rows: int, L: int, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None,
+                    ws=None, stream=None):
+    """S10 on draws under temperature, top-k, top-p and min-p (dartree_verify_filtered): target and u as the row
+    mode says, u [C, L] or [C, B+1] float32 in [0, 1); settings are numbers or tensors [C]
+    -> dict(accepted_len, path, bonus)."""
+    C, S = tree["tok"].shape
+    V = target.shape[-1]
+    n = L if rows == ROWS_PER_POSITION else S
+    _need(target, "target", None, (C, n, V))
+    _need(u, "u", torch.float32, (C, n))
+    dev = target.device
+    for k in ("tok", "par", "depth"):
+        _need(tree[k], f"tree[{k!r}]", torch.int32, (C, S))
+    _need(tree["n_nodes"], "tree['n_nodes']", torch.int32, (C,))
+    _same_device(dev, u=u, out=out["path"] if out else None, ws=ws,
+                 **{k: tree[k] for k in ("tok", "par", "depth", "n_nodes")})
+    with torch.cuda.device(dev):
+        with torch.cuda.stream(stream):
+            if out is None:
+                out = dict(accepted_len=torch.empty((C,), dtype=torch.int32, device=dev),
+                           path=torch.empty((C, L), dtype=torch.int32, device=dev),
+                           bonus=torch.empty((C,), dtype=torch.int32, device=dev))
+            if ws is None:
+                ws = new_workspace(256, dev)
+        for k, shape in (("accepted_len", (C,)), ("path", (C, L)), ("bonus", (C,))):
+            _need(out[k], k, torch.int32, shape)
+        _need(ws, "ws", torch.uint8)
+        f = _filter(C, dev, temperature, top_k, top_p, min_p)
+        p = _params(C, L, 1, 1, S - 1, 0.0)
+        ts = _tree_struct({k: tree[k] for k in ("tok", "par", "depth", "n_nodes")})
+        _call("dartree_verify_filtered", ctypes.byref(p), ctypes.byref(ts), target.data_ptr(), int(rows), V,
+              _dtype_code(target), ctypes.byref(f), u.data_ptr(), out["accepted_len"].data_ptr(),
+              out["path"].data_ptr(), out["bonus"].data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
     return out
 
 
@@ -753,7 +856,8 @@ class PagedCache:
         self.rows = self.max_pages * self.page
         L = lib()
         self._fn = {n: getattr(L, "dartree_paged_" + n)
-                    for n in ("append", "attention", "weights", "evict", "commit", "commit_weights")}
+                    for n in ("append", "attention", "weights", "evict", "commit", "commit_weights", "reserve",
+                              "release")}
         self._pp, self._mp = ctypes.byref(self.p), ctypes.byref(self._m)
         self._t = Tree()
         self._tp = ctypes.byref(self._t)
@@ -931,4 +1035,46 @@ class PagedCache:
         else:
             wp = self._need(weights, "weights", torch.float32, self._shapes["w"])
             self._run("commit_weights", stream, self._pp, self._mp, pp, ap, L, wp, op)
+        return n_out
+
+    def reserve(self, n_new, free, n_free, out=None, stream=None):
+        """Pages and rows for a step's new tokens (dartree_paged_reserve): request c wants n_new[c] tokens (0..S,
+        int32 [C]) behind its n_ctx[c] rows. The pages it still needs come from the end of the stack free
+        (int32, n_free [1] of them) into the cache's table; a request that does not fit is granted nothing.
+        The cache's q_start, if it has one, is written. -> dict(granted [C], slot [T] int64, pos [T],
+        request [T], n_free [1]); out: the same tensors, made before (n_free may be n_free itself, slot, pos
+        and request None)."""
+        np_ = self._need(n_new, "n_new", torch.int32, self._shapes["C"])
+        fp, nf = self._stack(free, n_free)
+        if out is None:
+            new = lambda n, dt: self._new(torch.empty, (n,), dt, stream)  # noqa: E731
+            out = dict(granted=new(self.C, torch.int32), slot=new(self.T, torch.int64), pos=new(self.T, torch.int32),
+                       request=new(self.T, torch.int32), n_free=new(1, torch.int32))
+        x = PagedStep(self._m.table, self._m.n_ctx, np_, fp, nf)
+        x.n_free_out = self._need(out["n_free"], "n_free", torch.int32, (1,))
+        x.granted = self._need(out["granted"], "granted", torch.int32, self._shapes["C"])
+        x.q_start = self._m.q_start
+        for k, dt in (("slot", torch.int64), ("pos", torch.int32), ("request", torch.int32)):
+            if out.get(k) is not None:
+                setattr(x, k, self._need(out[k], k, dt, (self.T,)))
+        self._run("reserve", stream, self._pp, ctypes.byref(x))
+        return out
+
+    def _stack(self, free, n_free):
+        if not isinstance(free, torch.Tensor) or free.dim() != 1 or free.numel() < self.n_pages:
+            raise ValueError("free must have room for the pool's pages, [n_pages]")
+        return self._need(free, "free", torch.int32, free.shape), self._need(n_free, "n_free", torch.int32, (1,))
+
+    def release(self, n_held, n_keep, free, n_free, n_shared=None, n_out=None, stream=None):
+        """The pages behind the first max(n_keep, n_shared) of each request's n_held rows (int32 [C] each) put on the
+        stack free, [n_pages], of n_free [1] pages (dartree_paged_release) -> pages on it then, [1] (n_out, which may
+        be n_free itself)."""
+        hp = self._need(n_held, "n_held", torch.int32, self._shapes["C"])
+        kp = self._need(n_keep, "n_keep", torch.int32, self._shapes["C"])
+        sp = None if n_shared is None else self._need(n_shared, "n_shared", torch.int32, self._shapes["C"])
+        fp, nf = self._stack(free, n_free)
+        if n_out is None:
+            n_out = self._new(torch.empty, (1,), torch.int32, stream)
+        op = self._need(n_out, "n_out", torch.int32, (1,))
+        self._run("release", stream, self._pp, self._m.table, hp, kp, sp, fp, nf, op)
         return n_out

@@ -509,6 +509,47 @@ int dartree_verify_sample(const dartree_params* p, const dartree_tree* tree, con
                                 bonus, at<int>(ws, 0), as_stream(stream));
 }
 
+static int check_filter(const dartree_filter* f) {
+    if (!f) return DARTREE_EINVAL;
+    if (!f->temperatures && !(f->temperature >= 0.f && isfinite(f->temperature))) return DARTREE_EINVAL;
+    if (!f->top_ks && f->top_k < 0) return DARTREE_EINVAL;
+    if (!f->top_ps && !(f->top_p >= 0.f && f->top_p <= 1.f)) return DARTREE_EINVAL;
+    if (!f->min_ps && !(f->min_p >= 0.f && f->min_p <= 1.f)) return DARTREE_EINVAL;
+    return DARTREE_OK;
+}
+
+int dartree_sample(const void* logits, int rows, int V, int64_t ld, int dtype, const dartree_filter* f, const float* u,
+                   int32_t* tok, void* ws, size_t ws_bytes, void* stream) {
+    if (rows < 0 || V < 1 || ld < V) return DARTREE_EINVAL;
+    if (!dtype_ok(dtype)) return DARTREE_EDTYPE;
+    if (int e = check_filter(f)) return e;
+    if (!sample_supported(V, dtype) || rows >= (1 << 24)) return DARTREE_EUNSUPPORTED;
+    if (rows == 0) return DARTREE_OK;
+    if (!logits || reinterpret_cast<uintptr_t>(logits) % (dtype == DARTREE_BF16 ? 2 : 4) != 0 || !u || !tok)
+        return DARTREE_EINVAL;
+    if (int e = check_ws(ws, ws_bytes, kAlign)) return e;
+    return launch_sample(logits, rows, V, ld, dtype, *f, u, tok, at<int>(ws, 0), as_stream(stream));
+}
+
+int dartree_verify_filtered(const dartree_params* p, const dartree_tree* tree, const void* target, int rows, int V,
+                            int dtype, const dartree_filter* f, const float* u, int32_t* accepted_len, int32_t* path,
+                            int32_t* bonus, void* ws, size_t ws_bytes, void* stream) {
+    if (!p || p->C < 0 || p->L < 1 || p->B < 1 || V < 1) return DARTREE_EINVAL;
+    if (!dtype_ok(dtype) || (rows != DARTREE_ROWS_PER_POSITION && rows != DARTREE_ROWS_PER_NODE))
+        return DARTREE_EDTYPE;
+    if (int e = check_filter(f)) return e;
+    if (p->L > DARTREE_MAX_L || p->B + 1 > DARTREE_MAX_SLOTS || !sample_supported(V, dtype) || p->C >= (1 << 24))
+        return DARTREE_EUNSUPPORTED;
+    if (p->C == 0) return DARTREE_OK;
+    if (!tree || !tree->tok || !tree->par || !tree->depth || !tree->n_nodes || !target ||
+        reinterpret_cast<uintptr_t>(target) % (dtype == DARTREE_BF16 ? 2 : 4) != 0 || !u || !accepted_len || !path ||
+        !bonus)
+        return DARTREE_EINVAL;
+    if (int e = check_ws(ws, ws_bytes, kAlign)) return e;
+    return launch_sample_walk(p->C, p->L, p->B, tree->tok, tree->par, tree->depth, tree->n_nodes, target, rows, V,
+                              dtype, *f, u, accepted_len, path, bonus, at<int>(ws, 0), as_stream(stream));
+}
+
 size_t dartree_lm_head_workspace_bytes(int R, int V, int H, int K) {
     if (!lmhead_supported(R, V, H, K)) return 0;
     return kAlign + up(lmhead_part_bytes(R < 64 ? R : 64, V, K));
@@ -764,6 +805,35 @@ int dartree_paged_commit_weights(const dartree_paged_params* p, const dartree_pa
                                  const int32_t* accepted_len, int L, float* weights, int32_t* n_out, void* ws,
                                  size_t ws_bytes, void* stream) {
     return paged_commit(p, cache, path, accepted_len, L, true, weights, n_out, ws, ws_bytes, stream);
+}
+
+int dartree_paged_reserve(const dartree_paged_params* p, const dartree_paged_step* x, void* ws, size_t ws_bytes,
+                          void* stream) {
+    PagedArgs a;
+    if (int e = check_paged(p, &a)) return e;
+    if (!x || !x->n_free || !x->n_free_out || a.n_pages < 1 || a.max_pages < 1) return DARTREE_EINVAL;
+    if (!x->q_start && int64_t(a.C) * a.S != a.T) return DARTREE_EINVAL;
+    if (a.C > 0 && (!x->table || !x->n_ctx || !x->n_new || !x->free_pages || !x->granted ||
+                    overlap(x->granted, int64_t(a.C) * 4, x->n_new, int64_t(a.C) * 4)))
+        return DARTREE_EINVAL;
+    if (x->slot && reinterpret_cast<uintptr_t>(x->slot) % 8 != 0) return DARTREE_EINVAL;
+    if (int e = check_ws(ws, ws_bytes, paged_layout(a).part)) return e;
+    a.status = at<int>(ws, 0);
+    return launch_paged_reserve(a, *x, as_stream(stream));
+}
+
+int dartree_paged_release(const dartree_paged_params* p, const int32_t* table, const int32_t* n_held,
+                          const int32_t* n_keep, const int32_t* n_shared, int32_t* free_pages, const int32_t* n_free,
+                          int32_t* n_free_out, void* ws, size_t ws_bytes, void* stream) {
+    PagedArgs a;
+    if (int e = check_paged(p, &a)) return e;
+    if (!n_free || !n_free_out || a.n_pages < 1 || a.max_pages < 1) return DARTREE_EINVAL;
+    if (a.C > 0 && (!table || !n_held || !n_keep || !free_pages ||
+                    overlap(free_pages, int64_t(a.n_pages) * 4, table, int64_t(a.C) * a.max_pages * 4)))
+        return DARTREE_EINVAL;
+    if (int e = check_ws(ws, ws_bytes, paged_layout(a).part)) return e;
+    a.status = at<int>(ws, 0);
+    return launch_paged_release(a, table, n_held, n_keep, n_shared, free_pages, n_free, n_free_out, as_stream(stream));
 }
 
 int dartree_adaptive_budget(int C, int* B, int* W) {

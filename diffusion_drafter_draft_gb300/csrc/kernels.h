@@ -34,7 +34,8 @@ enum KernelId {
     KID_TOPK_ROWS = 0, KID_TOPK_STREAM, KID_GEMM, KID_CONTRACT, KID_EXPAND_G, KID_GATHER, KID_SELECT,
     KID_STATE, KID_HEAP, KID_FINISH, KID_PRUNE, KID_MASK, KID_ROWMAX, KID_WALK, KID_ROWSAMPLE, KID_LMHEAD,
     KID_LMMERGE, KID_ATTN_PREP, KID_ATTN, KID_ATTN_COMBINE, KID_PAGED_APPEND, KID_PAGED_ATTN,
-    KID_PAGED_COMBINE, KID_PAGED_WEIGHTS, KID_PAGED_SELECT, KID_PAGED_MOVE, KID_PAGED_COMMIT, KID_OTHER,
+    KID_PAGED_COMBINE, KID_PAGED_WEIGHTS, KID_PAGED_SELECT, KID_PAGED_MOVE, KID_PAGED_COMMIT, KID_PAGED_RESERVE,
+    KID_PAGED_RELEASE, KID_SAMPLE, KID_SAMPLE_WALK, KID_OTHER,
     KID_COUNT
 };
 // Brackets the launches of its scope with timing events when timing is enabled.
@@ -301,6 +302,20 @@ int launch_paged_evict(const PagedArgs& a, const float* weights, int budget, int
                        int32_t* counts, cudaStream_t stream);
 int launch_paged_commit(const PagedArgs& a, const int32_t* path, const int32_t* accepted_len, int L, float* weights,
                         int32_t* n_out, cudaStream_t stream);
+
+int launch_paged_reserve(const PagedArgs& a, const dartree_paged_step& x, cudaStream_t stream);
+int launch_paged_release(const PagedArgs& a, const int32_t* table, const int32_t* n_held, const int32_t* n_keep,
+                         const int32_t* n_shared, int32_t* free_pages, const int32_t* n_free, int32_t* n_free_out,
+                         cudaStream_t stream);
+
+// Draws under temperature, top-k, top-p and min-p: a token for each row, and a tree's walk.
+bool sample_supported(int V, int dtype);
+int launch_sample(const void* logits, int rows, int V, int64_t ld, int dtype, const dartree_filter& f, const float* u,
+                  int32_t* tok, int* status, cudaStream_t stream);
+int launch_sample_walk(int C, int L, int B, const int32_t* tok, const int32_t* par, const int32_t* depth,
+                       const int32_t* n_nodes, const void* target, int rows_mode, int V, int dtype,
+                       const dartree_filter& f, const float* u, int32_t* accepted, int32_t* path, int32_t* bonus,
+                       int* status, cudaStream_t stream);
 
 // Bounded-wait self-test (which = 0: mbarrier, 1: grid barrier on ctr).
 int launch_selftest_wait(int which, unsigned* ctr, int* status, uint64_t limit_ns, cudaStream_t stream);

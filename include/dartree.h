@@ -228,6 +228,50 @@ DARTREE_API int dartree_verify_sample(const dartree_params* p, const dartree_tre
                                       int32_t* accepted_len, int32_t* path, int32_t* bonus, void* ws,
                                       size_t ws_bytes, void* stream);
 
+/* Settings of a draw from logits x, applied in this order, w_v = exp((x_v - max x) / temperature):
+ *   top_k   the first k in the order (logit descending, token ascending); 0: all
+ *   top_p   of those the smallest leading set that holds top_p of their weight, at least the first
+ *   min_p   of those the tokens with w_v >= min_p (the first always stays)
+ * temperature 0, top_k 1 and top_p 0 give the largest logit's token (the lowest among equals). A number holds
+ * for every request, an array [requests] (device) takes its place. */
+typedef struct {
+    float temperature;            /* >= 0, finite */
+    int top_k;                    /* >= 0 */
+    float top_p;                  /* 0..1 */
+    float min_p;                  /* 0..1 */
+    const float* temperatures;    /* or NULL */
+    const int32_t* top_ks;
+    const float* top_ps;
+    const float* min_ps;
+} dartree_filter;
+
+/* A token for each row of logits under `f`, from one uniform number u in [0, 1) a row: the lowest token at
+ * which the sum of the kept w_0 .. w_v passes u times their whole sum. -inf is never drawn, nor is
+ * NaN (counted as -inf); where the maximum is +inf, the tokens that reach it share the weight; a row
+ * of -inf alone gives -1. Sums are exact sums of weights rounded to 2^-42 of the largest:
+ * a row's token does not depend on the batch it is in.
+ *   logits  [rows, V], consecutive rows ld >= V elements apart, aligned to their type
+ *   f       one request to a row
+ *   u       [rows]
+ *   tok     [rows]
+ * Numbers that are no settings give DARTREE_EINVAL; entries of arrays and u are checked on the device and
+ * give DARTREE_EINTERNAL in the status word of ws (256 bytes): a temperature taken for 0, other
+ * settings for none, u for 0. V at most 2^20, and rows of at most 190 kB for each of eight CTAs
+ * (DARTREE_EUNSUPPORTED: fp32 beyond 389 thousand tokens, bf16 beyond 778). */
+DARTREE_API int dartree_sample(const void* logits, int rows, int V, int64_t ld, int dtype, const dartree_filter* f,
+                               const float* u, int32_t* tok, void* ws, size_t ws_bytes, void* stream);
+
+/* S10 on such draws: the walk of dartree_verify_sample with the token of dartree_sample from the current slot's
+ * target row and its u (one of `f` to a request). Every emitted token is a draw of the filtered target.
+ *   u       [C, L] (DARTREE_ROWS_PER_POSITION) or [C, B+1] (DARTREE_ROWS_PER_NODE), as the rows of target
+ *   bonus   -1, too, when the last row holds nothing but -inf
+ *   other arguments, outputs and errors as for dartree_verify_sample; ws 256 bytes. Only the rows on the
+ * walk are read. */
+DARTREE_API int dartree_verify_filtered(const dartree_params* p, const dartree_tree* tree, const void* target,
+                                        int rows, int V, int dtype, const dartree_filter* f, const float* u,
+                                        int32_t* accepted_len, int32_t* path, int32_t* bonus, void* ws,
+                                        size_t ws_bytes, void* stream);
+
 /* The block drafter's LM head fused with S1 (DARTree blog post, "3.1 Basic flow",
  * candidate generation: the top-K tokens of every block position's base logits).
  * The base logits L[r, v] = <hidden[r], W_lm[v]> (a linear head without bias; the
@@ -449,6 +493,56 @@ DARTREE_API int dartree_paged_commit_weights(const dartree_paged_params* p, cons
                                              const int32_t* path, const int32_t* accepted_len, int L, float* weights,
                                              int32_t* n_out, void* ws, size_t ws_bytes, void* stream);
 
+/* Pages and rows for a step's new tokens, from the requests' lengths: request c with n_ctx[c] cached
+ * rows wants n_new[c] more. It needs ceil((n_ctx + n_new) / page) - ceil(n_ctx / page) pages
+ * beyond those that its first n_ctx rows take, and gets them from the end of a stack of free pages
+ * (the i-th page that the step takes is free_pages[n_free - 1 - i]). Requests are served in their
+ * order; one whose pages, tokens (T rows of q with q_start) or row of the block table do not
+ * suffice is granted nothing, and those behind it are served from what is left.
+ *   table       [C, max_pages] entries of the new pages written (the cache's; others not touched)
+ *   n_ctx       [C] rows cached
+ *   n_new       [C] tokens wanted, 0..S (tree->n_nodes, say)
+ *   free_pages  the stack, at least n_free entries; read only
+ *   n_free      [1] pages on the stack, 0..n_pages; n_free_out [1]: what is left (may be n_free itself)
+ *   granted     [C] n_new[c], or 0 (not part of n_new)
+ *   q_start     [C + 1] first rows of q of the granted tokens, as the other calls read them, or NULL:
+ *               S rows of q to every request (T = C * S)
+ *   slot        [T] place of each row of q in the pools: page * page size + row in it; -1: no token
+ *   pos         [T] its position n_ctx[c] + i; -1
+ *   request     [T] its request; -1
+ *   slot, pos and request may be NULL.
+ * Checked on the device, with DARTREE_EINTERNAL in the status word: n_free outside 0..n_pages (clamped),
+ * n_ctx outside the block table's rows and n_new outside 0..S (granted nothing), pages that are none
+ * of the pool (their entries are written as they are, their slots are -1). */
+typedef struct {
+    int32_t* table;
+    const int32_t* n_ctx;
+    const int32_t* n_new;
+    const int32_t* free_pages;
+    const int32_t* n_free;
+    int32_t* n_free_out;
+    int32_t* granted;
+    int32_t* q_start;
+    int64_t* slot;
+    int32_t* pos;
+    int32_t* request;
+} dartree_paged_step;
+DARTREE_API int dartree_paged_reserve(const dartree_paged_params* p, const dartree_paged_step* x, void* ws,
+                                      size_t ws_bytes, void* stream);
+
+/* Pages go back: of request c, whose first n_held[c] rows have pages, those behind its first
+ * max(n_keep[c], n_shared[c]) rows are put on the stack, in the requests' order and each request's from
+ * the first on. For a finished request n_keep is 0, after a commit the rows cached then.
+ *   table       [C, max_pages]; not written (entries behind a request's rows are never read)
+ *   n_shared    [C] leading rows whose pages are not the request's to give, or NULL: none
+ *   free_pages  the stack, room for n_pages entries; n_free, n_free_out as for dartree_paged_reserve
+ * DARTREE_EINTERNAL in the status word: n_free outside 0..n_pages, lengths below zero or past the block
+ * table, more pages than the pool has (left out), entries that are no page (passed on as they are). */
+DARTREE_API int dartree_paged_release(const dartree_paged_params* p, const int32_t* table, const int32_t* n_held,
+                                      const int32_t* n_keep, const int32_t* n_shared, int32_t* free_pages,
+                                      const int32_t* n_free, int32_t* n_free_out, void* ws, size_t ws_bytes,
+                                      void* stream);
+
 /* Node budget and width for a batch of C concurrent requests (DARTree blog post,
  * section 4.4: at concurrency 4 the budget B shrinks from 64 to 32 and the width W
  * from 12 to 3; at concurrency 1 and 2 the defaults run). Reading: the reduced pair
@@ -585,7 +679,7 @@ DARTREE_API int dartree_selftest_wait(void* ws, size_t ws_bytes, int which, unsi
  * device time. Kernel ids 0..DARTREE_NUM_KERNEL_IDS-1, named by
  * dartree_kernel_name. Not for launches captured into a CUDA graph; adds two
  * event records per launch while on. */
-#define DARTREE_NUM_KERNEL_IDS 28
+#define DARTREE_NUM_KERNEL_IDS 32
 DARTREE_API int dartree_timing(int enable);
 DARTREE_API int dartree_timing_read(int kernel_id, int* launches, double* total_ms);
 DARTREE_API const char* dartree_kernel_name(int kernel_id);

@@ -1,0 +1,120 @@
+"""The entry points of a serving step reject bad arguments on the host, before any CUDA call (no GPU
+needed; the fake pointers are never dereferenced)."""
+import ctypes
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def dd():
+    from diffusion_drafter_draft_gb300 import _build
+    _build.build()
+    import diffusion_drafter_draft_gb300 as m
+    m.lib()
+    return m
+
+
+FAKE, WS = ctypes.c_void_p(256), ctypes.c_void_p(1 << 20)
+GOOD = dict(C=2, T=6, S=3, Hq=8, Hkv=2, D=128, page=64, n_pages=8, max_pages=4, dtype=1)
+NAN, INF = float("nan"), float("inf")
+
+
+def _p(dd, **kw):
+    return dd.PagedParams(**{**GOOD, **kw})
+
+
+def _filter(dd, **kw):
+    return dd.Filter(**{**dict(temperature=0.7, top_k=20, top_p=0.9, min_p=0.0), **kw})
+
+
+BAD_FILTERS = [dict(temperature=-1.0), dict(temperature=NAN), dict(temperature=INF), dict(top_k=-1), dict(top_p=-0.1),
+               dict(top_p=1.5), dict(top_p=NAN), dict(min_p=-0.1), dict(min_p=1.1), dict(min_p=NAN)]
+
+
+def test_sample_arguments(dd):
+    L = dd.lib()
+
+    def call(x=FAKE, rows=2, V=100, ld=100, dtype=1, f=None, u=FAKE, tok=FAKE, ws=WS, n=256):
+        return L.dartree_sample(x, rows, V, ld, dtype, ctypes.byref(f or _filter(dd)), u, tok, ws, n, None)
+
+    for kw in BAD_FILTERS:
+        assert call(f=_filter(dd, **kw)) == dd.EINVAL, kw
+    for kw in (dict(rows=-1), dict(V=0), dict(ld=99), dict(x=None), dict(x=ctypes.c_void_p(257)), dict(u=None),
+               dict(tok=None), dict(x=ctypes.c_void_p(258), dtype=0)):
+        assert call(**kw) == dd.EINVAL, kw
+    assert L.dartree_sample(FAKE, 2, 100, 100, 1, None, FAKE, FAKE, WS, 256, None) == dd.EINVAL
+    assert call(dtype=3) == dd.EDTYPE
+    assert call(V=(1 << 20) + 1, ld=1 << 21) == dd.EUNSUPPORTED
+    assert call(V=400000, ld=400000, dtype=0) == dd.EUNSUPPORTED
+    assert call(rows=1 << 24) == dd.EUNSUPPORTED
+    assert call(ws=None) == dd.EWORKSPACE
+    assert call(ws=ctypes.c_void_p((1 << 20) + 8)) == dd.EWORKSPACE
+    assert call(n=255) == dd.EWORKSPACE
+    assert call(rows=0) == dd.OK
+    # arrays take the place of numbers
+    assert call(rows=0, f=_filter(dd, temperature=NAN, temperatures=256, top_p=NAN, top_ps=256, top_k=-1, top_ks=256,
+                                  min_p=NAN, min_ps=256)) == dd.OK
+
+
+def test_verify_filtered_arguments(dd):
+    L = dd.lib()
+    tree = dict(tok=256, par=256, depth=256, n_nodes=256)
+
+    def call(p=None, tree=tree, x=FAKE, rows=0, V=100, dtype=1, f=None, u=FAKE, out=FAKE, ws=WS, n=256):
+        t = dd.Tree(tree["tok"], tree["par"], tree["depth"], None, tree["n_nodes"], None, None)
+        return L.dartree_verify_filtered(ctypes.byref(p or dd.Params(2, 4, 1, 1, 8, 0.0)), ctypes.byref(t), x, rows, V,
+                                         dtype, ctypes.byref(f or _filter(dd)), u, out, FAKE, FAKE, ws, n, None)
+
+    for kw in BAD_FILTERS:
+        assert call(f=_filter(dd, **kw)) == dd.EINVAL, kw
+    for kw in (dict(V=0), dict(x=None), dict(u=None), dict(out=None), dict(x=ctypes.c_void_p(257)),
+               dict(p=dd.Params(-1, 4, 1, 1, 8, 0.0)), dict(p=dd.Params(2, 0, 1, 1, 8, 0.0)),
+               dict(p=dd.Params(2, 4, 1, 1, 0, 0.0))):
+        assert call(**kw) == dd.EINVAL, kw
+    for k in tree:
+        assert call(tree={**tree, k: None}) == dd.EINVAL, k
+    assert call(rows=2) == dd.EDTYPE
+    assert call(dtype=2) == dd.EDTYPE
+    assert call(p=dd.Params(2, 65, 1, 1, 8, 0.0)) == dd.EUNSUPPORTED
+    assert call(p=dd.Params(2, 4, 1, 1, 1024, 0.0)) == dd.EUNSUPPORTED
+    assert call(V=(1 << 20) + 1) == dd.EUNSUPPORTED
+    assert call(n=255) == dd.EWORKSPACE
+    assert call(p=dd.Params(0, 4, 1, 1, 8, 0.0)) == dd.OK
+
+
+def test_reserve_and_release_arguments(dd):
+    L = dd.lib()
+    need = L.dartree_paged_workspace_bytes(ctypes.byref(_p(dd)))
+    names = ("table", "n_ctx", "n_new", "free_pages", "n_free", "n_free_out", "granted", "q_start", "slot", "pos", "request")
+
+    def res(p=None, n=None, **kw):
+        x = dd.PagedStep(**{**{k: 4096 * (i + 1) for i, k in enumerate(names)}, **kw})
+        return L.dartree_paged_reserve(ctypes.byref(p or _p(dd)), ctypes.byref(x), WS, need if n is None else n, None)
+
+    for k in ("table", "n_ctx", "n_new", "free_pages", "n_free", "n_free_out", "granted"):
+        assert res(**{k: None}) == dd.EINVAL, k
+    assert res(granted=3 * 4096 + 4) == dd.EINVAL              # in n_new's last entry
+    assert res(slot=4100) == dd.EINVAL
+    assert res(p=_p(dd, T=7), q_start=None) == dd.EINVAL
+    assert res(p=_p(dd, n_pages=0)) == dd.EINVAL
+    assert res(p=_p(dd, max_pages=0)) == dd.EINVAL
+    assert res(p=_p(dd, page=24)) == dd.EUNSUPPORTED
+    assert res(n=511) == dd.EWORKSPACE
+    assert L.dartree_paged_reserve(ctypes.byref(_p(dd)), None, WS, need, None) == dd.EINVAL
+
+    def rel(p=None, n=None, **kw):
+        a = {**dict(table=1 << 16, held=4096, keep=8192, shared=None, free=1 << 17, nf=12288, out=12288), **kw}
+        return L.dartree_paged_release(ctypes.byref(p or _p(dd)), *(ctypes.c_void_p(a[k]) for k in (
+            "table", "held", "keep", "shared", "free", "nf", "out")), WS, need if n is None else n, None)
+
+    for k in ("table", "held", "keep", "free", "nf", "out"):
+        assert rel(**{k: None}) == dd.EINVAL, k
+    assert rel(free=(1 << 16) + 16) == dd.EINVAL               # in the table
+    assert rel(p=_p(dd, n_pages=0)) == dd.EINVAL
+    assert rel(n=511) == dd.EWORKSPACE
+
+
+def test_kernel_families_are_named(dd):
+    names = [dd.lib().dartree_kernel_name(i).decode() for i in range(dd.num_kernel_ids())]
+    for n in ("paged_reserve_kernel", "paged_release_kernel", "sample_kernel", "sample_walk_kernel"):
+        assert n in names
