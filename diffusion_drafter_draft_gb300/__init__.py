@@ -17,7 +17,7 @@ __all__ = [
     "workspace_bytes", "new_workspace", "topk", "expand", "prune", "tree_mask", "build_tree",
     "verify", "read_status", "clear_status", "Round", "EXPORTS", "heap_build", "HeapRound",
     "verify_sample", "adaptive_budget", "lm_head_topk", "tree_attention", "AttnParams", "HostRounds",
-    "HostInputs", "HostOutputs", "PagedCache", "sample", "verify_filtered",
+    "HostInputs", "HostOutputs", "PagedCache", "SharedRows", "sample", "verify_filtered",
 ]
 
 F32, BF16 = 0, 1
@@ -34,6 +34,7 @@ EXPORTS = ("dartree_head_init", "dartree_workspace_bytes", "dartree_topk", "dart
            "dartree_host_session_destroy", "dartree_host_stage", "dartree_host_round", "dartree_host_input_bytes",
            "dartree_paged_workspace_bytes", "dartree_paged_attention_plan", "dartree_paged_append",
            "dartree_paged_attention", "dartree_paged_weights", "dartree_paged_evict", "dartree_paged_commit", "dartree_paged_commit_weights",
+           "dartree_paged_shared_workspace_bytes", "dartree_paged_shared_attention", "dartree_paged_shared_plan",
            "dartree_paged_reserve", "dartree_paged_release", "dartree_sample", "dartree_verify_filtered")
 
 
@@ -77,6 +78,16 @@ class PagedCacheDesc(ctypes.Structure):
 
 class PagedPlan(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in ("few", "tiles_per_cta", "chunks", "cluster", "alone")] + \
+        [("part_bytes", ctypes.c_size_t)]
+
+
+class PagedGroups(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("G", "most_rows", "most_rest", "always")] + \
+        [(n, ctypes.c_void_p) for n in ("start", "rows")]
+
+
+class PagedSharedPlan(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("use", "few", "tiles_per_cta", "chunks", "own_chunks", "alone")] + \
         [("part_bytes", ctypes.c_size_t)]
 
 
@@ -165,6 +176,10 @@ def lib() -> ctypes.CDLL:
                                       ctypes.c_float, vp, vp, sz, vp]),
         "dartree_paged_evict": (i, [P(PagedParams), P(PagedCacheDesc), vp, i, i, i, vp, i, vp, vp, vp, vp, sz, vp]),
         "dartree_paged_commit": (i, [P(PagedParams), P(PagedCacheDesc), vp, vp, i, vp, vp, sz, vp]),
+        "dartree_paged_shared_workspace_bytes": (sz, [P(PagedParams), P(PagedGroups)]),
+        "dartree_paged_shared_plan": (i, [P(PagedParams), P(PagedGroups), P(PagedSharedPlan)]),
+        "dartree_paged_shared_attention": (i, [P(PagedParams), vp, P(PagedCacheDesc), P(Tree), P(PagedGroups),
+                                               ctypes.c_float, vp, vp, vp, sz, vp]),
         "dartree_paged_reserve": (i, [P(PagedParams), P(PagedStep), vp, sz, vp]),
         "dartree_paged_release": (i, [P(PagedParams), vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
         "dartree_sample": (i, [vp, i, i, ctypes.c_int64, i, P(Filter), vp, vp, vp, sz, vp]),
@@ -857,7 +872,7 @@ class PagedCache:
         L = lib()
         self._fn = {n: getattr(L, "dartree_paged_" + n)
                     for n in ("append", "attention", "weights", "evict", "commit", "commit_weights", "reserve",
-                              "release")}
+                              "release", "shared_attention")}
         self._pp, self._mp = ctypes.byref(self.p), ctypes.byref(self._m)
         self._t = Tree()
         self._tp = ctypes.byref(self._t)
@@ -897,27 +912,28 @@ class PagedCache:
         e.record(torch.cuda.current_stream(self.device))
         return e
 
-    def _meet(self, stream):
+    def _meet(self, stream, made, known, ws):
         """A stream other than the one that filled the workspace is about to use it."""
         if stream is None:
             stream = torch.cuda.current_stream(self.device)
         with torch.cuda.stream(stream):
-            self.ws.record_stream(stream)
+            ws.record_stream(stream)
             if not torch.cuda.is_current_stream_capturing():
-                if self._made is not None:
-                    stream.wait_event(self._made)
-                self._known.add(stream.cuda_stream)
+                if made is not None:
+                    stream.wait_event(made)
+                known.add(stream.cuda_stream)
 
-    def _run(self, name, stream, *args):
+    def _run(self, name, stream, *args, shared=None):
         # (the current stream as its handle: a torch.cuda.Stream object costs more than the launch)
         s = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(self.device.index)
-        if self._known is not None and s not in self._known:
-            self._meet(stream)
+        w = self if shared is None else shared
+        if w._known is not None and s not in w._known:
+            self._meet(stream, w._made, w._known, w.ws)
         if torch.cuda.current_device() == self.device.index:
-            rc = self._fn[name](*args, *self._wsp, s)
+            rc = self._fn[name](*args, *w._wsp, s)
         else:
             with torch.cuda.device(self.device):
-                rc = self._fn[name](*args, *self._wsp, s)
+                rc = self._fn[name](*args, *w._wsp, s)
         if rc != OK:
             raise DartreeError(rc, "dartree_paged_" + name)
 
@@ -967,15 +983,32 @@ class PagedCache:
         self._run("append", stream, self._pp, self._xp, self._mp, self._tree(tree, "pos"), op)
         return out
 
-    def attention(self, q, tree=None, scale=None, out=None, lse=None, stream=None):
+    def shared(self, start, rows, most_rows=0, most_rest=0, always=False, ws=None):
+        """Groups of requests that share their first rows, for attention(shared=): group g is requests start[g] ..
+        start[g + 1] - 1 (start [G + 1], rows [G], int32), whose first rows[g] cached rows are the same
+        (dartree_paged_shared_attention). The tensors are read at every call. most_rows, most_rest: rows shared and
+        rows of a request behind them (new tokens included) that the batch will have at most, 0: as many as the
+        table holds; they decide how the work is split, and whether rows are shared at all where that is not expected
+        to pay (always: in any case), not the result. The object keeps a workspace of its own
+        (ws: one to use, as for the cache); read_status(groups.ws) tells what the kernels found wrong."""
+        return SharedRows(self, start, rows, most_rows, most_rest, always, ws)
+
+    def attention(self, q, tree=None, scale=None, out=None, lse=None, stream=None, shared=None):
         """Attention of the new tokens, already appended, over the pages (dartree_paged_attention):
         q [T, Hq, D] rotated -> out [T, Hq, D], not q itself; lse [T, Hq] float32 is filled when given.
-        scale: None or 0 for 1 / sqrt(D)."""
+        scale: None or 0 for 1 / sqrt(D). shared: groups of requests that share rows (the cache's shared()),
+        whose shared rows are read once for the group."""
         qp = self._need(q, "q", self.dtype, self._shapes["q"])
         if out is None:
             out = self._new(torch.empty, self._shapes["q"], self.dtype, stream)
         op = self._need(out, "out", self.dtype, self._shapes["q"])
         lp = None if lse is None else self._need(lse, "lse", torch.float32, self._shapes["lse"])
+        if shared is not None:
+            if shared.cache is not self:
+                raise ValueError("shared belongs to another cache")
+            self._run("shared_attention", stream, self._pp, qp, self._mp, self._tree(tree, "mask"), shared._sp, scale or 0.0,
+                      op, lp, shared=shared)
+            return out
         self._run("attention", stream, self._pp, qp, self._mp, self._tree(tree, "mask"), scale or 0.0, op, lp)
         return out
 
@@ -1078,3 +1111,42 @@ class PagedCache:
         op = self._need(n_out, "n_out", torch.int32, (1,))
         self._run("release", stream, self._pp, self._m.table, hp, kp, sp, fp, nf, op)
         return n_out
+
+
+class SharedRows:
+    """Groups of a PagedCache's requests that share their first rows (PagedCache.shared). Streams and the workspace
+    are treated as the cache's."""
+
+    def __init__(self, cache, start, rows, most_rows=0, most_rest=0, always=False, ws=None):
+        if not isinstance(rows, torch.Tensor) or rows.dim() != 1:
+            raise ValueError("rows must be [G]")
+        G = rows.numel()
+        sp = cache._need(start, "start", torch.int32, (G + 1,))
+        rp = cache._need(rows, "rows", torch.int32, (G,))
+        self.cache, self.start, self.rows = cache, start, rows
+        self.s = PagedGroups(G, int(most_rows), int(most_rest), int(bool(always)), sp, rp)
+        self._sp = ctypes.byref(self.s)
+        self._made, self._known = None, None
+        if ws is None:
+            def make():
+                n = lib().dartree_paged_shared_workspace_bytes(ctypes.byref(cache.p), self._sp)
+                if n == 0:
+                    raise DartreeError(EUNSUPPORTED, "dartree_paged_shared_workspace_bytes")
+                w = torch.empty(n, dtype=torch.uint8, device=cache.device)
+                h = torch._C._cuda_getCurrentRawStream(cache.device.index)
+                self._known = {h}
+                self._made = cache._clear(w, h)
+                return w
+
+            ws = cache._on_device(make)
+        else:
+            cache._need(ws, "ws", torch.uint8)
+        self.ws = ws
+        self._wsp = (ws.data_ptr(), ws.numel())
+
+    def plan(self) -> PagedSharedPlan:
+        """How the attention takes these groups (dartree_paged_shared_plan)."""
+        out = PagedSharedPlan()
+        c = self.cache
+        c._on_device(lambda: _call("dartree_paged_shared_plan", ctypes.byref(c.p), self._sp, ctypes.byref(out)))
+        return out

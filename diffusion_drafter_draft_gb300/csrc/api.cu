@@ -739,6 +739,55 @@ int dartree_paged_attention(const dartree_paged_params* p, const void* q, const 
     return launch_paged_attention(a, q, scale, out, lse, at<void>(ws, l.part), as_stream(stream));
 }
 
+// Sizes of a call with shared prefixes.
+static int check_paged_groups(const dartree_paged_params* p, const dartree_paged_groups* s, PagedArgs* a) {
+    if (int e = check_paged(p, a)) return e;
+    if (a->dtype != DARTREE_BF16) return DARTREE_EUNSUPPORTED;
+    if (!s || s->G < 0 || s->G > a->C || s->most_rows < 0 || s->most_rest < 0) return DARTREE_EINVAL;
+    // (chunks and tiles of the groups: CTAs stay below 2^31)
+    if ((int64_t(a->T) + s->G) * a->Hkv * 64 >= (int64_t(1) << 31)) return DARTREE_EUNSUPPORTED;
+    return DARTREE_OK;
+}
+
+size_t dartree_paged_shared_workspace_bytes(const dartree_paged_params* p, const dartree_paged_groups* s) {
+    PagedArgs a;
+    if (check_paged_groups(p, s, &a) != DARTREE_OK) return 0;
+    const size_t part = a.C && a.T && s->G ? paged_shared_part_bytes(a, *s)
+                                           : paged_attention_part_bytes(a, false);
+    return paged_layout(a).part + up(part);
+}
+
+int dartree_paged_shared_plan(const dartree_paged_params* p, const dartree_paged_groups* s,
+                              dartree_paged_shared_plan_t* plan) {
+    PagedArgs a;
+    if (!plan) return DARTREE_EINVAL;
+    if (int e = check_paged_groups(p, s, &a)) return e;
+    if (a.C == 0 || a.T == 0 || s->G == 0) *plan = dartree_paged_shared_plan_t{};
+    else paged_shared_plan(a, *s, plan);
+    return DARTREE_OK;
+}
+
+int dartree_paged_shared_attention(const dartree_paged_params* p, const void* q, const dartree_paged_cache* cache,
+                                   const dartree_tree* tree, const dartree_paged_groups* s, float scale, void* out,
+                                   float* lse, void* ws, size_t ws_bytes, void* stream) {
+    PagedArgs a;
+    bool empty;
+    if (int e = check_paged_groups(p, s, &a)) return e;
+    if (int e = check_paged_scores(p, tree, q, cache, &scale, &a, &empty)) return e;
+    if (empty) return DARTREE_OK;
+    if (!al16(out) || (lse && reinterpret_cast<uintptr_t>(lse) % 4 != 0) || (s->G > 0 && (!s->start || !s->rows)))
+        return DARTREE_EINVAL;
+    const size_t at_part = paged_layout(a).part;
+    if (int e = check_ws(ws, ws_bytes, at_part + (s->G ? 0 : paged_attention_part_bytes(a, false)))) return e;
+    const int64_t rows = int64_t(a.T) * a.Hq, bytes = rows * a.D * 2;
+    if (overlap(out, bytes, q, bytes) || (lse && (overlap(lse, rows * 4, q, bytes) || overlap(lse, rows * 4, out, bytes))))
+        return DARTREE_EINVAL;
+    a.status = at<int>(ws, 0);
+    void* const part = at<void>(ws, at_part);
+    if (s->G == 0) return launch_paged_attention(a, q, scale, out, lse, part, as_stream(stream));
+    return launch_paged_shared(a, q, *s, scale, out, lse, part, ws_bytes - at_part, as_stream(stream));
+}
+
 int dartree_paged_weights(const dartree_paged_params* p, const void* q, const float* lse,
                           const dartree_paged_cache* cache, const dartree_tree* tree, float scale, float decay,
                           float* weights, void* ws, size_t ws_bytes, void* stream) {

@@ -295,6 +295,11 @@ size_t paged_attention_part_bytes(const PagedArgs& a, bool most);
 void paged_attention_plan(const PagedArgs& a, dartree_paged_plan* out);
 int launch_paged_attention(const PagedArgs& a, const void* q, float scale, void* out, float* lse, void* part,
                            cudaStream_t stream);
+// Attention of groups of requests that share their first rows (s.G > 0).
+size_t paged_shared_part_bytes(const PagedArgs& a, const dartree_paged_groups& s);
+void paged_shared_plan(const PagedArgs& a, const dartree_paged_groups& s, dartree_paged_shared_plan_t* out);
+int launch_paged_shared(const PagedArgs& a, const void* q, const dartree_paged_groups& s, float scale, void* out,
+                        float* lse, void* part, size_t part_bytes, cudaStream_t stream);
 int launch_paged_weights(const PagedArgs& a, const void* q, const float* lse, float scale, float decay,
                          float* weights, cudaStream_t stream);
 int launch_paged_evict(const PagedArgs& a, const float* weights, int budget, int sink, int recent,

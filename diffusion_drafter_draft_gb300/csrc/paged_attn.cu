@@ -71,11 +71,14 @@ struct PgPlan {
     int tt, tiles, nt, nchunk, rows;  // tokens per tile, tiles, tiles per CTA, chunks, rows kept per partial tile
     bool cluster, few, alone;         // the chunks merge through shared memory; at most 16 rows; a CTA per SM and tile
     size_t part_ml, total;            // workspace (partials): offset of the maxima and sums, bytes
+    double us;                        // expected time
     int64_t most_rows;                // partial rows of any plan for at most these sizes, their bytes
     size_t most;
 };
 
-template <int D, int NT, int ST, bool CL>
+// SH: a call with shared prefixes. CTAs below x.s.ctas take runs of a group's tokens over the rows that the group
+// shares (all seen by all), the others a request's tokens over its own rows, from row `kb` on.
+template <int D, int NT, int ST, bool CL, bool SH>
 __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PgArgs x) {
@@ -122,21 +125,42 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
     griddep_wait();
 
     // the last tiles (the most keys of a causal batch) first, of all heads or (x.inner) head by head
+    const bool whole = SH && blockIdx.x < x.s.ctas;                       // (over shared rows)
+    const int nchunk = whole ? x.s.np : x.nchunk;
+    const unsigned cta = SH && !whole ? blockIdx.x - x.s.ctas : blockIdx.x;
     const int ntile = (x.tiles + NT - 1) / NT;
-    const int chunk = int(blockIdx.x % x.nchunk);
-    const unsigned rest = blockIdx.x / x.nchunk, heads = a.C * a.Hkv, in = x.inner ? ntile : heads;
+    const int chunk = int(cta % nchunk);
+    const unsigned rest = cta / nchunk, heads = a.C * a.Hkv, in = x.inner ? ntile : heads;
     const int high = int(rest / in), low = int(rest - high * in);
     const int cg = x.inner ? high : low, tp = ntile - 1 - (x.inner ? low : high);
-    const int c = cg / a.Hkv, g = cg - c * a.Hkv;
+    int c = cg / a.Hkv, g = cg - c * a.Hkv;
+    int t0 = tp * NT * x.tt;                                              // first token
+    int kb = 0;                                                           // first key
     bool bad;
-    const PagedRequest r = paged_request(a, c, bad);
-    if (bad && threadIdx.x == 0 && g == 0 && tp == 0) set_status(a.status, DARTREE_EINTERNAL);
-    const int t0 = tp * NT * x.tt;                                        // first token
+    PagedRequest r;
+    if (whole) {
+        const unsigned unit = rest % x.s.units;
+        g = int(rest / x.s.units);
+        PgUnit u{0, 0, 0, 0, 0};
+        paged_shared_unit(x, unit, NT * x.tt, u, bad);
+        bad = bad && unit == 0;
+        c = u.c, t0 = u.t0;
+        r = PagedRequest{u.q0, u.n, u.keys, u.keys};
+    } else {
+        r = paged_request(a, c, bad);
+        if (SH) {
+            kb = paged_shared_rows(x, c);
+            bad |= kb > r.n_old;
+        }
+        bad = bad && tp == 0;
+    }
+    if (bad && threadIdx.x == 0 && g == 0) set_status(a.status, DARTREE_EINTERNAL);
+    const uint8_t* const mask = whole ? nullptr : a.mask;
     const int live = min(max(r.n_new - t0, 0), NT * x.tt);                // tokens
     const int nact = NT == 1 ? (live > 0) : (live + x.tt - 1) / x.tt;     // tiles with a token
-    const int end = a.mask ? r.n_keys : min(r.n_keys, r.n_old + t0 + live);
-    const int blocks = live > 0 ? (end + PG_BN - 1) / PG_BN : 0;
-    const int per = (blocks + x.nchunk - 1) / x.nchunk;
+    const int end = mask || whole ? r.n_keys : min(r.n_keys, r.n_old + t0 + live);
+    const int blocks = live > 0 ? (max(end - kb, 0) + PG_BN - 1) / PG_BN : 0;
+    const int per = (blocks + nchunk - 1) / nchunk;
     const int b0 = chunk * per, nblk = max(min(blocks, b0 + per) - b0, 0);
 
     // the softmax holds a row of scores in registers: its warpgroups take over registers that the
@@ -162,12 +186,12 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
             // this lane's table entry of block b (looked up two blocks ahead, checked when it is used), and
             // the page to fetch: n_pages, beyond the pool and so all zeros, past the end and for no page
             auto entry_of = [&](int b) -> int {
-                const int j = b * PG_BN + su * pr;
+                const int j = kb + b * PG_BN + su * pr;
                 return mine && j < r.n_keys ? table[j >> a.log2_page] : a.n_pages;
             };
             auto page_of = [&](int e, int b) -> int {
                 if (unsigned(e) < unsigned(a.n_pages)) return e;
-                if (mine && b * PG_BN + su * pr < r.n_keys) set_status(a.status, DARTREE_EINTERNAL);
+                if (mine && kb + b * PG_BN + su * pr < r.n_keys) set_status(a.status, DARTREE_EINTERNAL);
                 return a.n_pages;
             };
             int e0 = entry_of(b0), e1 = entry_of(b0 + 1), issued = 0;
@@ -186,14 +210,14 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
                     __syncwarp();
                     if (mine)
                         tc::tma_load_4d(smem + L::RING_OFF + s * L::TILE + pn * L::PANEL + size_t(su) * pr * 128,
-                                        kv ? &tmV : &tmK, 64 * pn, ((b0 + i) * PG_BN + su * pr) & (a.page - 1), g, pg,
+                                        kv ? &tmV : &tmK, 64 * pn, (kb + (b0 + i) * PG_BN + su * pr) & (a.page - 1), g, pg,
                                         &full[s]);
                     issued = idx + 1;
                 }
                 if (!ok) break;
             }
             // the last block's value rows past the end are zeroed once they have landed
-            const int have = r.n_keys - (b0 + nblk - 1) * PG_BN, vl = 2 * nblk - 1;
+            const int have = r.n_keys - kb - (b0 + nblk - 1) * PG_BN, vl = 2 * nblk - 1;
             if (have < PG_BN && issued > vl) {
                 bool ok = true;
                 if (lane == 0) ok = mbar_wait_bounded(&full[vl % ST], uint32_t(vl / ST) & 1u, a.status);
@@ -312,7 +336,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
                 const bool last = i + 1 == nblk;
                 ok = mbar_wait_bounded(&full[vi % ST], uint32_t(vi / ST) & 1u, a.status) &&
                      (last || mbar_wait_bounded(&full[ki % ST], uint32_t(ki / ST) & 1u, a.status));
-                if (ok && last && r.n_keys < (b0 + nblk) * PG_BN) ok = mbar_wait_bounded(vclean, 0, a.status);
+                if (ok && last && r.n_keys < kb + (b0 + nblk) * PG_BN) ok = mbar_wait_bounded(vclean, 0, a.status);
                 for (int t = 0; t < nact && ok; ++t) {
                     if (i > 0) ok = mbar_wait_bounded(&phalf[t], uint32_t(i - 1) & 1u, a.status);
                     if (ok) mbar_arrive(&phalf[t]);
@@ -333,9 +357,9 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
         const int row = quarter * 32 + lane;                     // row of the tile (TMEM lane)
         const int ti = row / x.grp, hg = row - ti * x.grp;
         const int i_tok = t0 + t * x.tt + ti;                    // token of the request
-        const bool slot_ok = ti < x.tt && i_tok < a.S;
+        const bool slot_ok = ti < x.tt && (whole || i_tok < a.S);
         const bool real = slot_ok && i_tok < r.n_new;
-        const int limit = !real ? 0 : a.mask ? r.n_keys : min(r.n_keys, r.n_old + i_tok + 1);
+        const int limit = !real ? 0 : mask || whole ? r.n_keys : min(r.n_keys, r.n_old + i_tok + 1);
         const bool work = __any_sync(0xffffffffu, real);         // a warp without a token forms no weights
         const uint32_t trow = tmem + (uint32_t(quarter * 32) << 16);
         const uint32_t scol = trow + uint32_t(t * PG_BN), ocol = trow + OCOL + uint32_t(t * D);
@@ -355,7 +379,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
                     const int i_q = min(t0 + t * x.tt + q0 + u, r.n_new - 1);
-                    const uint8_t* mrow = a.mask + (size_t(c) * a.S + i_q) * a.S;
+                    const uint8_t* mrow = mask + (size_t(c) * a.S + i_q) * a.S;
 #pragma unroll
                     for (int w = 0; w < 4; ++w) v[u][w] = mrow[min(max(sl + 32 * w, 0), r.n_new - 1)];
                 }
@@ -371,8 +395,8 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
         };
         if (t < nact) {
             for (int i = 0; i < nblk; ++i) {
-                const int key0 = (b0 + i) * PG_BN;
-                const bool tree = a.mask && key0 + PG_BN > r.n_old;
+                const int key0 = kb + (b0 + i) * PG_BN;
+                const bool tree = mask && key0 + PG_BN > r.n_old;
                 uint32_t bits[4];
                 if (tree && work) tree_bits(key0, bits);
                 ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&sfull[t], uint32_t(i) & 1u, a.status));
@@ -488,7 +512,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
         const bool has = ok && t < nact && nblk > 0 && real && l > 0.f;
         const bool load = ok && t < nact && nblk > 0 && work;    // (TMEM loads are warp-wide)
         const size_t orow = (size_t(r.q0) + i_tok) * a.Hq + size_t(g) * x.grp + hg;
-        if (!CL && x.nchunk == 1) {
+        if (!CL && !SH && x.nchunk == 1) {
             // tree slots without a node get zeros; rows of ragged batches only their own tokens
             const bool write = real || (slot_ok && !a.q_start);
             const float inv = has ? 1.0f / l : 0.f;
@@ -541,7 +565,8 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
             __syncwarp();
             cluster_sync();                                      // (no CTA leaves while its rows are read)
         } else {
-            const size_t pr = ((size_t(cg) * x.tiles + tp * NT + t) * x.nchunk + chunk) * x.rows + row;
+            const size_t pr = SH ? size_t(whole ? chunk : x.s.np + chunk) * (size_t(a.T) * a.Hq) + orow
+                                 : ((size_t(cg) * x.tiles + tp * NT + t) * x.nchunk + chunk) * x.rows + row;
             if (real) x.part_ml[pr] = has ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
             float4* dst = reinterpret_cast<float4*>(x.part_o + pr * D);
             if (load)
@@ -569,7 +594,8 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
 // Chunks that are no cluster. One warp per (request, token, query head): the chunks' (max, sum) pairs by the lanes in
 // parallel, then their rows of O eight at a time.
 
-template <int D>
+// SH: the chunks of the shared rows (a request without a group has none), then those of its own.
+template <int D, bool SH>
 __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constant__ PgArgs x) {
     constexpr int V = D / 32;
     const PagedArgs& a = x.a;
@@ -584,11 +610,18 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
     if (!real && a.q_start) return;
     const size_t orow = (size_t(r.q0) + i) * a.Hq + h;
     const int g = h / x.grp, tile = i / x.tt, row = (i - tile * x.tt) * x.grp + (h - g * x.grp);
-    const size_t p0 = ((size_t(c) * a.Hkv + g) * x.tiles + tile) * x.nchunk * size_t(x.rows) + row;
+    // (chunk k of this row lies at p0 + k * step)
+    int first = 0, n = x.nchunk;
+    size_t step = x.rows, p0 = ((size_t(c) * a.Hkv + g) * x.tiles + tile) * x.nchunk * size_t(x.rows) + row;
+    if (SH) {
+        step = size_t(a.T) * a.Hq, p0 = orow;
+        first = paged_in_group(x, c) ? 0 : x.s.np;
+        n = x.s.np + x.nchunk;
+    }
     float mx = -INFINITY;
     if (real)
-        for (int k = lane; k < x.nchunk; k += 32) {
-            const float2 ml = x.part_ml[p0 + size_t(k) * x.rows];
+        for (int k = first + lane; k < n; k += 32) {
+            const float2 ml = x.part_ml[p0 + size_t(k) * step];
             if (ml.y > 0.f) mx = fmaxf(mx, ml.x);
         }
     mx = warp_max(mx);
@@ -596,22 +629,22 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
 #pragma unroll
     for (int e = 0; e < V; ++e) acc[e] = 0.f;
     if (mx > -INFINITY)
-        for (int k0 = 0; k0 < x.nchunk; k0 += 32) {
+        for (int k0 = first; k0 < n; k0 += 32) {
             float f = 0.f;  // lane t: chunk k0 + t's factor 2^(m - mx)
-            if (k0 + lane < x.nchunk) {
-                const float2 ml = x.part_ml[p0 + size_t(k0 + lane) * x.rows];
+            if (k0 + lane < n) {
+                const float2 ml = x.part_ml[p0 + size_t(k0 + lane) * step];
                 if (ml.y > 0.f) {
                     f = ex2(ml.x - mx);
                     sum += f * ml.y;
                 }
             }
-            const int nk = min(32, x.nchunk - k0);
+            const int nk = min(32, n - k0);
             for (int u0 = 0; u0 < nk; u0 += 8) {
                 float o[8][V];
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
                     const float fu = __shfl_sync(0xffffffffu, f, (u0 + u) & 31);
-                    const float* src = x.part_o + (p0 + size_t(k0 + u0 + u) * x.rows) * D + lane * V;
+                    const float* src = x.part_o + (p0 + size_t(k0 + u0 + u) * step) * D + lane * V;
 #pragma unroll
                     for (int e = 0; e < V; ++e) o[u][e] = 0.f;
                     if (u0 + u < nk && fu > 0.f) {
@@ -672,14 +705,15 @@ static int64_t part_rows(int64_t tiles, int64_t blocks, int64_t rows, int D) {
     return all < cap ? all : cap;
 }
 
-static PgPlan paged_plan(const PagedArgs& a) {
+// `keys`: rows that a request may have, 0: what its row of the table holds.
+static PgPlan paged_plan(const PagedArgs& a, int64_t keys = 0) {
     PgPlan p{};
     const int grp = a.Hq / a.Hkv;
     p.tt = PG_BM / grp;
     p.tiles = (a.S + p.tt - 1) / p.tt;
     p.rows = p.tiles > 1 ? PG_BM : a.S * grp;
     const int64_t heads = int64_t(a.C) * a.Hkv;
-    const int64_t blocks = (((int64_t(a.max_pages) << a.log2_page)) + PG_BN - 1) / PG_BN;
+    const int64_t blocks = ((keys ? keys : int64_t(a.max_pages) << a.log2_page) + PG_BN - 1) / PG_BN;
     p.nt = 1, p.nchunk = 1;
     double best = 1e300;
     p.most_rows = part_rows(heads * p.tiles, blocks, p.rows, a.D);
@@ -726,6 +760,7 @@ static PgPlan paged_plan(const PagedArgs& a) {
                 best = t, p.nt = nt, p.nchunk = int(n), p.cluster = cluster, p.alone = alone;
         }
     }
+    p.us = best;
     auto bytes = [&](int64_t rows, size_t* ml) {
         auto up = [](size_t b) { return (b + 255) / 256 * 256; };
         *ml = up(size_t(rows) * a.D * 4);
@@ -761,15 +796,15 @@ bool make_query_map(CUtensorMap* m, const PagedArgs& a, const void* q, int tt) {
     return make_tensor_map_bf16_nd(m, q, 3, d, st, box);
 }
 
-template <int D, int NT, int ST, bool CL = false>
+template <int D, int NT, int ST, bool CL = false, bool SH = false>
 static int launch_attn_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PgArgs& x,
                          cudaStream_t stream) {
-    auto kern = paged_attn_kernel<D, NT, ST, CL>;
+    auto kern = paged_attn_kernel<D, NT, ST, CL, SH>;
     const size_t smem = PgSmem<D, NT, ST>::TOTAL;
     static std::atomic<uint64_t> raised{0};
     if (!raise_smem(kern, int(smem), raised)) return DARTREE_ECUDA;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned(x.nchunk) * unsigned(x.a.C) * x.a.Hkv * ((x.tiles + NT - 1) / NT));
+    cfg.gridDim = dim3(x.s.ctas + unsigned(x.nchunk) * unsigned(x.a.C) * x.a.Hkv * ((x.tiles + NT - 1) / NT));
     cfg.blockDim = dim3(128 + 128 * NT);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -798,7 +833,7 @@ int launch_paged_attention(const PagedArgs& a, const void* q, float scale, void*
     const bool inner = 4 * int64_t(a.S) <= int64_t(a.max_pages) << a.log2_page &&
                        ctas > num_sms() * (p.nt == 1 && !p.alone ? 2 : 1);
     PgArgs x{a, a.Hq / a.Hkv, p.tt, p.tiles, p.nchunk, p.rows, inner, scale * LOG2E, static_cast<bf16_t*>(out), lse,
-             reinterpret_cast<float*>(w), reinterpret_cast<float2*>(w + p.part_ml)};
+             reinterpret_cast<float*>(w), reinterpret_cast<float2*>(w + p.part_ml), PgGroups{}};
     int e;
     if (p.few)
         e = launch_paged_few(x, p.cluster, p.alone, tq, tk, tv, stream);
@@ -818,8 +853,139 @@ int launch_paged_attention(const PagedArgs& a, const void* q, float scale, void*
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     KTimer kt_(KID_PAGED_COMBINE, stream);
-    const cudaError_t ce = a.D == 64 ? cudaLaunchKernelEx(&cfg, paged_combine_kernel<64>, x)
-                                     : cudaLaunchKernelEx(&cfg, paged_combine_kernel<128>, x);
+    const cudaError_t ce = a.D == 64 ? cudaLaunchKernelEx(&cfg, paged_combine_kernel<64, false>, x)
+                                     : cudaLaunchKernelEx(&cfg, paged_combine_kernel<128, false>, x);
+    return ce == cudaSuccess ? DARTREE_OK : DARTREE_ECUDA;
+}
+
+// ----------------------------------------------------------------------------- shared prefixes
+//
+// Requests that share their first rows: those rows are read once for a tile of 128 rows of q instead of once for
+// each request. The new tokens of a group lie together in q, so the general kernel takes them as one request's, all
+// of which see all shared rows; each request's own rows follow as in a call without groups, from the first row
+// behind the shared pages. Both leave (maximum, sum, O) in memory and paged_combine_kernel joins them.
+
+struct PgSharedPlan {
+    bool use, few, alone, few_alone;  // shared at all; own rows by the transposed kernel; one CTA to an SM
+    int tt, tiles, nt, np, ns;
+    unsigned units;
+    size_t ml, total;
+};
+
+// In us, as paged_plan does: the prefix's CTAs, the own rows' (behind them, or in the same launch), the join
+// (4 and the partial results there and back at 5 TB/s).
+constexpr int64_t PG_SHARED_BYTES = int64_t(512) << 20;  // of partial rows, as long as there is a choice
+
+static PgSharedPlan shared_plan(const PagedArgs& a, const dartree_paged_groups& s) {
+    PgSharedPlan p{};
+    const int G = s.G;
+    int64_t most_rows = s.most_rows, most_rest = s.most_rest;
+    const int64_t cap = int64_t(a.max_pages) << a.log2_page;
+    if (most_rows <= 0 || most_rows > cap) most_rows = cap;
+    if (most_rest <= 0 || most_rest > cap) most_rest = cap;
+    const int grp = a.Hq / a.Hkv;
+    const int64_t sms = num_sms(), heads = int64_t(a.C) * a.Hkv;
+    const int64_t pb = (most_rows + PG_BN - 1) / PG_BN, rb = (most_rest + PG_BN - 1) / PG_BN;
+    p.tt = PG_BM / grp;
+    p.tiles = (a.S + p.tt - 1) / p.tt;
+    p.few = a.S * grp <= 16;
+    const int64_t row_bytes = int64_t(a.T) * a.Hq * a.D * 4;
+    const double chunk = double(row_bytes) * 2.0 / 5e6;
+    auto waves_of = [](double load) { return load <= 1.0 ? 1.0 : load < 3.0 ? ceil(load) : load + 0.5; };
+    double best = 1e300, own_few = 1e300;
+    int ns_few = 1;
+    for (int64_t ns = 1; p.few && ns <= rb && ns <= 16; ++ns) {
+        const double load = double(heads * ns) / double(sms), tile = 4.0 * PG_BN * a.D * double(sms) / 6.7e6;
+        const double waves = floor(load / 2.0), rest = load - 2.0 * waves, per = double((rb + ns - 1) / ns);
+        const double t = chunk * double(ns) +
+            (load <= 2.0 ? 3.0 + fmax(per * (load <= 1.0 ? 0.9 : 1.25), double(heads) * double(rb) * tile / double(sms))
+                         : waves * (3.0 + per * 2.0 * tile) + (rest > 0.0 ? 3.0 + per * fmax(1.25, rest * tile) : 0.0));
+        if (t < own_few) own_few = t, ns_few = int(ns);
+    }
+    for (int way = 0; way < 3; ++way) {
+        if (way == 2 && a.D == 64) break;
+        const int nt = way == 2 ? 2 : 1;
+        const int64_t per = int64_t(nt) * p.tt;
+        const int64_t units = (a.T + G * (per - 1)) / per, base = units * a.Hkv;
+        const double slots = double(sms) * (way == 0 ? 2.0 : 1.0);
+        const bool many = units >= 4 * G;
+        const double ends = way == 0 ? 5.0 : way == 1 ? 4.0 : 6.0;
+        const double block = a.D == 128 ? (way == 0 ? (many ? 2.1 : 2.5) : way == 1 ? (many ? 1.36 : 1.55) : 1.7)
+                                        : (way == 0 ? 1.4 : 1.5);
+        double own = own_few, prefix = 1e300;
+        int ns = ns_few, np = 1;
+        const double ctas = double(heads * ((p.tiles + nt - 1) / nt));
+        for (int64_t n = 1; !p.few && n <= rb && n <= 4; ++n) {
+            const double t = ctas * double(n) / slots * (ends + block * double((rb + n - 1) / n)) + chunk * double(n);
+            if (n == 1 || t < own) own = t, ns = int(n);
+        }
+        for (int64_t n = 1; n <= pb && n <= 64; ++n) {
+            if (n > 1 && (n + ns) * row_bytes > PG_SHARED_BYTES) break;
+            const double t = waves_of(double(base * n) / slots) * (ends + block * double((pb + n - 1) / n)) + chunk * double(n);
+            if (t < prefix) prefix = t, np = int(n);
+        }
+        if (own + prefix + 4.0 < best) {
+            best = own + prefix + 4.0;
+            p.nt = nt, p.np = np, p.ns = ns, p.alone = way == 1, p.units = unsigned(units);
+        }
+    }
+    p.few_alone = heads * p.ns <= sms;
+    p.use = s.always || best < paged_plan(a, most_rows + most_rest).us;
+    const int64_t rows = int64_t(a.T) * a.Hq * (p.np + p.ns);
+    p.ml = (size_t(rows) * a.D * 4 + 255) / 256 * 256;
+    p.total = p.ml + (size_t(rows) * 8 + 255) / 256 * 256;
+    return p;
+}
+
+size_t paged_shared_part_bytes(const PagedArgs& a, const dartree_paged_groups& s) {
+    const PgSharedPlan p = shared_plan(a, s);
+    return p.use ? p.total : paged_plan(a).total;
+}
+
+void paged_shared_plan(const PagedArgs& a, const dartree_paged_groups& s, dartree_paged_shared_plan_t* out) {
+    const PgSharedPlan p = shared_plan(a, s);
+    *out = dartree_paged_shared_plan_t{p.use, p.few, p.nt, p.np, p.ns, p.alone, p.use ? p.total : paged_plan(a).total};
+}
+
+int launch_paged_shared(const PagedArgs& a, const void* q, const dartree_paged_groups& s, float scale, void* out,
+                        float* lse, void* part, size_t part_bytes, cudaStream_t stream) {
+    const PgSharedPlan p = shared_plan(a, s);
+    if (part_bytes < (p.use ? p.total : paged_plan(a).total)) return DARTREE_EWORKSPACE;
+    if (!p.use) return launch_paged_attention(a, q, scale, out, lse, part, stream);
+    CUtensorMap tq, tk, tv;
+    if (!make_query_map(&tq, a, q, p.tt) || !make_page_map(&tk, a, a.k) || !make_page_map(&tv, a, a.v))
+        return DARTREE_ECUDA;
+    uint8_t* w = static_cast<uint8_t*>(part);
+    const int grp = a.Hq / a.Hkv;
+    // (own rows by the other kernel: no CTAs for them in this launch)
+    PgArgs x{a, grp, p.tt, p.few ? 0 : p.tiles, p.ns, 0, 0, scale * LOG2E, static_cast<bf16_t*>(out), lse,
+             reinterpret_cast<float*>(w), reinterpret_cast<float2*>(w + p.ml),
+             PgGroups{s.G, p.np, p.units, p.units * unsigned(a.Hkv) * unsigned(p.np), s.start, s.rows}};
+    int e;
+    if (a.D == 64)
+        e = (p.alone ? launch_attn_t<64, 1, 8, false, true> : launch_attn_t<64, 1, 4, false, true>)(tq, tk, tv, x, stream);
+    else
+        e = (p.nt == 2 ? launch_attn_t<128, 2, 5, false, true>
+             : p.alone ? launch_attn_t<128, 1, 5, false, true>
+                       : launch_attn_t<128, 1, 2, false, true>)(tq, tk, tv, x, stream);
+    if (e != DARTREE_OK) return e;
+    if (p.few) {
+        CUtensorMap tf;
+        if (!make_query_map(&tf, a, q, a.S)) return DARTREE_ECUDA;
+        PgArgs y = x;
+        y.tt = a.S, y.tiles = 1, y.rows = a.S * grp;
+        if ((e = launch_paged_few(y, false, p.few_alone, tf, tk, tv, stream))) return e;
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned((size_t(a.C) * a.S * a.Hq + 7) / 8));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1] = {pdl_attribute()};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    KTimer kt_(KID_PAGED_COMBINE, stream);
+    const cudaError_t ce = a.D == 64 ? cudaLaunchKernelEx(&cfg, paged_combine_kernel<64, true>, x)
+                                     : cudaLaunchKernelEx(&cfg, paged_combine_kernel<128, true>, x);
     return ce == cudaSuccess ? DARTREE_OK : DARTREE_ECUDA;
 }
 

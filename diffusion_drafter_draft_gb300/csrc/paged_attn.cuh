@@ -14,6 +14,16 @@ constexpr float PG_MOST = 16384.0f;    // weights from which a new maximum is ta
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr int PG_CLUSTER = 8;         // chunks that merge through shared memory
 
+// Groups of requests that share their first rows (a call with shared prefixes): the new tokens of a whole
+// group are attended over the shared rows together, in `np` chunks of the rows; then each request's over its
+// own rows in `nchunk`. The partial results of a row of q lie at chunk * rows + row, the prefix's chunks first.
+struct PgGroups {
+    int G, np;
+    unsigned units, ctas;             // CTAs' worth of tiles of all groups (a bound), CTAs of the prefix
+    const int32_t* start;             // [G + 1] first requests
+    const int32_t* rows;              // [G] rows shared
+};
+
 struct PgArgs {
     PagedArgs a;
     int grp, tt, tiles, nchunk, rows;
@@ -23,7 +33,80 @@ struct PgArgs {
     float* lse;
     float* part_o;
     float2* part_ml;
+    PgGroups s;
 };
+
+// Whether request c is in a group.
+__device__ __forceinline__ bool paged_in_group(const PgArgs& x, int c) {
+    return c >= x.s.start[0] && c < x.s.start[x.s.G];
+}
+
+// Rows that request c shares with its group, in whole pages (0: no group). By a whole warp, the same for all lanes.
+__device__ __forceinline__ int paged_shared_rows(const PgArgs& x, int c) {
+    const int lane = threadIdx.x & 31;
+    int n = 0;                                            // starts up to c
+    for (int j = 0; j <= x.s.G; j += 32) {
+        const bool in = j + lane <= x.s.G && x.s.start[j + lane] <= c;
+        const unsigned b = __ballot_sync(0xffffffffu, in);
+        n += __popc(b);
+        if (b != 0xffffffffu) break;
+    }
+    if (n == 0 || n > x.s.G) return 0;
+    const int64_t cap = int64_t(x.a.max_pages) << x.a.log2_page;
+    return int(min(int64_t(max(x.s.rows[n - 1], 0)), cap)) & ~(x.a.page - 1);
+}
+
+// The `unit`-th run of `per` tokens of the groups' tokens: its group's first request, rows of q, tokens, shared
+// rows, and its first token among them. False past the last. By a whole warp, the same for all lanes.
+struct PgUnit {
+    int c, q0, n, t0, keys;
+};
+__device__ __forceinline__ bool paged_shared_unit(const PgArgs& x, unsigned unit, int per, PgUnit& u, bool& bad) {
+    const int lane = threadIdx.x & 31;
+    const PagedArgs& a = x.a;
+    const int64_t cap = int64_t(a.max_pages) << a.log2_page;
+    bad = false;
+    bool found = false;
+    unsigned before = 0;
+    for (int j0 = 0; j0 < x.s.G; j0 += 32) {
+        const int j = j0 + lane;
+        int c = 0, f0 = 0, f1 = 0;
+        bool wrong = false;
+        if (j < x.s.G) {
+            const int s0 = x.s.start[j], s1 = x.s.start[j + 1];
+            c = min(max(s0, 0), a.C);
+            const int e = min(max(s1, c), a.C);
+            wrong = c != s0 || e != s1 || x.s.rows[j] < 0 || x.s.rows[j] > cap;
+            if (a.q_start) {
+                f0 = min(max(a.q_start[c], 0), a.T);
+                f1 = min(max(a.q_start[e], f0), a.T);
+            } else {
+                f0 = c * a.S, f1 = e * a.S;
+            }
+        }
+        bad |= __any_sync(0xffffffffu, wrong) != 0;
+        const unsigned mine = unsigned((f1 - f0 + per - 1) / per);
+        unsigned inc = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, unit < before + inc);
+        if (hit && !found) {
+            const int l = __ffs(hit) - 1;
+            u.c = __shfl_sync(0xffffffffu, c, l);
+            u.q0 = __shfl_sync(0xffffffffu, f0, l);
+            u.n = __shfl_sync(0xffffffffu, f1, l) - u.q0;
+            u.t0 = int(unit - before - __shfl_sync(0xffffffffu, inc - mine, l)) * per;
+            u.keys = int(min(int64_t(max(x.s.rows[j0 + l], 0)), cap)) & ~(a.page - 1);
+            if (unit != 0) return true;                   // (the first unit's CTAs look at all groups)
+            found = true;
+        }
+        before += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    return found;
+}
 
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);

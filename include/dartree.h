@@ -437,6 +437,48 @@ DARTREE_API int dartree_paged_attention(const dartree_paged_params* p, const voi
                                         const dartree_paged_cache* cache, const dartree_tree* tree, float scale,
                                         void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
 
+/* dartree_paged_attention of a batch whose requests share prefixes: the same outputs (up to the order of
+ * the sums), with the rows that a group shares read for all its new tokens at once. Group g is requests
+ * start[g] .. start[g+1] - 1; their first rows[g] cached rows are the same: their table entries for these
+ * are the same pages, or copies with the same contents. Whole pages of them are read through the table of
+ * the group's first request, rows behind the last whole page through each request's own. Requests before
+ * start[0] and from start[G] on are in no group.
+ *   start       [G + 1] ascending, in 0..C
+ *   rows        [G], at most the n_ctx of each of the group's requests
+ *   most_rows, most_rest  rows shared and rows of a request behind them (new tokens included) that the
+ *               batch is expected to have at most, 0: as many as the block table holds. They size the
+ *               workspace and decide how the work is split, not the results; where sharing does not pay by
+ *               them, the call is dartree_paged_attention.
+ * Checked on the device, with DARTREE_EINTERNAL in the status word and unspecified results: start not
+ * ascending or outside 0..C, rows below zero, past the table or past n_ctx, besides what dartree_paged_attention
+ * checks. Other arguments and errors as there; the workspace is dartree_paged_shared_workspace_bytes
+ * (that of these sizes; nothing is promised for smaller batches). */
+typedef struct {
+    int G;                  /* groups, 0..C */
+    int most_rows, most_rest;
+    int always;             /* 1: the rows are shared even where that is not expected to pay (tests, tuning) */
+    const int32_t* start;
+    const int32_t* rows;
+} dartree_paged_groups;
+DARTREE_API size_t dartree_paged_shared_workspace_bytes(const dartree_paged_params* p, const dartree_paged_groups* s);
+DARTREE_API int dartree_paged_shared_attention(const dartree_paged_params* p, const void* q,
+                                               const dartree_paged_cache* cache, const dartree_tree* tree,
+                                               const dartree_paged_groups* s, float scale, void* out, float* lse,
+                                               void* ws, size_t ws_bytes, void* stream);
+
+/* How it takes these sizes on the current device (host only; for tests and tuning). */
+typedef struct {
+    int use;            /* 0: as dartree_paged_attention */
+    int few;            /* 1: own rows by the kernel for at most 16 rows of a key/value head */
+    int tiles_per_cta;  /* 128-row tiles of a CTA: 1 or 2 */
+    int chunks;         /* parts of the shared rows */
+    int own_chunks;     /* parts of a request's own */
+    int alone;          /* 1: one CTA of one tile to an SM */
+    size_t part_bytes;  /* partial results in the workspace */
+} dartree_paged_shared_plan_t;
+DARTREE_API int dartree_paged_shared_plan(const dartree_paged_params* p, const dartree_paged_groups* s,
+                                          dartree_paged_shared_plan_t* plan);
+
 /* Attention weight each cached row receives, summed over the new tokens and the query
  * heads of its key/value head: with N = max_pages * page, for every row j that request
  * c holds (new ones included)

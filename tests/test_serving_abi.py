@@ -114,6 +114,65 @@ def test_reserve_and_release_arguments(dd):
     assert rel(n=511) == dd.EWORKSPACE
 
 
+def test_shared_attention_arguments(dd):
+    L = dd.lib()
+    g = lambda G=1, most_rows=0, most_rest=0, always=1, start=256, rows=256: dd.PagedGroups(  # noqa: E731
+        G, most_rows, most_rest, always, start, rows)
+    need = L.dartree_paged_shared_workspace_bytes(ctypes.byref(_p(dd)), ctypes.byref(g()))
+    assert need > 512
+    m = dd.PagedCacheDesc(256, 256, 256, 256, None)
+    at = lambda n: ctypes.c_void_p((1 << 24) + n)  # noqa: E731
+    n = 6 * 8 * 128 * 2
+
+    def call(p=None, s=None, q=at(0), m=m, tree=None, scale=0.0, out=at(n), lse=None, bytes_=None):
+        return L.dartree_paged_shared_attention(ctypes.byref(p or _p(dd)), q, ctypes.byref(m), tree, ctypes.byref(s or g()),
+                                                scale, out, lse, WS, need if bytes_ is None else bytes_, None)
+
+    bad = [dict(G=-1), dict(G=3), dict(most_rows=-1), dict(most_rest=-5)]
+    for kw in bad:
+        assert call(s=g(**kw)) == dd.EINVAL, kw
+        assert L.dartree_paged_shared_workspace_bytes(ctypes.byref(_p(dd)), ctypes.byref(g(**kw))) == 0
+        assert L.dartree_paged_shared_plan(ctypes.byref(_p(dd)), ctypes.byref(g(**kw)), ctypes.byref(dd.PagedSharedPlan())) \
+            == dd.EINVAL
+    for kw in (dict(s=g(start=None)), dict(s=g(rows=None)), dict(q=None), dict(q=at(8)), dict(out=None), dict(out=at(16)),
+               dict(lse=at(n - 4)), dict(lse=at(2 * n - 4)), dict(lse=at(2 * n + 2)), dict(scale=-1.0), dict(scale=NAN),
+               dict(p=_p(dd, T=7)), dict(m=dd.PagedCacheDesc(256, 256, None, 256, None))):
+        assert call(**kw) == dd.EINVAL, kw
+    assert call(p=_p(dd, dtype=0)) == dd.EUNSUPPORTED
+    assert call(p=_p(dd, D=96)) == dd.EUNSUPPORTED
+    assert call(bytes_=need - 1) == dd.EWORKSPACE
+    assert call(bytes_=255) == dd.EWORKSPACE
+    assert call(p=_p(dd, C=0, T=0), s=g(G=0)) == dd.OK
+    assert L.dartree_paged_shared_plan(ctypes.byref(_p(dd)), ctypes.byref(g()), None) == dd.EINVAL
+
+
+def test_every_way_of_sharing_is_taken(dd):
+    """(own rows by the transposed kernel, tiles per CTA, alone): what is compiled is what plans choose; the
+    workspace holds what the plan stores, and little more of it than half a gigabyte where chunks are a choice."""
+    import random
+    rng, taken, used = random.Random(5), {64: set(), 128: set()}, set()
+    for _ in range(4000):
+        C, S = rng.randint(1, 100), rng.choice([1, 1, 2, int(2 ** rng.uniform(0, 9))])
+        Hkv, grp = rng.choice([(1, 8), (2, 5), (4, 4), (8, 4), (8, 1), (4, 7), (2, 16), (1, 1)])
+        width = int(2 ** rng.uniform(0, 11))
+        for D, seen in taken.items():
+            p = dd.PagedParams(C, C * S, S, Hkv * grp, Hkv, D, 64, 1 << 20, width, 1)
+            s = dd.PagedGroups(rng.randint(1, C), rng.choice([0, rng.randint(1, 10000)]), rng.choice([0, rng.randint(1, 2000)]),
+                               rng.choice([0, 1]), None, None)
+            o = dd.PagedSharedPlan()
+            assert dd.lib().dartree_paged_shared_plan(ctypes.byref(p), ctypes.byref(s), ctypes.byref(o)) == dd.OK
+            need = dd.lib().dartree_paged_shared_workspace_bytes(ctypes.byref(p), ctypes.byref(s))
+            assert 256 + o.part_bytes <= need <= 256 + 4 * C + 512 + o.part_bytes
+            used.add((bool(s.always), bool(o.use)))
+            if o.use:
+                seen.add((o.few, o.tiles_per_cta, o.alone))
+                row = C * S * Hkv * grp * (D * 4 + 8)
+                assert o.part_bytes <= max(512 << 20, 2 * row) * 1.1 + 1024
+    assert used == {(True, True), (False, True), (False, False)}
+    one = {(f, 1, a) for f in (0, 1) for a in (0, 1)}
+    assert taken[64] == one and taken[128] == one | {(0, 2, 0), (1, 2, 0)}
+
+
 def test_kernel_families_are_named(dd):
     names = [dd.lib().dartree_kernel_name(i).decode() for i in range(dd.num_kernel_ids())]
     for n in ("paged_reserve_kernel", "paged_release_kernel", "sample_kernel", "sample_walk_kernel"):
