@@ -16,7 +16,7 @@
 //   load    slice to shared memory, maximum and minimum, each thread's largest
 //   top-k   up to 1024: what reaches the j-th largest of the threads' largest, j = ceil(k / CTAs), in
 //           every CTA holds the k first (and few others): a list in CTA 0, sorted, which finishes
-//           there when at most 256 are kept
+//           there
 //   top-p   a histogram of 2048 bins of x between maximum and minimum, of counts and places in the bin, tells
 //           within 1e-3 of the weight which x hold the border; one pass takes the weights of all, of what
 //           lies above and of each warp's stretch, and lists what lies between; CTA 0 finds the border and the
@@ -35,8 +35,9 @@ constexpr int SP_NT = 512;
 constexpr int SP_WARPS = SP_NT / 32;
 constexpr int SP_BINS = 2048;
 constexpr int SP_LIST = 1024;     // elements of CTA 0's list
-constexpr int SP_FEW = 256;       // kept elements among which CTA 0 draws by itself
+constexpr int SP_FEW = 256;       // twice the elements that are compared with one another
 constexpr int SP_MAXC = 8;        // CTAs of a cluster
+constexpr int SP_FLUSH = 512;     // elements whose weights' sums fit 32 bits each (Weigher::add)
 constexpr int SP_Q = 43;          // a weight of 1 is 2^43; 2^20 of them stay below 2^64
 
 // 2^(i/256) as a pair of floats, i < 256 (evaluated by the compiler in double).
@@ -249,7 +250,7 @@ struct Weigher {
             w[e + 1] = whole(h[1] + g[1] - 2u * SP_C1, q[1] - SP_C2);
         }
     }
-    // Sums of weights, 2^-22 and 2^-43 apart; a thread's share of a row (at most 2^9 elements) fits.
+    // Sums of weights, 2^-22 and 2^-43 apart; SP_FLUSH elements fit (a thread's share of a held slice is below that).
     // add_above: of all, and of those above `bound`.
     template <int N>
     __device__ __forceinline__ void add_above(const float (&x)[N], float bound, uint32_t& i1, uint32_t& i2, uint32_t& a1,
@@ -326,11 +327,77 @@ template <> struct SpElem<bf16_t> {
     static __device__ __forceinline__ void put(bf16_t* p, float x) { *p = bf16_t{uint16_t(__float_as_uint(x) >> 16)}; }
 };
 
-// A CTA's slice of a row: `nv` vectors in shared memory, element e of vector v being token
-// first + v * VEC + e (first may lie before the slice; what is no element of it is -inf, never kept).
+// A CTA's slice [lo, hi) of a row as `nv` vectors of 16 bytes, element e of vector v being token first + v * VEC + e
+// (first may lie before the slice; what is no element of it reads as -inf, which is never kept, like NaN).
+// HELD: in shared memory; else read again from memory (the L2, mostly) by every pass, for batches of more rows
+// than fit.
+template <typename T, bool HELD>
 struct Slice {
-    uint4* v;
-    int nv, first;
+    using E = SpElem<T>;
+    static constexpr int VEC = E::VEC;
+    const uint4* v;               // HELD: the CTA's shared memory; else the row from `first` on, aligned
+    const T* row;
+    int nv, first, lo, hi;
+    bool only_inf;                // the maximum is +inf: it counts as 0 and all else as -inf
+
+    // Vector i as it lies, its ends cleared.
+    __device__ __forceinline__ uint4 raw(int i) const {
+        if (HELD) return v[i];
+        const int t = first + i * VEC;
+        if (t >= lo && t + VEC <= hi) return __ldg(v + i);
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if constexpr (sizeof(T) == 4) {
+                w[k] = t + k >= lo && t + k < hi ? __float_as_uint(row[t + k]) : 0xff800000u;
+            } else {
+                const int a = t + 2 * k;
+                w[k] = (a >= lo && a < hi ? uint32_t(row[a].bits) : 0xff80u) |
+                       (a + 1 >= lo && a + 1 < hi ? uint32_t(row[a + 1].bits) : 0xff80u) << 16;
+            }
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ __forceinline__ void values(uint4 r, float (&x)[VEC]) const {
+        if (!HELD) r = E::clean4(r);
+        E::widen(r, x);
+        if (only_inf)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) x[e] = x[e] == INFINITY ? 0.f : -INFINITY;
+    }
+    __device__ __forceinline__ void values(int i, float (&x)[VEC]) const { values(raw(i), x); }
+    // One element of the slice.
+    __device__ __forceinline__ float value(int tok) const {
+        float x;
+        if (HELD) x = E::get(reinterpret_cast<const T*>(v) + (tok - first));
+        else x = tok >= lo && tok < hi ? E::get(row + tok) : -INFINITY;
+        return only_inf ? (x == INFINITY ? 0.f : -INFINITY) : x;
+    }
+    // f(i, x) for vectors i0, i0 + step, ... below i1; read ahead where that takes long.
+    template <typename F>
+    __device__ __forceinline__ void over(int i0, int i1, int step, F f) const {
+        float x[VEC];
+        if (HELD) {
+            for (int i = i0; i < i1; i += step) {
+                values(i, x);
+                f(i, x);
+            }
+        } else {
+            constexpr int A = 3;                           // vectors ahead
+            uint4 r[A];
+#pragma unroll
+            for (int k = 0; k < A; ++k)
+                if (i0 + k * step < i1) r[k] = raw(i0 + k * step);
+            for (int i = i0; i < i1; i += step) {
+                const uint4 now = r[0];
+#pragma unroll
+                for (int k = 0; k + 1 < A; ++k) r[k] = r[k + 1];
+                if (i + A * step < i1) r[A - 1] = raw(i + A * step);
+                values(now, x);
+                f(i, x);
+            }
+        }
+    }
 };
 
 // Elements that are still in question: bin of the first histogram and a range of keys.
@@ -351,23 +418,21 @@ struct Kept {                     // the last element kept
 };
 
 // What a row needs of the cluster. All functions are called by all threads of the cluster.
-template <typename T>
+template <typename T, bool HELD>
 struct Sampler {
     using E = SpElem<T>;
     static constexpr int VEC = E::VEC;
     SpShared& sh;
-    Slice sl;
+    Slice<T, HELD> sl;
     uint32_t S, cr;               // CTAs, this one
     Weigher<E::EXACT> wg;
 
     template <typename F>
     __device__ __forceinline__ void each(F f) const {          // f(x, token), this thread's elements
-        for (int i = threadIdx.x; i < sl.nv; i += SP_NT) {
-            float x[VEC];
-            E::widen(sl.v[i], x);
+        sl.over(threadIdx.x, sl.nv, SP_NT, [&](int i, const float (&x)[VEC]) {
 #pragma unroll
             for (int e = 0; e < VEC; ++e) f(x[e], sl.first + i * VEC + e);
-        }
+        });
     }
 
     // Sum over the block, and the sum before this thread (exclusive, in thread order).
@@ -407,16 +472,14 @@ struct Sampler {
             }
             return b;
         };
-        for (int i = threadIdx.x; i < sl.nv; i += SP_NT) {
-            float x[VEC];
-            E::widen(sl.v[i], x);
+        sl.over(threadIdx.x, sl.nv, SP_NT, [&](int i, const float (&x)[VEC]) {
             bool in[VEC], any = false;
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 in[e] = kept.has(x[e], sl.first + i * VEC + e) && (g.bin < 0 || bin_of(x[e]) >= 0);
                 any |= in[e];
             }
-            if (!any) continue;
+            if (!any) return;
             if constexpr (!MASS) {
 #pragma unroll
                 for (int e = 0; e < VEC; ++e)
@@ -438,7 +501,7 @@ struct Sampler {
                     if (up) atomicAdd(&sh.hi[b], up);
                 }
             }
-        }
+        });
         if (MASS && share) {
             uint64_t before;
             rest = block_scan(rest, before);
@@ -610,9 +673,8 @@ struct Sampler {
         }
         return t;
     }
-    // Elements of vector i, what is not taken as -inf; false: none is.
+    // The elements x of vector i, what is not taken as -inf; false: none is.
     __device__ __forceinline__ bool taken(int i, const Take& t, uint64_t wmin, float (&x)[VEC]) const {
-        E::widen(sl.v[i], x);
         float top = x[0];
         bool near = false;
 #pragma unroll
@@ -624,7 +686,7 @@ struct Sampler {
             uint32_t in = 0;                               // (by shared memory: x[] stays in registers)
 #pragma unroll 1
             for (int e = 0; e < VEC; ++e) {
-                const float y = E::get(reinterpret_cast<const T*>(sl.v + i) + e);
+                const float y = sl.value(sl.first + i * VEC + e);
                 if (t.kept.has(y, sl.first + i * VEC + e) &&
                     (y > t.sure || y == wg.m || !wmin || wg.one_call(y) >= wmin))
                     in |= 1u << e;
@@ -642,9 +704,9 @@ struct Sampler {
     __device__ __forceinline__ uint64_t lane_sum(int v0, int v1, const Take& t, uint64_t wmin) const {
         uint64_t sum = 0;
         uint32_t i1 = 0, i2 = 0;
-        for (int i = v0 + int(threadIdx.x & 31); i < v1; i += 32) {
-            float x[VEC];
-            if (!taken(i, t, wmin, x)) continue;
+        int n = 0;
+        sl.over(v0 + int(threadIdx.x & 31), v1, 32, [&](int i, float (&x)[VEC]) {
+            if (!taken(i, t, wmin, x)) return;
             if (wg.slow) {
                 uint64_t w[VEC];
                 wg.template each<VEC>(x, w);
@@ -652,8 +714,9 @@ struct Sampler {
                 for (int e = 0; e < VEC; ++e) sum += x[e] > -INFINITY ? w[e] : 0;
             } else {
                 wg.template add<VEC>(x, i1, i2);
+                if (!HELD && ++n == SP_FLUSH / VEC) sum += Weigher<E::EXACT>::whole(i1, i2), i1 = i2 = 0, n = 0;
             }
-        }
+        });
         return sum + Weigher<E::EXACT>::whole(i1, i2);
     }
 
@@ -682,7 +745,7 @@ struct Sampler {
     }
 
     // The CTA that holds stretch `owner`: its strips, a warp each, then the strip that holds the unit `left`; the
-    // token to all CTAs. measure(i, w): the weights of vector i's elements.
+    // token to all CTAs. measure(i, x, w): the weights of vector i's elements x.
     template <typename F>
     __device__ int walk(int owner, uint64_t left, F measure) {
         if (owner / SP_WARPS == int(cr)) {
@@ -694,7 +757,11 @@ struct Sampler {
                 uint64_t w[VEC], s = 0;
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) w[e] = 0;
-                if (i < v1) measure(i, w);
+                if (i < v1) {
+                    float x[VEC];
+                    sl.values(i, x);
+                    measure(i, x, w);
+                }
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) s += w[e];
                 const uint64_t inc = sp_warp_scan(s), end = shfl_idx_u64(inc, 31);
@@ -726,8 +793,7 @@ struct Sampler {
     }
     __device__ int walk_kept(int owner, uint64_t left, const Kept& kept, const Filter& f) {
         const Take t = take_of(kept, f);
-        return walk(owner, left, [&](int i, uint64_t (&w)[VEC]) {
-            float x[VEC];
+        return walk(owner, left, [&](int i, float (&x)[VEC], uint64_t (&w)[VEC]) {
             if (!taken(i, t, f.wmin, x)) return;
             wg.template each<VEC>(x, w);
 #pragma unroll
@@ -750,19 +816,17 @@ struct Sampler {
     // The (goal + 1)-th token whose value is `value`, of those in `kept`.
     __device__ int nth_equal(const Kept& kept, float value, uint64_t goal) {
         const int wid = threadIdx.x >> 5, per = stretch(sl.nv), v1 = min(wid * per + per, sl.nv);
-        auto measure = [&](int i, uint64_t (&w)[VEC]) {
-            float x[VEC];
-            E::widen(sl.v[i], x);
+        auto measure = [&](int i, const float (&x)[VEC], uint64_t (&w)[VEC]) {
 #pragma unroll
             for (int e = 0; e < VEC; ++e) w[e] = x[e] == value && kept.has(x[e], sl.first + i * VEC + e);
         };
         uint64_t sum = 0;
-        for (int i = wid * per + int(threadIdx.x & 31); i < v1; i += 32) {
+        sl.over(wid * per + int(threadIdx.x & 31), v1, 32, [&](int i, const float (&x)[VEC]) {
             uint64_t w[VEC];
-            measure(i, w);
+            measure(i, x, w);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) sum += w[e];
-        }
+        });
         sum = sp_warp_sum(sum);
         if ((threadIdx.x & 31) < S) st_dsmem_u64(dsmem_addr(&sh.sums[cr][wid], threadIdx.x & 31), sum);
         cluster_sync();
@@ -774,7 +838,8 @@ struct Sampler {
     // top-p of the whole row. 0: not found this way; 1: the token; 2: the last one kept (min-p comes behind it).
     // (row, V, seg: where a token's stretch is)
     __device__ int nucleus(const Filter& f, float low, const T* row, int V, int seg, Kept& kept, int& tok) {
-        const float m = wg.m, range = fminf(m - low, 31.0f * f.T);
+        // (a little more than the range: the lowest value stays below the last place's end)
+        const float m = wg.m, range = fminf(1.0001f * (m - low), 31.0f * f.T);
         const float s = range > 0.f ? 256.0f * SP_BINS / range : 0.f;
         if (!(s > 1e-30f && s < 1e30f) || wg.slow) return 0;
         const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
@@ -784,19 +849,18 @@ struct Sampler {
         // a bin's word: elements in the upper 12 bits, their 256ths of the bin (8 bits each) in the lower 20. (More than
         // 4095 of a CTA's elements in a bin: the elements do not add up, and the other way is taken.)
         uint32_t n = 0;
-        for (int i = threadIdx.x; i < sl.nv; i += SP_NT) {
-            float x[VEC];
-            E::widen(sl.v[i], x);
+        sl.over(threadIdx.x, sl.nv, SP_NT, [&](int, const float (&x)[VEC]) {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                if (x[e] > -INFINITY) {
-                    // (the sum's low bits are the nearest whole number)
-                    const uint32_t q = __float_as_uint(fminf(__fmul_rn(__fsub_rn(m, x[e]), s), 256.0f * SP_BINS - 1.0f) +
-                                                       8388608.0f);
+            for (int e = 0; e < VEC; ++e) {
+                // (beyond the range, 31 T: no weight; the sum's low bits are the nearest whole number)
+                const float v = __fmul_rn(__fsub_rn(m, x[e]), s);
+                if (v < 256.0f * SP_BINS - 0.5f) {
+                    const uint32_t q = __float_as_uint(v + 8388608.0f);
                     atomicAdd(&sh.lo[(q >> 8) & (SP_BINS - 1)], (1u << 20) + (q & 255u));
                     ++n;
                 }
-        }
+            }
+        });
         n = block_count(int(n));
         if (threadIdx.x < S) st_dsmem_u32(dsmem_addr(&sh.count[cr], threadIdx.x), n);
         cluster_sync();
@@ -856,12 +920,13 @@ struct Sampler {
         const float slack = (fabsf(m) + hi_at) * 1.9073486e-6f;            // 2^-19: roundings of (m - x) * s
         const float x_hi = sh.b_lo == 0 ? INFINITY : (m - lo_at) + slack;
         const float x_lo = sh.b_hi == SP_BINS - 1 ? -3.402823466e38f : (m - hi_at) - slack;
+        if (f.wmin && take_of(kept, f).never > x_hi) return 2;             // (min-p keeps less than top-p)
         // weights of all and of what lies above x_hi, by stretches; x_lo .. x_hi to the list
         const int sv = stretch(sl.nv), v1 = min(wid * sv + sv, sl.nv);
         uint32_t i1 = 0, i2 = 0, a1 = 0, a2 = 0;
-        for (int i = wid * sv + lane; i < v1; i += 32) {
-            float x[VEC];
-            E::widen(sl.v[i], x);
+        uint64_t t_sum = 0, a_sum = 0;
+        int held = 0;
+        sl.over(wid * sv + lane, v1, 32, [&](int i, const float (&x)[VEC]) {
             uint32_t near = 0;
 #pragma unroll
             for (int e = 0; e < VEC; ++e) near |= x[e] >= x_lo && x[e] <= x_hi ? 1u << e : 0u;
@@ -869,11 +934,15 @@ struct Sampler {
             while (near) {                                 // (by shared memory: x[] stays in registers)
                 const int e = __ffs(near) - 1;
                 near &= near - 1;
-                take(E::get(reinterpret_cast<const T*>(sl.v + i) + e), sl.first + i * VEC + e);
+                take(sl.value(sl.first + i * VEC + e), sl.first + i * VEC + e);
             }
-        }
-        const uint64_t total = sp_warp_sum(Weigher<E::EXACT>::whole(i1, i2));
-        const uint64_t above = sp_warp_sum(Weigher<E::EXACT>::whole(a1, a2));
+            if (!HELD && ++held == SP_FLUSH / VEC) {
+                t_sum += Weigher<E::EXACT>::whole(i1, i2), a_sum += Weigher<E::EXACT>::whole(a1, a2);
+                i1 = i2 = a1 = a2 = 0, held = 0;
+            }
+        });
+        const uint64_t total = sp_warp_sum(t_sum + Weigher<E::EXACT>::whole(i1, i2));
+        const uint64_t above = sp_warp_sum(a_sum + Weigher<E::EXACT>::whole(a1, a2));
         if (lane == 0) {
             st_dsmem_u64(dsmem_addr(&sh.sums[cr][wid], 0), total);
             st_dsmem_u64(dsmem_addr(&sh.above[cr][wid], 0), above);
@@ -1071,9 +1140,9 @@ struct Sampler {
         }
     }
 
-    // CTA 0: top-k, top-p and min-p on the list's n elements, and the draw when few are kept (the token, done);
-    // else the last one kept.
-    __device__ bool finish_in_list(int n, const Filter& f, Kept& kept, int& tok) {
+    // CTA 0: top-k, top-p and min-p on the list's n elements, and the draw (true: the token); false: the last
+    // one kept.
+    __device__ bool finish_in_list(int n, const Filter& f, int V, Kept& kept, int& tok) {
         if (cr == 0) {
             sort_list(n);
             const int k = min(f.k, n), i = 2 * int(threadIdx.x);
@@ -1091,25 +1160,49 @@ struct Sampler {
                 const bool keep = i + e < k && (i + e == 0 || (before < goal && w[e] >= f.wmin && w[e] > 0));
                 before += w[e];
                 if (keep) kw += w[e], ++kn;
-                if (i + e < SP_FEW) sh.lw[i + e] = keep ? w[e] : 0;
+                else w[e] = 0;
             }
             const uint64_t total = block_scan(kw, before);
             const int n_kept = int(block_count(kn));
-            if (n_kept <= SP_FEW) {
-                const uint64_t at = __umul64hi(f.u, total);
-                const int t = threadIdx.x;
-                if (t < n_kept && sh.lw[t]) {
-                    const uint64_t e = sh.list[t];
-                    uint64_t a = 0;
-                    for (int j = 0; j < n_kept; ++j)
-                        if (uint32_t(sh.list[j]) > uint32_t(e)) a += sh.lw[j];   // lower tokens
-                    if (a <= at && at < a + sh.lw[t])
+            // the draw: the kept weights by slices of the tokens, the slice of the goal, its elements compared
+            unsigned long long* const slices = reinterpret_cast<unsigned long long*>(sh.lo);
+            const float by_tok = float(SP_NT) / float(V);
+            slices[threadIdx.x] = 0;
+            if (threadIdx.x == 0) sh.first[0] = 0;
+            __syncthreads();
+            int at[2] = {-1, -1};
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (i + e < n_kept) {
+                    at[e] = min(int(float(list_tok(sh.list[i + e])) * by_tok), SP_NT - 1);
+                    atomicAdd(&slices[at[e]], (unsigned long long)w[e]);
+                }
+            __syncthreads();
+            const uint64_t own = slices[threadIdx.x], pick = __umul64hi(f.u, total);
+            block_scan(own, before);
+            if (before <= pick && pick < before + own) sh.x.bin = threadIdx.x, sh.x.above = before;
+            __syncthreads();
+            uint64_t* const some = sh.lw;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (at[e] >= 0 && at[e] == int(sh.x.bin)) {
+                    const uint32_t q = atomicAdd(&sh.first[0], 1u);
+                    if (q < SP_FEW / 2) some[2 * q] = uint64_t(list_tok(sh.list[i + e])), some[2 * q + 1] = w[e];
+                }
+            __syncthreads();
+            const int ns = int(sh.first[0]);
+            if (ns <= SP_FEW / 2) {
+                if (int(threadIdx.x) < ns) {
+                    const uint64_t me = some[2 * threadIdx.x];
+                    uint64_t a = sh.x.above;
+                    for (int q = 0; q < ns; ++q) a += some[2 * q] < me ? some[2 * q + 1] : 0;
+                    if (a <= pick && pick < a + some[2 * threadIdx.x + 1])
                         for (uint32_t q = 0; q < S; ++q) {
-                            st_dsmem_u32(dsmem_addr(&sh.token, q), uint32_t(list_tok(e)));
+                            st_dsmem_u32(dsmem_addr(&sh.token, q), uint32_t(me));
                             st_dsmem_u32(dsmem_addr(&sh.done, q), 1u);
                         }
                 }
-            } else if (threadIdx.x == 0) {
+            } else if (threadIdx.x == 0) {                 // (more neighbouring tokens than that: by a pass over the row)
                 post_kept(sh.list[n_kept - 1]);
                 for (uint32_t q = 0; q < S; ++q) st_dsmem_u32(dsmem_addr(&sh.done, q), 0u);
             }
@@ -1132,7 +1225,7 @@ struct Sampler {
 
 // The token of one row, to every thread of the cluster; -1 for a row that holds nothing but -inf and NaN.
 // `data`: the CTA's shared memory for its slice. sh.f is set by a thread before.
-template <typename T>
+template <typename T, bool HELD>
 __device__ int sp_row(const T* row, int V, int seg, SpShared& sh, uint4* data, int* status) {
     using E = SpElem<T>;
     constexpr int VEC = E::VEC;
@@ -1154,30 +1247,20 @@ __device__ int sp_row(const T* row, int V, int seg, SpShared& sh, uint4* data, i
             low = x[e] > -INFINITY ? fminf(low, x[e]) : low;
         }
     };
-    const int i0 = shift ? 1 : 0, i1 = (shift + (hi - lo)) / VEC;       // whole vectors
+    // (thread t has vectors t, t + SP_NT, ..., as every pass over the slice by single vectors)
+    const Slice<T, false> mem{reinterpret_cast<const uint4*>(base), row, nv, lo - shift, lo, hi, false};
     constexpr int U = 4;
-    for (int i = i0 + int(threadIdx.x); i < i1; i += U * SP_NT) {
+    for (int i = threadIdx.x; i < nv; i += U * SP_NT) {
         uint4 v[U];
 #pragma unroll
         for (int k = 0; k < U; ++k)
-            if (i + k * SP_NT < i1) v[k] = __ldg(reinterpret_cast<const uint4*>(base) + i + k * SP_NT);
+            if (i + k * SP_NT < nv) v[k] = mem.raw(i + k * SP_NT);
 #pragma unroll
         for (int k = 0; k < U; ++k)
-            if (i + k * SP_NT < i1) {
+            if (i + k * SP_NT < nv) {
                 v[k] = E::clean4(v[k]);
-                data[i + k * SP_NT] = v[k];
+                if (HELD) data[i + k * SP_NT] = v[k];
                 see(v[k]);
-            }
-    }
-    if (threadIdx.x < 2 && nv > 0) {                                    // the ends, element by element
-        const int i = threadIdx.x == 0 ? 0 : nv - 1;
-        if ((i < i0 || i >= i1) && (threadIdx.x == 0 || nv > 1 || i0 == 0))
-            for (int e = 0; e < VEC; ++e) {
-                const int at = i * VEC + e;
-                const float x = at >= shift && at < shift + (hi - lo) ? E::get(base + at) : -INFINITY;
-                E::put(reinterpret_cast<T*>(data) + at, x);
-                top = fmaxf(top, x);
-                low = x > -INFINITY ? fminf(low, x) : low;
             }
     }
     __syncthreads();
@@ -1213,10 +1296,11 @@ __device__ int sp_row(const T* row, int V, int seg, SpShared& sh, uint4* data, i
     }
     int tok = -1;
     if (top > -INFINITY) {
-        Sampler<T> s{sh, Slice{data, nv, lo - shift}, S, cr, Weigher<E::EXACT>{}};
+        Sampler<T, HELD> s{sh, Slice<T, HELD>{HELD ? data : mem.v, row, nv, lo - shift, lo, hi, false}, S, cr,
+                           Weigher<E::EXACT>{}};
         if (f.greedy) {                                    // the maximum's lowest token
             uint32_t best = 0xffffffffu;
-            s.each([&](float x, int t) { if (x == top) best = min(best, uint32_t(t)); });
+            if (mine == top) s.each([&](float x, int t) { if (x == top) best = min(best, uint32_t(t)); });
             best = __reduce_min_sync(0xffffffffu, best);
             __syncthreads();
             if (lane == 0) sh.redc[wid] = best;
@@ -1228,23 +1312,20 @@ __device__ int sp_row(const T* row, int V, int seg, SpShared& sh, uint4* data, i
             tok = int(best);
         } else {
             if (top == INFINITY) {                         // it holds all the weight: nothing else is kept
-                for (int i = threadIdx.x; i < nv; i += SP_NT) {
-                    float x[VEC];
-                    E::widen(data[i], x);
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e)
-                        E::put(reinterpret_cast<T*>(data) + i * VEC + e, x[e] == INFINITY ? 0.f : -INFINITY);
-                }
-                __syncthreads();
+                s.sl.only_inf = true;
                 top = low = 0.f, reach = 0;
             }
             s.wg = sp_weigher<E::EXACT>(top, f, sh.table);
             Kept kept{-INFINITY, -1};
             bool done = false, cut = f.p < 1.f;
             if (short_k) {
-                const uint32_t n = s.gather([&](float x, int) { return x > -INFINITY && ord_f32(x) >= reach; });
+                if (s.sl.only_inf || ord_f32(mine) >= reach)           // (the thread has some)
+                    s.each([&](float x, int t) {
+                        if (x > -INFINITY && ord_f32(x) >= reach) s.take(x, t);
+                    });
+                const uint32_t n = s.listed();
                 if (n <= uint32_t(SP_LIST)) {
-                    done = s.finish_in_list(int(n), f, kept, tok);
+                    done = s.finish_in_list(int(n), f, V, kept, tok);
                     cut = false;
                 } else {
                     kept = s.template select<false>(kept, f, low);
@@ -1287,7 +1368,7 @@ __device__ __forceinline__ void sp_filter(const SampleArgs& a, int r, float u, S
     sh.f = f;
 }
 
-template <typename T, bool TREE>
+template <typename T, bool TREE, bool HELD>
 __global__ void __launch_bounds__(SP_NT, 2) sample_kernel(const __grid_constant__ SampleArgs a) {
     extern __shared__ __align__(16) uint4 sp_data[];
     __shared__ SpShared sh;
@@ -1300,7 +1381,7 @@ __global__ void __launch_bounds__(SP_NT, 2) sample_kernel(const __grid_constant_
     const T* x = static_cast<const T*>(a.x);
     if constexpr (!TREE) {
         if (threadIdx.x == SP_NT - 1) sp_filter(a, r, a.u[r], sh);
-        const int tok = sp_row<T>(x + size_t(r) * a.ld, a.V, a.seg, sh, sp_data, a.status);
+        const int tok = sp_row<T, HELD>(x + size_t(r) * a.ld, a.V, a.seg, sh, sp_data, a.status);
         if (cr == 0 && threadIdx.x == 0) a.tok[r] = tok;
     } else {
         const int SL = a.B + 1, n = min(SL, a.n_nodes[r]);
@@ -1312,7 +1393,7 @@ __global__ void __launch_bounds__(SP_NT, 2) sample_kernel(const __grid_constant_
             if (row < 0 || row >= a.per) break;            // no row for this depth
             const size_t at = size_t(r) * a.per + row;
             if (threadIdx.x == SP_NT - 1) sp_filter(a, r, a.u[at], sh), found_s = 0x7fffffff;
-            const int t = sp_row<T>(x + at * a.V, a.V, a.seg, sh, sp_data, a.status);
+            const int t = sp_row<T, HELD>(x + at * a.V, a.V, a.seg, sh, sp_data, a.status);
             for (int j = 1 + int(threadIdx.x); j < n; j += SP_NT)
                 if (pr[j] == cur && tk[j] == t) atomicMin(&found_s, j);
             __syncthreads();
@@ -1350,23 +1431,16 @@ bool sample_supported(int V, int dtype) {
     return V <= (1 << 20) && sp_bytes(V, SP_MAXC, dtype == DARTREE_BF16 ? 2 : 4) <= SP_MOST;
 }
 
-template <typename T, bool TREE>
-static int launch_sample_t(SampleArgs a, int rows, cudaStream_t stream) {
-    const int es = int(sizeof(T));
-    // as few CTAs as leave room for two on an SM, more while that does not fill the SMs
-    int S = 1;
-    while (S < SP_MAXC && (sp_bytes(a.V, S, es) > SP_SLICE ||
-                           (int64_t(rows) * S * 2 <= 2 * num_sms() && a.V / (2 * S) >= 1024)))
-        S *= 2;
+template <typename T, bool TREE, bool HELD>
+static int launch_sample_t(SampleArgs& a, int rows, int S, cudaStream_t stream) {
     a.seg = sp_seg(a.V, S);
-    const int bytes = sp_bytes(a.V, S, es);
-    auto kern = sample_kernel<T, TREE>;
+    auto kern = sample_kernel<T, TREE, HELD>;
     static std::atomic<uint64_t> raised{0};
-    if (!raise_smem(kern, SP_MOST, raised)) return DARTREE_ECUDA;
+    if (HELD && !raise_smem(kern, SP_MOST, raised)) return DARTREE_ECUDA;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned(rows) * unsigned(S));
     cfg.blockDim = dim3(SP_NT);
-    cfg.dynamicSmemBytes = size_t(bytes);
+    cfg.dynamicSmemBytes = HELD ? size_t(sp_bytes(a.V, S, int(sizeof(T)))) : 0;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2] = {pdl_attribute()};
     attr[1].id = cudaLaunchAttributeClusterDimension;
@@ -1376,6 +1450,27 @@ static int launch_sample_t(SampleArgs a, int rows, cudaStream_t stream) {
     cfg.numAttrs = 2;
     KTimer kt_(TREE ? KID_SAMPLE_WALK : KID_SAMPLE, stream);
     return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? DARTREE_OK : DARTREE_ECUDA;
+}
+
+// Rows held in shared memory: as few CTAs to a row as leave room for two on an SM, more while that does not fill
+// the SMs. Batches that do not run at once that way are read again by each pass instead, by as many CTAs as fill
+// the SMs.
+template <typename T, bool TREE>
+static int launch_sample_rows(SampleArgs& a, int rows, cudaStream_t stream) {
+    const int es = int(sizeof(T));
+    const int64_t slots = 2 * num_sms();
+    int S = 1;
+    while (S < SP_MAXC &&
+           (sp_bytes(a.V, S, es) > SP_SLICE || (int64_t(rows) * S * 2 <= slots && a.V / (2 * S) >= 1024)))
+        S *= 2;
+    if constexpr (!TREE) {
+        if (int64_t(rows) * S > slots && S > 1) {
+            S = 1;
+            while (S < SP_MAXC && int64_t(rows) * S * 2 <= slots) S *= 2;
+            return launch_sample_t<T, false, false>(a, rows, S, stream);
+        }
+    }
+    return launch_sample_t<T, TREE, true>(a, rows, S, stream);
 }
 
 static SampleArgs sample_args(const void* x, int V, const dartree_filter& f, const float* u, int* status) {
@@ -1390,8 +1485,8 @@ int launch_sample(const void* logits, int rows, int V, int64_t ld, int dtype, co
                   int32_t* tok, int* status, cudaStream_t stream) {
     SampleArgs a = sample_args(logits, V, f, u, status);
     a.ld = ld, a.tok = tok;
-    return dtype == DARTREE_BF16 ? launch_sample_t<bf16_t, false>(a, rows, stream)
-                                 : launch_sample_t<float, false>(a, rows, stream);
+    return dtype == DARTREE_BF16 ? launch_sample_rows<bf16_t, false>(a, rows, stream)
+                                 : launch_sample_rows<float, false>(a, rows, stream);
 }
 
 int launch_sample_walk(int C, int L, int B, const int32_t* tok, const int32_t* par, const int32_t* depth,
@@ -1403,8 +1498,8 @@ int launch_sample_walk(int C, int L, int B, const int32_t* tok, const int32_t* p
     a.L = L, a.B = B, a.per = node ? B + 1 : L;
     a.t_tok = tok, a.t_par = par, a.t_depth = node ? nullptr : depth, a.n_nodes = n_nodes;
     a.accepted = accepted, a.path = path, a.bonus = bonus;
-    return dtype == DARTREE_BF16 ? launch_sample_t<bf16_t, true>(a, C, stream)
-                                 : launch_sample_t<float, true>(a, C, stream);
+    return dtype == DARTREE_BF16 ? launch_sample_rows<bf16_t, true>(a, C, stream)
+                                 : launch_sample_rows<float, true>(a, C, stream);
 }
 
 }  // namespace dartree
