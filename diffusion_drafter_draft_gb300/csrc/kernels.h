@@ -35,7 +35,7 @@ enum KernelId {
     KID_STATE, KID_HEAP, KID_FINISH, KID_PRUNE, KID_MASK, KID_ROWMAX, KID_WALK, KID_ROWSAMPLE, KID_LMHEAD,
     KID_LMMERGE, KID_ATTN_PREP, KID_ATTN, KID_ATTN_COMBINE, KID_PAGED_APPEND, KID_PAGED_ATTN,
     KID_PAGED_COMBINE, KID_PAGED_WEIGHTS, KID_PAGED_SELECT, KID_PAGED_MOVE, KID_PAGED_COMMIT, KID_PAGED_RESERVE,
-    KID_PAGED_RELEASE, KID_SAMPLE, KID_SAMPLE_WALK, KID_OTHER,
+    KID_PAGED_RELEASE, KID_SAMPLE, KID_SAMPLE_WALK, KID_PAGED_OWN, KID_OTHER,
     KID_COUNT
 };
 // Brackets the launches of its scope with timing events when timing is enabled.

@@ -121,8 +121,11 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *slot;
-    griddep_launch_dependents();
+    // (SH: the launch behind may start before this one ends and does not wait itself until its merge, so what
+    // came before has to be done by then)
+    if (!SH) griddep_launch_dependents();
     griddep_wait();
+    if (SH) griddep_launch_dependents();
 
     // the last tiles (the most keys of a causal batch) first, of all heads or (x.inner) head by head
     const bool whole = SH && blockIdx.x < x.s.ctas;                       // (over shared rows)
@@ -862,18 +865,21 @@ int launch_paged_attention(const PagedArgs& a, const void* q, float scale, void*
 //
 // Requests that share their first rows: those rows are read once for a tile of 128 rows of q instead of once for
 // each request. The new tokens of a group lie together in q, so the general kernel takes them as one request's, all
-// of which see all shared rows; each request's own rows follow as in a call without groups, from the first row
-// behind the shared pages. Both leave (maximum, sum, O) in memory and paged_combine_kernel joins them.
+// of which see all shared rows, and leaves (maximum, sum, O) of each chunk in memory. Own rows of at most 16 rows of q
+// to a request are the launch behind it (paged_own.cu), which joins; others are CTAs of the same launch, from the
+// first row behind the shared pages on, and paged_combine_kernel joins.
 
 struct PgSharedPlan {
-    bool use, few, alone, few_alone;  // shared at all; own rows by the transposed kernel; one CTA to an SM
+    bool use, few, alone;             // shared at all; own rows by the transposed kernel; one CTA to an SM
     int tt, tiles, nt, np, ns;
     unsigned units;
     size_t ml, total;
 };
 
-// In us, as paged_plan does: the prefix's CTAs, the own rows' (behind them, or in the same launch), the join
-// (4 and the partial results there and back at 5 TB/s).
+// In us, fitted to sweeps like paged_plan's times. Shared rows: CTAs as there, and the partial results at 5 TB/s.
+// Own rows of few (paged_own.cu): 5, then for each round of two CTAs to an SM 3, a block 1.1 and the join's loads
+// 0.8 for every eight chunks; side by side with the shared rows' CTAs where both fit. Other own rows: as in
+// paged_plan, behind the shared rows' CTAs in the same launch; the join is a launch, 4.
 constexpr int64_t PG_SHARED_BYTES = int64_t(512) << 20;  // of partial rows, as long as there is a choice
 
 static PgSharedPlan shared_plan(const PagedArgs& a, const dartree_paged_groups& s) {
@@ -892,16 +898,8 @@ static PgSharedPlan shared_plan(const PagedArgs& a, const dartree_paged_groups& 
     const int64_t row_bytes = int64_t(a.T) * a.Hq * a.D * 4;
     const double chunk = double(row_bytes) * 2.0 / 5e6;
     auto waves_of = [](double load) { return load <= 1.0 ? 1.0 : load < 3.0 ? ceil(load) : load + 0.5; };
-    double best = 1e300, own_few = 1e300;
-    int ns_few = 1;
-    for (int64_t ns = 1; p.few && ns <= rb && ns <= 16; ++ns) {
-        const double load = double(heads * ns) / double(sms), tile = 4.0 * PG_BN * a.D * double(sms) / 6.7e6;
-        const double waves = floor(load / 2.0), rest = load - 2.0 * waves, per = double((rb + ns - 1) / ns);
-        const double t = chunk * double(ns) +
-            (load <= 2.0 ? 3.0 + fmax(per * (load <= 1.0 ? 0.9 : 1.25), double(heads) * double(rb) * tile / double(sms))
-                         : waves * (3.0 + per * 2.0 * tile) + (rest > 0.0 ? 3.0 + per * fmax(1.25, rest * tile) : 0.0));
-        if (t < own_few) own_few = t, ns_few = int(ns);
-    }
+    double best = 1e300;
+    const double rounds = ceil(double(heads) / double(2 * sms));
     for (int way = 0; way < 3; ++way) {
         if (way == 2 && a.D == 64) break;
         const int nt = way == 2 ? 2 : 1;
@@ -912,26 +910,36 @@ static PgSharedPlan shared_plan(const PagedArgs& a, const dartree_paged_groups& 
         const double ends = way == 0 ? 5.0 : way == 1 ? 4.0 : 6.0;
         const double block = a.D == 128 ? (way == 0 ? (many ? 2.1 : 2.5) : way == 1 ? (many ? 1.36 : 1.55) : 1.7)
                                         : (way == 0 ? 1.4 : 1.5);
-        double own = own_few, prefix = 1e300;
-        int ns = ns_few, np = 1;
+        const double own_few = 5.0 + rounds * (3.0 + 1.1 * double(rb));
+        double own = own_few;
+        int ns = 1;
         const double ctas = double(heads * ((p.tiles + nt - 1) / nt));
         for (int64_t n = 1; !p.few && n <= rb && n <= 4; ++n) {
-            const double t = ctas * double(n) / slots * (ends + block * double((rb + n - 1) / n)) + chunk * double(n);
+            const double t = ctas * double(n) / slots * (ends + block * double((rb + n - 1) / n)) + chunk * double(n) + 4.0;
             if (n == 1 || t < own) own = t, ns = int(n);
         }
-        for (int64_t n = 1; n <= pb && n <= 64; ++n) {
+        // (of the chunks that leave equally many blocks to each, the fewest)
+        for (int64_t n = 1, k = pb; n <= 64; n = (pb + k - 2) / (k - 1)) {
             if (n > 1 && (n + ns) * row_bytes > PG_SHARED_BYTES) break;
-            const double t = waves_of(double(base * n) / slots) * (ends + block * double((pb + n - 1) / n)) + chunk * double(n);
-            if (t < prefix) prefix = t, np = int(n);
-        }
-        if (own + prefix + 4.0 < best) {
-            best = own + prefix + 4.0;
-            p.nt = nt, p.np = np, p.ns = ns, p.alone = way == 1, p.units = unsigned(units);
+            k = (pb + n - 1) / n;
+            const double prefix = waves_of(double(base * n) / slots) * (ends + block * double(k)) + chunk * double(n);
+            const bool beside = p.few && double(base * n) / slots + double(heads) / double(2 * sms) <= 1.0;
+            const double t = (beside ? fmax(prefix, own) : prefix + own) + (p.few ? rounds * 0.8 * ceil(double(n) / 8.0) : 0.0);
+            if (t < best) {
+                best = t;
+                p.nt = nt, p.np = int(n), p.ns = ns, p.alone = way == 1, p.units = unsigned(units);
+            }
+            if (k == 1) break;
         }
     }
-    p.few_alone = heads * p.ns <= sms;
-    p.use = s.always || best < paged_plan(a, most_rows + most_rest).us;
-    const int64_t rows = int64_t(a.T) * a.Hq * (p.np + p.ns);
+    // Where sharing pays, from sweeps of 26 batches (both ways' times for each): the plain call's requests find the
+    // shared rows in the L2, so that its expected times are high; few rows: 64 tokens behind 16384 rows 59 us against 357,
+    // 48 requests of three tokens in five groups 28 against 35, 40 tokens behind 1205 rows 19 against 17. More rows than
+    // that only save what the requests' own tiles leave empty: ten trees of 34 slots (136 rows) behind 6932 rows 63 against
+    // 82, sixteen of 65 (260 rows) behind 8192 141 against 111.
+    const double plain = paged_plan(a, most_rows + most_rest).us;
+    p.use = s.always || (p.few ? 1.1 * best + 2.5 < 0.95 * plain : a.S * grp < 2 * PG_BM && best < 0.75 * plain);
+    const int64_t rows = int64_t(a.T) * a.Hq * (p.np + (p.few ? 0 : p.ns));
     p.ml = (size_t(rows) * a.D * 4 + 255) / 256 * 256;
     p.total = p.ml + (size_t(rows) * 8 + 255) / 256 * 256;
     return p;
@@ -974,7 +982,7 @@ int launch_paged_shared(const PagedArgs& a, const void* q, const dartree_paged_g
         if (!make_query_map(&tf, a, q, a.S)) return DARTREE_ECUDA;
         PgArgs y = x;
         y.tt = a.S, y.tiles = 1, y.rows = a.S * grp;
-        if ((e = launch_paged_few(y, false, p.few_alone, tf, tk, tv, stream))) return e;
+        return launch_paged_own(y, tf, tk, tv, stream);
     }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned((size_t(a.C) * a.S * a.Hq + 7) / 8));

@@ -44,16 +44,18 @@ __device__ __forceinline__ bool paged_in_group(const PgArgs& x, int c) {
 // Rows that request c shares with its group, in whole pages (0: no group). By a whole warp, the same for all lanes.
 __device__ __forceinline__ int paged_shared_rows(const PgArgs& x, int c) {
     const int lane = threadIdx.x & 31;
-    int n = 0;                                            // starts up to c
-    for (int j = 0; j <= x.s.G; j += 32) {
-        const bool in = j + lane <= x.s.G && x.s.start[j + lane] <= c;
-        const unsigned b = __ballot_sync(0xffffffffu, in);
+    int n = 0, rows = 0;                                  // starts up to c; the last one's rows
+    for (int j = 0; j <= x.s.G; j += 32) {                // (starts and rows at once: one round of loads for 31 groups)
+        const int s = j + lane <= x.s.G ? x.s.start[j + lane] : 0x7fffffff;
+        const int r = j + lane < x.s.G ? x.s.rows[j + lane] : 0;
+        const unsigned b = __ballot_sync(0xffffffffu, s <= c);
+        if (b) rows = __shfl_sync(0xffffffffu, r, 31 - __clz(b));
         n += __popc(b);
         if (b != 0xffffffffu) break;
     }
     if (n == 0 || n > x.s.G) return 0;
     const int64_t cap = int64_t(x.a.max_pages) << x.a.log2_page;
-    return int(min(int64_t(max(x.s.rows[n - 1], 0)), cap)) & ~(x.a.page - 1);
+    return int(min(int64_t(max(rows, 0)), cap)) & ~(x.a.page - 1);
 }
 
 // The `unit`-th run of `per` tokens of the groups' tokens: its group's first request, rows of q, tokens, shared
@@ -181,8 +183,29 @@ __device__ __forceinline__ void paged_merge(const PgArgs& x, const float* ob, in
     }
 }
 
+constexpr int PF_BM = 128;           // few rows: keys of a block
+constexpr int PF_N = 16;             // rows
+
+// Column-wise reduction of 16 values per lane over a warp: lane i gets column i % 16.
+template <class F>
+__device__ __forceinline__ float warp_columns(float (&v)[PF_N], int lane, F op) {
+#pragma unroll
+    for (int w = PF_N / 2; w > 0; w >>= 1) {
+        const bool up = lane & w;
+#pragma unroll
+        for (int k = 0; k < w; ++k) {
+            const float mine = up ? v[k + w] : v[k], other = up ? v[k] : v[k + w];
+            v[k] = op(mine, __shfl_xor_sync(0xffffffffu, other, w));
+        }
+    }
+    return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
+}
+
 // Few rows (paged_few.cu): tiles of 16 rows, one per request and key/value head.
 int launch_paged_few(const PgArgs& x, bool cluster, bool alone, const CUtensorMap& tq,
                      const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t stream);
+// Their own rows in a call with shared prefixes, and the join (paged_own.cu).
+int launch_paged_own(const PgArgs& x, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                     cudaStream_t stream);
 
 }  // namespace dartree

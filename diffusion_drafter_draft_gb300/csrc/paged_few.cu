@@ -26,8 +26,6 @@
 
 namespace dartree {
 
-constexpr int PF_BM = 128;   // keys of a block
-constexpr int PF_N = 16;     // rows
 constexpr int PF_NT = 192;
 
 template <int D, int ST>
@@ -51,23 +49,7 @@ struct PfSmem {
     static_assert(PF_N * PITCH * 4 <= ST * TILE, "merge fits in the ring's place");
 };
 
-// Column-wise reduction of 16 values per lane over a warp: lane i gets column i % 16.
-template <class F>
-__device__ __forceinline__ float warp_columns(float (&v)[PF_N], int lane, F op) {
-#pragma unroll
-    for (int w = PF_N / 2; w > 0; w >>= 1) {
-        const bool up = lane & w;
-#pragma unroll
-        for (int k = 0; k < w; ++k) {
-            const float mine = up ? v[k + w] : v[k], other = up ? v[k] : v[k + w];
-            v[k] = op(mine, __shfl_xor_sync(0xffffffffu, other, w));
-        }
-    }
-    return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
-}
-
-// SH: a call with shared prefixes; the request's own rows, from row `kb` on, to memory.
-template <int D, int ST, bool CL, bool SH>
+template <int D, int ST, bool CL>
 __global__ void __launch_bounds__(PF_NT, 2)
     paged_few_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PgArgs x) {
@@ -110,10 +92,8 @@ __global__ void __launch_bounds__(PF_NT, 2)
     const int c = cg / a.Hkv, g = cg - c * a.Hkv;
     bool bad;
     const PagedRequest r = paged_request(a, c, bad);
-    const int kb = SH ? paged_shared_rows(x, c) : 0;
-    bad |= kb > r.n_old;
     if (bad && threadIdx.x == 0 && g == 0) set_status(a.status, DARTREE_EINTERNAL);
-    const int blocks = r.n_new > 0 ? (max(r.n_keys - kb, 0) + PF_BM - 1) / PF_BM : 0;
+    const int blocks = r.n_new > 0 ? (r.n_keys + PF_BM - 1) / PF_BM : 0;
     const int per = (blocks + x.nchunk - 1) / x.nchunk;
     const int b0 = chunk * per, nblk = max(min(blocks, b0 + per) - b0, 0);
 
@@ -132,12 +112,12 @@ __global__ void __launch_bounds__(PF_NT, 2)
             // this lane's table entry of block b (looked up two blocks ahead, checked when it is used), and
             // the page to fetch: n_pages, beyond the pool and so all zeros, past the end and for no page
             auto entry_of = [&](int b) -> int {
-                const int j = kb + b * PF_BM + su * pr;
+                const int j = b * PF_BM + su * pr;
                 return mine && j < r.n_keys ? table[j >> a.log2_page] : a.n_pages;
             };
             auto page_of = [&](int e, int b) -> int {
                 if (unsigned(e) < unsigned(a.n_pages)) return e;
-                if (mine && kb + b * PF_BM + su * pr < r.n_keys) set_status(a.status, DARTREE_EINTERNAL);
+                if (mine && b * PF_BM + su * pr < r.n_keys) set_status(a.status, DARTREE_EINTERNAL);
                 return a.n_pages;
             };
             int e0 = entry_of(b0), e1 = entry_of(b0 + 1), issued = 0;
@@ -156,7 +136,7 @@ __global__ void __launch_bounds__(PF_NT, 2)
                     __syncwarp();
                     if (mine)
                         tc::tma_load_4d(smem + s * L::TILE + pn * L::PANEL + size_t(su) * pr * 128, kv ? &tmV : &tmK,
-                                        64 * pn, (kb + (b0 + i) * PF_BM + su * pr) & (a.page - 1), g, pg, &full[s]);
+                                        64 * pn, ((b0 + i) * PF_BM + su * pr) & (a.page - 1), g, pg, &full[s]);
                     issued = idx + 1;
                 }
             }
@@ -220,7 +200,7 @@ __global__ void __launch_bounds__(PF_NT, 2)
             return any != 0;
         };
         for (int i = 0; i < nblk; ++i) {
-            const int j = kb + (b0 + i) * PF_BM + key, s = j - r.n_old, vi = 2 * i + 1;
+            const int j = (b0 + i) * PF_BM + key, s = j - r.n_old, vi = 2 * i + 1;
             uint32_t seen = j < r.n_keys ? live : 0u;
             if (s >= 0 && seen) {                                    // a new row
                 if (!a.mask) {
@@ -238,7 +218,7 @@ __global__ void __launch_bounds__(PF_NT, 2)
             }
             ok = ok && mbar_wait_bounded(&sfull[i & 1], uint32_t(i >> 1) & 1u, a.status);
             if (i >= 2) ok = ok && mbar_wait_bounded(&pdone[i & 1], uint32_t((i >> 1) - 1) & 1u, a.status);
-            if (i + 1 == nblk && r.n_keys < kb + (b0 + nblk) * PF_BM) {
+            if (i + 1 == nblk && r.n_keys < (b0 + nblk) * PF_BM) {
                 // rows past the end may hold anything: their values are zeroed (0 * NaN is NaN)
                 ok = ok && mbar_wait_bounded(&full[vi % ST], uint32_t(vi / ST) & 1u, a.status);
                 if (ok && j >= r.n_keys) {
@@ -365,7 +345,7 @@ __global__ void __launch_bounds__(PF_NT, 2)
         const size_t o0 = size_t(r.q0) * a.Hq + size_t(g) * x.grp;
         auto row_of = [&](int n) -> size_t { return o0 + size_t(n / x.grp) * a.Hq + n % x.grp; };
         const int rows = a.q_start ? cols : x.rows;
-        if (!CL && !SH && x.nchunk == 1) {
+        if (!CL && x.nchunk == 1) {
             if (key < rows) {                                        // (a row's sum: by its number among the threads)
                 float lk = 0.f, mk = -INFINITY;
 #pragma unroll
@@ -385,10 +365,6 @@ __global__ void __launch_bounds__(PF_NT, 2)
             float2* const ml = reinterpret_cast<float2*>(smem + L::ML_OFF);
             int* const places = reinterpret_cast<int*>(smem + L::PLACE_OFF);
             const size_t pr = (size_t(cg) * x.nchunk + chunk) * x.rows;
-            // where row n's part goes: a tile's rows together, or (SH) by the row of q
-            auto part_of = [&](int n) -> size_t {
-                return SH ? size_t(x.s.np + chunk) * (size_t(a.T) * a.Hq) + row_of(n) : pr + n;
-            };
             if (key < PF_N) {
                 float2 mine = make_float2(-INFINITY, 0.f);
 #pragma unroll
@@ -398,7 +374,7 @@ __global__ void __launch_bounds__(PF_NT, 2)
                     ml[key] = mine;
                     places[key] = key < cols ? int(row_of(key)) : key < rows ? -2 - int(row_of(key)) : -1;
                 } else if (key < cols) {
-                    x.part_ml[part_of(key)] = mine;
+                    x.part_ml[pr + key] = mine;
                 }
             }
             float* const ob = reinterpret_cast<float*>(smem);
@@ -406,7 +382,7 @@ __global__ void __launch_bounds__(PF_NT, 2)
             for (int n = 0; n < PF_N; ++n)
                 if (n < cols && inv[n] > 0.f && key < D) {
                     if constexpr (CL) ob[n * L::PITCH + key] = __uint_as_float(o[n]);
-                    else x.part_o[part_of(n) * D + key] = __uint_as_float(o[n]);
+                    else x.part_o[(pr + n) * D + key] = __uint_as_float(o[n]);
                 }
             if constexpr (CL) {
                 __syncwarp();
@@ -428,10 +404,10 @@ __global__ void __launch_bounds__(PF_NT, 2)
     if (warp == 5) tc::tmem_dealloc(tmem, TCOLS);
 }
 
-template <int D, int ST, bool CL, bool SH = false>
+template <int D, int ST, bool CL>
 static int launch_few_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PgArgs& x,
                         cudaStream_t stream) {
-    auto kern = paged_few_kernel<D, ST, CL, SH>;
+    auto kern = paged_few_kernel<D, ST, CL>;
     const size_t smem = PfSmem<D, ST>::TOTAL;
     static std::atomic<uint64_t> raised{0};
     if (!raise_smem(kern, int(smem), raised)) return DARTREE_ECUDA;
@@ -453,13 +429,6 @@ static int launch_few_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
 // Alone on its SM a CTA has room for three blocks' keys and values (heads of 64: six), else two share the SM with half of that.
 int launch_paged_few(const PgArgs& x, bool cluster, bool alone, const CUtensorMap& tq, const CUtensorMap& tk,
                      const CUtensorMap& tv, cudaStream_t stream) {
-    if (x.s.G > 0) {
-        if (x.a.D == 64)
-            return alone ? launch_few_t<64, 12, false, true>(tq, tk, tv, x, stream)
-                         : launch_few_t<64, 6, false, true>(tq, tk, tv, x, stream);
-        return alone ? launch_few_t<128, 6, false, true>(tq, tk, tv, x, stream)
-                     : launch_few_t<128, 3, false, true>(tq, tk, tv, x, stream);
-    }
     if (x.a.D == 64)
         return cluster ? launch_few_t<64, 12, true>(tq, tk, tv, x, stream)
                : alone ? launch_few_t<64, 12, false>(tq, tk, tv, x, stream)

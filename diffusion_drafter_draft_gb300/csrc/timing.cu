@@ -49,7 +49,7 @@ const char* const kNames[KID_COUNT] = {
     "lmhead_merge_kernel", "attn_prep_kernel", "attn_kernel", "attn_combine_kernel",
     "paged_append_kernel", "paged_attn_kernel", "paged_combine_kernel", "paged_weights_kernel",
     "paged_select_kernel", "paged_move_kernel", "paged_commit_kernel",
-    "paged_reserve_kernel", "paged_release_kernel", "sample_kernel", "sample_walk_kernel", "other"};
+    "paged_reserve_kernel", "paged_release_kernel", "sample_kernel", "sample_walk_kernel", "paged_own_kernel", "other"};
 }  // namespace
 
 KTimer::KTimer(int id, cudaStream_t s) : id_(id), s_(s), b_(nullptr) {

@@ -721,7 +721,7 @@ DARTREE_API int dartree_selftest_wait(void* ws, size_t ws_bytes, int which, unsi
  * device time. Kernel ids 0..DARTREE_NUM_KERNEL_IDS-1, named by
  * dartree_kernel_name. Not for launches captured into a CUDA graph; adds two
  * event records per launch while on. */
-#define DARTREE_NUM_KERNEL_IDS 32
+#define DARTREE_NUM_KERNEL_IDS 33
 DARTREE_API int dartree_timing(int enable);
 DARTREE_API int dartree_timing_read(int kernel_id, int* launches, double* total_ms);
 DARTREE_API const char* dartree_kernel_name(int kernel_id);

@@ -175,5 +175,5 @@ def test_every_way_of_sharing_is_taken(dd):
 
 def test_kernel_families_are_named(dd):
     names = [dd.lib().dartree_kernel_name(i).decode() for i in range(dd.num_kernel_ids())]
-    for n in ("paged_reserve_kernel", "paged_release_kernel", "sample_kernel", "sample_walk_kernel"):
+    for n in ("paged_reserve_kernel", "paged_release_kernel", "sample_kernel", "sample_walk_kernel", "paged_own_kernel"):
         assert n in names
