@@ -1341,8 +1341,7 @@ __device__ int sp_row(const T* row, int V, int seg, SpShared& sh, uint4* data, i
             if (!done) tok = s.draw(kept, f);
         }
     }
-    cluster_sync();                                        // (what the next row writes has been read)
-    return tok;
+    return tok;                                            // (behind a cluster barrier and what is read of others)
 }
 
 // Settings of request r for the row with uniform number ui; what is no setting is an error and taken for none.
@@ -1360,8 +1359,11 @@ __device__ __forceinline__ void sp_filter(const SampleArgs& a, int r, float u, S
     if (!(u >= 0.f && u < 1.f)) bad = true, u = 0.f;
     if (bad) set_status(a.status, DARTREE_EINTERNAL);
     f.greedy = f.T == 0.f || f.k == 1 || f.p == 0.f;
-    const double c = fmin(369.32993046757463 / double(f.T > 0.f ? f.T : 1.f), 1e37);   // 256 / ln 2
-    f.ch = float(c), f.cl = float(c - double(f.ch));
+    // 256 / ln 2 (a pair) by T: the quotient, and the remainder's
+    constexpr float KH = 369.329925537109375f, KL = 4.9304653e-6f;
+    const float T = f.T > 0.f ? f.T : 1.f;
+    f.ch = fminf(__fdiv_rn(KH, T), 1e37f);
+    f.cl = f.ch < 1e37f ? __fdiv_rn(__fmaf_rn(-f.ch, T, KH) + KL, T) : 0.f;
     f.u = sp_fixed(u, 64, false), f.share = f.p < 1.f ? sp_fixed(f.p, 64, true) : 0;
     f.wmin = f.least < 1.f ? sp_fixed(f.least, SP_Q, true) : uint64_t(1) << SP_Q;
     f.cut = sp_fixed(0.99f * (1.0f - f.p) / float(a.V), SP_Q, false);
