@@ -40,6 +40,8 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
+#include <algorithm>
+
 #include "paged_attn.cuh"
 #include "tc.cuh"
 
@@ -870,6 +872,7 @@ int launch_paged_attention(const PagedArgs& a, const void* q, float scale, void*
 // first row behind the shared pages on, and paged_combine_kernel joins.
 
 struct PgSharedPlan {
+    int early, early_items;           // own rows of few: CTAs beside the shared rows' and what each takes
     bool use, few, alone;             // shared at all; own rows by the transposed kernel; one CTA to an SM
     int tt, tiles, nt, np, ns;
     unsigned units;
@@ -899,7 +902,6 @@ static PgSharedPlan shared_plan(const PagedArgs& a, const dartree_paged_groups& 
     const double chunk = double(row_bytes) * 2.0 / 5e6;
     auto waves_of = [](double load) { return load <= 1.0 ? 1.0 : load < 3.0 ? ceil(load) : load + 0.5; };
     double best = 1e300;
-    const double rounds = ceil(double(heads) / double(2 * sms));
     for (int way = 0; way < 3; ++way) {
         if (way == 2 && a.D == 64) break;
         const int nt = way == 2 ? 2 : 1;
@@ -910,8 +912,8 @@ static PgSharedPlan shared_plan(const PagedArgs& a, const dartree_paged_groups& 
         const double ends = way == 0 ? 5.0 : way == 1 ? 4.0 : 6.0;
         const double block = a.D == 128 ? (way == 0 ? (many ? 2.1 : 2.5) : way == 1 ? (many ? 1.36 : 1.55) : 1.7)
                                         : (way == 0 ? 1.4 : 1.5);
-        const double own_few = 5.0 + rounds * (3.0 + 1.1 * double(rb));
-        double own = own_few;
+        const double pair = 3.0 + 1.1 * double(rb);
+        double own = 0.0;
         int ns = 1;
         const double ctas = double(heads * ((p.tiles + nt - 1) / nt));
         for (int64_t n = 1; !p.few && n <= rb && n <= 4; ++n) {
@@ -922,9 +924,23 @@ static PgSharedPlan shared_plan(const PagedArgs& a, const dartree_paged_groups& 
         for (int64_t n = 1, k = pb; n <= 64; n = (pb + k - 2) / (k - 1)) {
             if (n > 1 && (n + ns) * row_bytes > PG_SHARED_BYTES) break;
             k = (pb + n - 1) / n;
-            const double prefix = waves_of(double(base * n) / slots) * (ends + block * double(k)) + chunk * double(n);
-            const bool beside = p.few && double(base * n) / slots + double(heads) / double(2 * sms) <= 1.0;
-            const double t = (beside ? fmax(prefix, own) : prefix + own) + (p.few ? rounds * 0.8 * ceil(double(n) / 8.0) : 0.0);
+            const double cta = ends + block * double(k), load = double(base * n) / slots;
+            const double prefix = waves_of(load) * cta + chunk * double(n);
+            double t = prefix + own;
+            if (p.few) {
+                // own CTAs that find room beside the shared rows' serve pairs for as long as these last
+                const int64_t left = load < 1.0 ? int64_t(2.0 * (1.0 - load) * double(sms)) : 0;
+                const int64_t most = left > 0 ? (heads + left - 1) / left : 0;
+                const int64_t early = std::min(most, std::max(int64_t(cta / pair), int64_t(1)));
+                const int64_t rest = heads - left * early;
+                const double join = 1.2 * ceil(double(n) / 8.0);
+                t = fmax(prefix, double(early) * pair) + 5.0 + join * double(std::max(early, int64_t(1)));
+                if (rest > 0) t += ceil(double(rest) / double(2 * sms)) * (pair + join);
+                // (pairs that run at once hold each other up, and own rows pass the memory)
+                t += 2.5 * double(heads) / double(2 * sms) + (heads > 2 * sms ? 3.0 : 0.0);
+                t = fmax(t, 10.0 + double(heads) * double(most_rest) * a.D * 4.0 / 5.3e6);
+                if (t < best) p.early = int(std::min(left, (heads + most - 1) / std::max(most, int64_t(1)))), p.early_items = int(early);
+            }
             if (t < best) {
                 best = t;
                 p.nt = nt, p.np = int(n), p.ns = ns, p.alone = way == 1, p.units = unsigned(units);
@@ -932,14 +948,14 @@ static PgSharedPlan shared_plan(const PagedArgs& a, const dartree_paged_groups& 
             if (k == 1) break;
         }
     }
-    // Where sharing pays, from sweeps of 26 batches (both ways' times for each): the plain call's requests find the
-    // shared rows in the L2, so that its expected times are high; few rows: 64 tokens behind 16384 rows 59 us against 357,
-    // 48 requests of three tokens in five groups 28 against 35, 40 tokens behind 1205 rows 19 against 17. More rows than
-    // that only save what the requests' own tiles leave empty: ten trees of 34 slots (136 rows) behind 6932 rows 63 against
-    // 82, sixteen of 65 (260 rows) behind 8192 141 against 111.
-    const double plain = paged_plan(a, most_rows + most_rest).us;
-    p.use = s.always || (p.few ? 1.1 * best + 2.5 < 0.95 * plain : a.S * grp < 2 * PG_BM && best < 0.75 * plain);
-    const int64_t rows = int64_t(a.T) * a.Hq * (p.np + (p.few ? 0 : p.ns));
+    // Where sharing pays, from sweeps of 63 batches of few rows and 26 of more (both ways' times for each). The plain call's
+    // requests find the shared rows in the L2, so that of its expected time over 25 about half comes true. Few rows: 64
+    // tokens behind 16384 rows 56 us against 357, 8 behind 2048 13.1 against 15.2, 64 behind 442 28 against 25, 128 with 998
+    // of their own behind 470 96 against 71. More rows than that only save what the requests' own tiles leave empty: ten
+    // trees of 34 slots (136 rows) behind 6932 rows 63 against 82, sixteen of 65 (260 rows) behind 8192 141 against 111.
+    const double plain = paged_plan(a, most_rows + most_rest).us, met = plain < 25.0 ? plain : 25.0 + 0.5 * (plain - 25.0);
+    p.use = s.always || (p.few ? best < 0.92 * met : a.S * grp < 2 * PG_BM && best < 0.75 * plain);
+    const int64_t rows = int64_t(a.T) * a.Hq * (p.np + p.ns);
     p.ml = (size_t(rows) * a.D * 4 + 255) / 256 * 256;
     p.total = p.ml + (size_t(rows) * 8 + 255) / 256 * 256;
     return p;
@@ -968,7 +984,8 @@ int launch_paged_shared(const PagedArgs& a, const void* q, const dartree_paged_g
     // (own rows by the other kernel: no CTAs for them in this launch)
     PgArgs x{a, grp, p.tt, p.few ? 0 : p.tiles, p.ns, 0, 0, scale * LOG2E, static_cast<bf16_t*>(out), lse,
              reinterpret_cast<float*>(w), reinterpret_cast<float2*>(w + p.ml),
-             PgGroups{s.G, p.np, p.units, p.units * unsigned(a.Hkv) * unsigned(p.np), s.start, s.rows}};
+             PgGroups{s.G, p.np, p.units, p.units * unsigned(a.Hkv) * unsigned(p.np), s.start, s.rows,
+                      p.early, p.early_items}};
     int e;
     if (a.D == 64)
         e = (p.alone ? launch_attn_t<64, 1, 8, false, true> : launch_attn_t<64, 1, 4, false, true>)(tq, tk, tv, x, stream);

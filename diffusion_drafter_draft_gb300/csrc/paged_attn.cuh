@@ -22,6 +22,7 @@ struct PgGroups {
     unsigned units, ctas;             // CTAs' worth of tiles of all groups (a bound), CTAs of the prefix
     const int32_t* start;             // [G + 1] first requests
     const int32_t* rows;              // [G] rows shared
+    int early, early_items;           // own rows: the first CTAs take early_items (request, head) pairs each
 };
 
 struct PgArgs {

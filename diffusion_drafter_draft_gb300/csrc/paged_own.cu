@@ -7,20 +7,24 @@
 // request has beside a document that all have), so that a CTA for each (request, key/value head) would
 // be mostly its own start: 64 requests of 8 heads are 512 CTAs, two waves of 10 us. So one wave of CTAs goes through
 // them: tensor memory, barriers and descriptors are set up once, the next ones' keys and values are on their way
-// while one is finished, and the first ones' work runs beside the shared rows' launch, which lets this one start when all
-// its CTAs have waited for what came before; only the join waits for it.
+// while one is finished. The shared rows' launch lets this one start when all its CTAs have waited for what came before, and
+// only the join waits for that launch: CTAs that find an SM free beside it take more requests than the others.
 //
-// CTA = (request, key/value head), and the ones gridDim behind it:
-//   warps 0..3  softmax, one thread per key, and the products with V (warp 0); then, a warp to a row of q, the join
+// CTA = some (request, key/value head) pairs, one after another, then their join:
+//   warps 0..3  softmax, one thread per key, and the products with V (warp 0); O, maximum and sum as one more chunk,
+//               in memory and the last pair's in shared memory; then, a warp to a row of q, the join
 //   warp 4      producer: keys and values through a ring of ST stages; q when the scores before are done
 //   warp 5      issues S^T, a block ahead of the softmax, into one of two buffers
 // Blocks are numbered through all of a CTA's requests, so that the barriers' phases go on. Rows past the end may hold
 // anything: their scores are masked and their values zeroed. P is rounded to bf16, everything else is fp32. Every wait is
 // bounded; one that runs out records DARTREE_ETIMEOUT and ends the CTA's work.
-// 64 tokens behind 16384 shared rows and up to 512 of their own (134 MB, 20 us at the memory's rate): 59 us, of which the
-// shared rows' launch takes 27; a CTA for each request and head 65, with the join in a launch of its own 64. Bound by the
-// chain of a request's blocks, sums and chunks, two CTAs to an SM.
+// 64 tokens behind 16384 shared rows and up to 512 of their own (134 MB, 20 us at the memory's rate): 55.5 us with the
+// shared rows in 64 CTAs and three pairs to each of the 176 others, 61.5 with the shared rows on 128 SMs, 65 with a CTA for
+// each request and head. A CTA of one pair keeps no chunk in memory and is compiled by itself (8 tokens behind 2048 rows
+// 12.3 us, 14 with the loops). Bound by the chain of a pair's blocks, sums and chunks, two CTAs to an SM.
 #include <cuda.h>
+
+#include <algorithm>
 
 #include "paged_attn.cuh"
 #include "tc.cuh"
@@ -48,7 +52,8 @@ struct PoSmem {
     static_assert(2 * (TOTAL + 1024) <= 228 * 1024, "two CTAs fit in shared memory");
 };
 
-template <int D, int ST>
+// ONE: each CTA has one pair
+template <int D, int ST, bool ONE>
 __global__ void __launch_bounds__(PO_NT, 2)
     paged_own_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PgArgs x) {
@@ -88,7 +93,18 @@ __global__ void __launch_bounds__(PO_NT, 2)
     const uint32_t tmem = *slot;
     griddep_launch_dependents();     // (what comes before the shared rows' launch is done: that waited for it)
 
-    const int items = a.C * a.Hkv;
+    // this CTA's pairs: the first CTAs' early_items each, of the others an equal share (one more in the first of them)
+    const int items = a.C * a.Hkv, cta = int(blockIdx.x), first = min(x.s.early * x.s.early_items, items);
+    int it0, it1;
+    if (ONE) {
+        it0 = cta, it1 = cta + 1;
+    } else if (cta < x.s.early) {
+        it0 = min(cta * x.s.early_items, items), it1 = min(it0 + x.s.early_items, items);
+    } else {
+        const int others = int(gridDim.x) - x.s.early, i = cta - x.s.early, each = (items - first) / others,
+                  extra = (items - first) - each * others;
+        it0 = first + i * each + min(i, extra), it1 = it0 + each + int(i < extra);
+    }
     struct Item {
         int c, g, kb, nblk;
         PagedRequest r;
@@ -113,7 +129,7 @@ __global__ void __launch_bounds__(PO_NT, 2)
         const int su = lane % sub, pn = lane / sub;                       // this lane's page and panel
         const bool mine = pn < L::PANELS;
         int n = 0, issued = 0;                                            // items with blocks so far; stages filled
-        for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
+        for (int it = it0; it < it1 && ok; ++it) {
             const Item t = item_of(it);
             if (t.bad && t.g == 0 && lane == 0) set_status(a.status, DARTREE_EINTERNAL);
             if (t.nblk == 0) continue;
@@ -172,7 +188,7 @@ __global__ void __launch_bounds__(PO_NT, 2)
         // (warp-uniform values, one elected lane: descriptors stay in uniform registers)
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         int n = 0;
-        for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
+        for (int it = it0; it < it1 && ok; ++it) {
             const Item t = item_of(it);
             const int nb = __shfl_sync(0xffffffffu, t.nblk, 0), b0 = __shfl_sync(0xffffffffu, B, 0);
             if (nb == 0) continue;
@@ -226,7 +242,7 @@ __global__ void __launch_bounds__(PO_NT, 2)
                          : "=r"(any) : "r"(uint32_t(v)) : "memory");
             return any != 0;
         };
-        for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
+        for (int it = it0; it < it1 && ok; ++it) {
             const Item t = item_of(it);
             const PagedRequest& r = t.r;
             const int nblk = t.nblk, cols = r.n_new * x.grp;         // rows of q with a token
@@ -374,53 +390,77 @@ __global__ void __launch_bounds__(PO_NT, 2)
                 tc::tmem_ld16(trow + OCOL, o);
                 tc::fence_before_sync();
             }
-            // O as rows of q (in P's place: every product is done), maxima and sums
+            // one more chunk of the rows of q: in memory, the last pair's in P's place (every product is done)
+            const bool last = ONE || it + 1 == it1;
+            const size_t own = size_t(x.s.np) * step + size_t(r.q0) * a.Hq + size_t(t.g) * x.grp;
 #pragma unroll
             for (int n = 0; n < PF_N; ++n) {
                 const float sum = nblk > 0 ? (red[n] + red[PF_N + n]) + (red[2 * PF_N + n] + red[3 * PF_N + n]) : 0.f;
-                if (n == key) ml[n] = sum > 0.f ? make_float2(m[n], sum) : make_float2(-INFINITY, 0.f);
-                if (key < D && n < cols && nblk > 0) ob[n * D + key] = __uint_as_float(o[n]);
-            }
-            vote(false);
-            // ------------------------------------------------------------ join: a warp to a row of q
-            griddep_wait();                                          // the shared rows' launch
-            const int np = paged_in_group(x, t.c) ? x.s.np : 0;
-            const size_t o0 = size_t(r.q0) * a.Hq + size_t(t.g) * x.grp;
-            auto row_of = [&](int n) -> size_t { return o0 + size_t(n / x.grp) * a.Hq + n % x.grp; };
-            const int rows = a.q_start ? cols : x.rows;              // (slots without a node get zeros)
-            constexpr int V = D / 32, RW = PF_N / 4;
-            float2 pm[RW][2];                                        // chunks `lane` and `lane` + 32 of the warp's rows
-#pragma unroll
-            for (int q = 0; q < RW; ++q)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int n = warp + 4 * q, k = lane + 32 * h;
-                    pm[q][h] = n < cols && k < np ? __ldcg(x.part_ml + k * step + row_of(n)) : make_float2(-INFINITY, 0.f);
+                const size_t at = own + size_t(n / x.grp) * a.Hq + n % x.grp;
+                const float2 own_ml = sum > 0.f ? make_float2(m[n], sum) : make_float2(-INFINITY, 0.f);
+                if (last) {
+                    if (n == key) ml[n] = own_ml;
+                    if (key < D && n < cols && nblk > 0) ob[n * D + key] = __uint_as_float(o[n]);
+                } else if (n < cols) {
+                    if (n == key) x.part_ml[at] = own_ml;
+                    if (key < D && nblk > 0) x.part_o[at * D + key] = __uint_as_float(o[n]);
                 }
+            }
+            vote(false);                                             // (red is read)
+            B += nblk;
+        }
+        // ------------------------------------------------------------ join: a warp to a row of q
+        PagedRequest r{};
+        bool shares = false;                                         // (looked up before the waits)
+        auto look = [&](int it) {
+            if (!ONE && it < it0) return;
+            r = paged_request(a, it / a.Hkv);
+            shares = paged_in_group(x, it / a.Hkv);
+        };
+        look(it1 - 1);
+        griddep_wait();                                              // the shared rows' launch
+        for (int it = it1 - 1; it >= it0 && ok; --it) {
+            const bool last = ONE || it + 1 == it1;
+            const int g = it % a.Hkv;
+            const int cols = r.n_new * x.grp, rows = a.q_start ? cols : x.rows;   // (slots without a node get zeros)
+            const int np = shares ? x.s.np : 0;
+            const size_t o0 = size_t(r.q0) * a.Hq + size_t(g) * x.grp;
+            auto row_of = [&](int n) -> size_t { return o0 + size_t(n / x.grp) * a.Hq + n % x.grp; };
+            constexpr int V = D / 32, RW = PF_N / 4;
+            float2 pm[RW][3];                                        // chunks `lane` and `lane` + 32 (np <= 64), own rows
+#pragma unroll
+            for (int q = 0; q < RW; ++q) {
+                const int n = warp + 4 * q;
+#pragma unroll
+                for (int h = 0; h < 3; ++h) {
+                    const int k = h == 2 ? x.s.np : lane + 32 * h;
+                    pm[q][h] = make_float2(-INFINITY, 0.f);
+                    if (n < cols && (h == 2 || k < np)) pm[q][h] = h == 2 && last ? ml[n] : __ldcg(x.part_ml + k * step + row_of(n));
+                }
+            }
+            if (!ONE) look(it - 1);
 #pragma unroll
             for (int q = 0; q < RW; ++q) {
                 const int n = warp + 4 * q;
                 if (n >= rows) break;
-                const float2 own = n < cols ? ml[n] : make_float2(-INFINITY, 0.f);
-                float top = own.y > 0.f ? own.x : -INFINITY;
+                const size_t row = row_of(n);
+                float top = -INFINITY, fk[3];
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int h = 0; h < 3; ++h)
                     if (pm[q][h].y > 0.f) top = fmaxf(top, pm[q][h].x);
                 top = warp_max(top);
-                float fk[2], sum = 0.f;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    fk[h] = pm[q][h].y > 0.f ? ex2(pm[q][h].x - top) : 0.f;
-                    sum = fmaf(fk[h], pm[q][h].y, sum);
-                }
-                sum = warp_sum(sum);
-                const float fo = own.y > 0.f ? ex2(own.x - top) : 0.f;
-                sum = fmaf(fo, own.y, sum);
+                for (int h = 0; h < 3; ++h) fk[h] = pm[q][h].y > 0.f ? ex2(pm[q][h].x - top) : 0.f;
+                const float sum = fmaf(fk[2], pm[q][2].y, warp_sum(fmaf(fk[0], pm[q][0].y, fk[1] * pm[q][1].y)));
                 const float inv = sum > 0.f ? 1.0f / sum : 0.f;
                 float acc[V];
 #pragma unroll
-                for (int e = 0; e < V; ++e) acc[e] = fo > 0.f ? ob[n * D + lane * V + e] * (fo * inv) : 0.f;
-                const size_t row = row_of(n);
+                for (int e = 0; e < V; ++e) acc[e] = 0.f;
+                if (fk[2] > 0.f) {
+                    const float* src = x.part_o + (x.s.np * step + row) * D + lane * V;
+#pragma unroll
+                    for (int e = 0; e < V; ++e) acc[e] = (last ? ob[n * D + lane * V + e] : __ldcg(src + e)) * (fk[2] * inv);
+                }
                 for (int k0 = 0; k0 < np && n < cols; k0 += 8) {
                     float y[8][V], w[8];
 #pragma unroll
@@ -452,10 +492,7 @@ __global__ void __launch_bounds__(PO_NT, 2)
                 if (x.lse && lane == 0)
                     x.lse[row] = sum > 0.f ? (top + log2f(sum)) * 0.6931471805599453f : n < cols ? -INFINITY : 0.f;
             }
-            vote(false);                                             // (P's place and ml are read)
-            B += nblk;
         }
-        griddep_wait();                                              // (a CTA without items, too, ends behind that launch)
     }
     __syncwarp();
     tc::fence_before_sync();
@@ -466,15 +503,17 @@ __global__ void __launch_bounds__(PO_NT, 2)
 template <int D, int ST>
 static int launch_own_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PgArgs& x,
                         cudaStream_t stream) {
-    auto kern = paged_own_kernel<D, ST>;
     const size_t smem = PoSmem<D, ST>::TOTAL;
-    static std::atomic<uint64_t> raised{0};
-    if (!raise_smem(kern, int(smem), raised)) return DARTREE_ECUDA;
     cudaLaunchConfig_t cfg{};
+    // the early CTAs, and of others as many as the fewest rounds need
     const int64_t items = int64_t(x.a.C) * x.a.Hkv, slots = 2 * num_sms();
-    // (equal shares: as many CTAs as the fewest rounds need)
-    const int64_t rounds = (items + slots - 1) / slots;
-    cfg.gridDim = dim3(unsigned((items + rounds - 1) / rounds));
+    const int64_t left = items - std::min(items, int64_t(x.s.early) * x.s.early_items);
+    const int64_t rounds = (left + slots - 1) / slots;
+    const bool one = (x.s.early == 0 || x.s.early_items == 1) && rounds <= 1;
+    auto kern = one ? paged_own_kernel<D, ST, true> : paged_own_kernel<D, ST, false>;
+    static std::atomic<uint64_t> raised[2];
+    if (!raise_smem(kern, int(smem), raised[one])) return DARTREE_ECUDA;
+    cfg.gridDim = dim3(unsigned(one ? items : x.s.early + (rounds > 0 ? (left + rounds - 1) / rounds : 0)));
     cfg.blockDim = dim3(PO_NT);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
