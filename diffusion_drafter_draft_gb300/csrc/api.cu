@@ -863,7 +863,8 @@ int dartree_paged_reserve(const dartree_paged_params* p, const dartree_paged_ste
     if (!x || !x->n_free || !x->n_free_out || a.n_pages < 1 || a.max_pages < 1) return DARTREE_EINVAL;
     if (!x->q_start && int64_t(a.C) * a.S != a.T) return DARTREE_EINVAL;
     if (a.C > 0 && (!x->table || !x->n_ctx || !x->n_new || !x->free_pages || !x->granted ||
-                    overlap(x->granted, int64_t(a.C) * 4, x->n_new, int64_t(a.C) * 4)))
+                    overlap(x->granted, int64_t(a.C) * 4, x->n_new, int64_t(a.C) * 4) ||
+                    overlap(x->granted, int64_t(a.C) * 4, x->n_ctx, int64_t(a.C) * 4)))
         return DARTREE_EINVAL;
     if (x->slot && reinterpret_cast<uintptr_t>(x->slot) % 8 != 0) return DARTREE_EINVAL;
     if (int e = check_ws(ws, ws_bytes, paged_layout(a).part)) return e;
@@ -880,6 +881,8 @@ int dartree_paged_release(const dartree_paged_params* p, const int32_t* table, c
     if (a.C > 0 && (!table || !n_held || !n_keep || !free_pages ||
                     overlap(free_pages, int64_t(a.n_pages) * 4, table, int64_t(a.C) * a.max_pages * 4)))
         return DARTREE_EINVAL;
+    // (a turn's sums, were all its requests to give back all that the table holds)
+    if (int64_t(a.C < 512 ? a.C : 512) * a.max_pages >= (int64_t(1) << 31)) return DARTREE_EUNSUPPORTED;
     if (int e = check_ws(ws, ws_bytes, paged_layout(a).part)) return e;
     a.status = at<int>(ws, 0);
     return launch_paged_release(a, table, n_held, n_keep, n_shared, free_pages, n_free, n_free_out, as_stream(stream));

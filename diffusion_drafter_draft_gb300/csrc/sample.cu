@@ -21,9 +21,9 @@
 //           within 1e-3 of the weight which x hold the border; one pass takes the weights of all, of what
 //           lies above and of each warp's stretch, and lists what lies between; CTA 0 finds the border and the
 //           warp that holds the goal
-//   select  (where that is not enough: larger k, top-p of what it left, runs of equal values) a histogram of 2048 bins of x between maximum and minimum, weights or
-//           counts; the bin in which the goal is reached, as a list in CTA 0, sorted and summed; while a bin
-//           holds more than the list, finer bins of its keys (one value: the r-th by token)
+//   select  (where that is not enough: larger k, top-p of what it left, runs of equal values) the same histogram of
+//           weights or counts; the bin in which the goal is reached, as a list in CTA 0, sorted and summed; while a
+//           bin holds more than the list, finer bins of its keys (one value: the r-th by token)
 //   draw    sums of each warp's stretch of the row; the warp that holds the goal walks its own
 #include <math.h>
 
@@ -1397,7 +1397,7 @@ __global__ void __launch_bounds__(SP_NT, 2) sample_kernel(const __grid_constant_
             if (threadIdx.x == SP_NT - 1) sp_filter(a, r, a.u[at], sh), found_s = 0x7fffffff;
             const int t = sp_row<T, HELD>(x + at * a.V, a.V, a.seg, sh, sp_data, a.status);
             for (int j = 1 + int(threadIdx.x); j < n; j += SP_NT)
-                if (pr[j] == cur && tk[j] == t) atomicMin(&found_s, j);
+                if (t >= 0 && pr[j] == cur && tk[j] == t) atomicMin(&found_s, j);
             __syncthreads();
             const int next = found_s;
             __syncthreads();

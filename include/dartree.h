@@ -248,7 +248,7 @@ typedef struct {
 /* A token for each row of logits under `f`, from one uniform number u in [0, 1) a row: the lowest token at
  * which the sum of the kept w_0 .. w_v passes u times their whole sum. -inf is never drawn, nor is
  * NaN (counted as -inf); where the maximum is +inf, the tokens that reach it share the weight; a row
- * of -inf alone gives -1. Sums are exact sums of weights rounded to 2^-42 of the largest:
+ * of -inf alone gives -1. Sums are exact sums of weights rounded to 2^-43 of the largest:
  * a row's token does not depend on the batch it is in.
  *   logits  [rows, V], consecutive rows ld >= V elements apart, aligned to their type
  *   f       one request to a row
@@ -546,7 +546,7 @@ DARTREE_API int dartree_paged_commit_weights(const dartree_paged_params* p, cons
  *   n_new       [C] tokens wanted, 0..S (tree->n_nodes, say)
  *   free_pages  the stack, at least n_free entries; read only
  *   n_free      [1] pages on the stack, 0..n_pages; n_free_out [1]: what is left (may be n_free itself)
- *   granted     [C] n_new[c], or 0 (not part of n_new)
+ *   granted     [C] n_new[c], or 0 (not part of n_new or n_ctx)
  *   q_start     [C + 1] first rows of q of the granted tokens, as the other calls read them, or NULL:
  *               S rows of q to every request (T = C * S)
  *   slot        [T] place of each row of q in the pools: page * page size + row in it; -1: no token
@@ -575,7 +575,8 @@ DARTREE_API int dartree_paged_reserve(const dartree_paged_params* p, const dartr
 /* Pages go back: of request c, whose first n_held[c] rows have pages, those behind its first
  * max(n_keep[c], n_shared[c]) rows are put on the stack, in the requests' order and each request's from
  * the first on. For a finished request n_keep is 0, after a commit the rows cached then.
- *   table       [C, max_pages]; not written (entries behind a request's rows are never read)
+ *   table       [C, max_pages]; not written (entries behind a request's rows are never read); 512 requests' entries
+ *               (or all, if fewer) at most 2^31 (DARTREE_EUNSUPPORTED)
  *   n_shared    [C] leading rows whose pages are not the request's to give, or NULL: none
  *   free_pages  the stack, room for n_pages entries; n_free, n_free_out as for dartree_paged_reserve
  * DARTREE_EINTERNAL in the status word: n_free outside 0..n_pages, lengths below zero or past the block

@@ -177,3 +177,17 @@ def test_kernel_families_are_named(dd):
     names = [dd.lib().dartree_kernel_name(i).decode() for i in range(dd.num_kernel_ids())]
     for n in ("paged_reserve_kernel", "paged_release_kernel", "sample_kernel", "sample_walk_kernel", "paged_own_kernel"):
         assert n in names
+
+
+def test_reserve_and_release_sums_and_lengths_apart(dd):
+    L = dd.lib()
+    ptr = lambda n: ctypes.c_void_p(n)  # noqa: E731
+    # 512 requests that give back 2^22 pages each pass 31 bits (whatever the pool holds)
+    for C, pages, e in ((512, 1 << 22, dd.EUNSUPPORTED), (4096, 1 << 22, dd.EUNSUPPORTED), (511, 1 << 22, dd.EWORKSPACE),
+                        (512, (1 << 22) - 1, dd.EWORKSPACE)):
+        p = _p(dd, C=C, T=C, S=1, Hq=1, Hkv=1, page=16, max_pages=pages)
+        assert L.dartree_paged_release(ctypes.byref(p), ptr(1 << 44), ptr(4096), ptr(8192), None, ptr(1 << 20), ptr(12288),
+                                       ptr(12288), WS, 0, None) == e
+    x = dd.PagedStep(table=4096, n_ctx=1 << 20, n_new=1 << 21, free_pages=1 << 22, n_free=256, n_free_out=256,
+                     granted=(1 << 20) + 4)                     # lengths are read while grants are written
+    assert L.dartree_paged_reserve(ctypes.byref(_p(dd)), ctypes.byref(x), WS, 1 << 20, None) == dd.EINVAL
