@@ -202,3 +202,27 @@ def test_lengths_change_in_place_graph_and_streams(dd):
         out2 = x.cache.attention(x.q, shared=s, stream=side)
         side.synchronize()
         assert torch.equal(out2, got)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_requests_to_a_cta_again_and_again(dd, D):
+    """Several (request, head) pairs follow one another in a CTA, with rings that are refilled across them: every wait
+    ends, call after call, and outputs are the same."""
+    rng = np.random.default_rng(D)
+    rows = 320
+    x = tp.Case(dd, new=[1] * 128, old=[rows + int(n) for n in rng.integers(0, 700, 128)], Hq=8, Hkv=8, D=D, page=16,
+                seed=70 + D).fill()
+    s = _groups(x, [0, 128], [rows])
+    first = _run(x, s)
+    out, lse = torch.empty_like(first[0]), torch.empty_like(first[1])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(8):
+            x.cache.attention(x.q, shared=s, out=out, lse=lse)
+    for _ in range(25):
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert dd.read_status(s.ws) == 0
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    _check(x, s)
