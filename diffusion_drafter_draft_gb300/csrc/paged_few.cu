@@ -53,6 +53,7 @@ template <int D, int ST, bool CL>
 __global__ void __launch_bounds__(PF_NT, 2)
     paged_few_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PgArgs x) {
+    static_assert(ST == 3 || ST % 2 == 0, "what a stage of keys held before");
     using L = PfSmem<D, ST>;
     constexpr uint32_t OCOL = 2 * PF_N, TCOLS = 64;          // TMEM: S^T at 16 b, O^T at 32
     const PagedArgs& a = x.a;
@@ -159,10 +160,12 @@ __global__ void __launch_bounds__(PF_NT, 2)
             auto desc = [&](uint32_t at) { return (uint64_t(HI) << 32) | (LO | at); };
             bool ok = mbar_wait_bounded(qfull, 0, a.status);
             for (int i = 0; i < nb && ok; ++i) {
-                // (every phase of a stage is waited for, the values' before too: a wait two phases ahead
-                // would take the phase before for its own)
+                // A wait for a phase that is two ahead would take the one before for it, one for a phase that is two
+                // behind would not end. A stage of keys in a ring of three held the values of block i - 2 before, which
+                // are waited for elsewhere: once they were read, the keys' phase is the next. In an even ring it held
+                // keys.
                 const int ki = 2 * i, s = ki % ST;
-                if (i > 0) ok = mbar_wait_bounded(&full[(ki - 1) % ST], uint32_t((ki - 1) / ST) & 1u, a.status);
+                if (ST == 3 && i >= 2) ok = mbar_wait_bounded(&pdone[i & 1], uint32_t((i >> 1) - 1) & 1u, a.status);
                 ok = ok && mbar_wait_bounded(&full[s], uint32_t(ki / ST) & 1u, a.status);
                 if (ok && i >= 2) ok = mbar_wait_bounded(&sfree[i & 1], uint32_t((i >> 1) - 1) & 1u, a.status);
                 if (!ok) break;
