@@ -231,6 +231,12 @@ __global__ void __launch_bounds__(PO_NT, 2)
         // ---------------------------------------------------------------- softmax
         const int key = threadIdx.x;                                 // row of a block (TMEM lane)
         const uint32_t head1 = (1u << x.grp) - 1u;                   // (grp <= 16)
+        const uint32_t by_grp = 65535u / uint32_t(x.grp) + 1u;
+        // row of q of column n < 16 behind column 0's: the token n / grp, its head (exact; a division here is 40 instructions)
+        auto row_at = [&](int n) -> size_t {
+            const uint32_t t = uint32_t(n) * by_grp >> 16;
+            return size_t(t) * a.Hq + (uint32_t(n) - t * uint32_t(x.grp));
+        };
         const uint32_t trow = tmem + (uint32_t(warp * 32) << 16);
         float* const red = reinterpret_cast<float*>(smem + L::RED_OFF);
         float2* const ml = reinterpret_cast<float2*>(smem + L::ML_OFF);
@@ -399,7 +405,7 @@ __global__ void __launch_bounds__(PO_NT, 2)
 #pragma unroll
             for (int n = 0; n < PF_N; ++n) {
                 const float sum = nblk > 0 ? (red[n] + red[PF_N + n]) + (red[2 * PF_N + n] + red[3 * PF_N + n]) : 0.f;
-                const size_t at = own + size_t(n / x.grp) * a.Hq + n % x.grp;
+                const size_t at = own + row_at(n);
                 const float2 own_ml = sum > 0.f ? make_float2(m[n], sum) : make_float2(-INFINITY, 0.f);
                 if (last) {
                     if (n == key) ml[n] = own_ml;
@@ -428,7 +434,7 @@ __global__ void __launch_bounds__(PO_NT, 2)
             const int cols = r.n_new * x.grp, rows = a.q_start ? cols : x.rows;   // (slots without a node get zeros)
             const int np = shares ? x.s.np : 0;
             const size_t o0 = size_t(r.q0) * a.Hq + size_t(g) * x.grp;
-            auto row_of = [&](int n) -> size_t { return o0 + size_t(n / x.grp) * a.Hq + n % x.grp; };
+            auto row_of = [&](int n) -> size_t { return o0 + row_at(n); };
             constexpr int V = D / 32, RW = PF_N / 4;
             float2 pm[RW][3];                                        // chunks `lane` and `lane` + 32 (np <= 64), own rows
 #pragma unroll
@@ -447,6 +453,27 @@ __global__ void __launch_bounds__(PO_NT, 2)
                 const int n = warp + 4 * q;
                 if (n >= rows) break;
                 const size_t row = row_of(n);
+                // the chunks' O, eight at a time; the first are on their way before the weights (a chunk in which
+                // nothing was seen has no O: what is read has no weight)
+                float y[8][V];
+                auto fetch = [&](int k0) {
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+#pragma unroll
+                        for (int e = 0; e < V; ++e) y[u][e] = 0.f;
+                        if (k0 + u < np && n < cols) {
+                            const float* src = x.part_o + (size_t(k0 + u) * step + row) * D + lane * V;
+                            if (V == 4) {
+                                const float4 z = __ldcg(reinterpret_cast<const float4*>(src));
+                                y[u][0] = z.x, y[u][1] = z.y, y[u][V - 2] = z.z, y[u][V - 1] = z.w;
+                            } else {
+                                const float2 z = __ldcg(reinterpret_cast<const float2*>(src));
+                                y[u][0] = z.x, y[u][1] = z.y;
+                            }
+                        }
+                    }
+                };
+                fetch(0);
                 float top = -INFINITY, fk[3];
 #pragma unroll
                 for (int h = 0; h < 3; ++h)
@@ -465,29 +492,14 @@ __global__ void __launch_bounds__(PO_NT, 2)
                     for (int e = 0; e < V; ++e) acc[e] = (last ? ob[n * D + lane * V + e] : __ldcg(src + e)) * (fk[2] * inv);
                 }
                 for (int k0 = 0; k0 < np && n < cols; k0 += 8) {
-                    float y[8][V], w[8];
+                    if (k0 > 0) fetch(k0);
 #pragma unroll
                     for (int u = 0; u < 8; ++u) {
                         const int k = k0 + u;
-                        w[u] = __shfl_sync(0xffffffffu, k < 32 ? fk[0] : fk[1], k & 31) * inv;
-                        // (a chunk in which nothing was seen has no O)
+                        const float w = __shfl_sync(0xffffffffu, k < 32 ? fk[0] : fk[1], k & 31) * inv;
 #pragma unroll
-                        for (int e = 0; e < V; ++e) y[u][e] = 0.f;
-                        if (w[u] > 0.f) {
-                            const float* src = x.part_o + (size_t(k) * step + row) * D + lane * V;
-                            if (V == 4) {
-                                const float4 z = __ldcg(reinterpret_cast<const float4*>(src));
-                                y[u][0] = z.x, y[u][1] = z.y, y[u][V - 2] = z.z, y[u][V - 1] = z.w;
-                            } else {
-                                const float2 z = __ldcg(reinterpret_cast<const float2*>(src));
-                                y[u][0] = z.x, y[u][1] = z.y;
-                            }
-                        }
+                        for (int e = 0; e < V; ++e) acc[e] = w > 0.f ? fmaf(w, y[u][e], acc[e]) : acc[e];
                     }
-#pragma unroll
-                    for (int u = 0; u < 8; ++u)
-#pragma unroll
-                        for (int e = 0; e < V; ++e) acc[e] = fmaf(w[u], y[u][e], acc[e]);
                 }
                 uint32_t* dst = reinterpret_cast<uint32_t*>(x.out + row * D) + lane * (V / 2);
 #pragma unroll
