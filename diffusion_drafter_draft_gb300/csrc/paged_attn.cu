@@ -950,11 +950,11 @@ static PgSharedPlan shared_plan(const PagedArgs& a, const dartree_paged_groups& 
     }
     // Where sharing pays, from sweeps of 63 batches of few rows and 26 of more (both ways' times for each). The plain call's
     // requests find the shared rows in the L2, so that of its expected time over 25 about half comes true. Few rows: 64
-    // tokens behind 16384 rows 56 us against 357, 8 behind 2048 13.1 against 15.2, 64 behind 442 28 against 25, 128 with 998
+    // tokens behind 16384 rows 52 us against 357, 8 behind 2048 12.4 against 15.3, 64 behind 442 27 against 25, 128 with 998
     // of their own behind 470 96 against 71. More rows than that only save what the requests' own tiles leave empty: ten
     // trees of 34 slots (136 rows) behind 6932 rows 63 against 82, sixteen of 65 (260 rows) behind 8192 141 against 111.
     const double plain = paged_plan(a, most_rows + most_rest).us, met = plain < 25.0 ? plain : 25.0 + 0.5 * (plain - 25.0);
-    p.use = s.always || (p.few ? best < 0.92 * met : a.S * grp < 2 * PG_BM && best < 0.75 * plain);
+    p.use = s.always || (p.few ? best < 0.97 * met : a.S * grp < 2 * PG_BM && best < 0.75 * plain);
     const int64_t rows = int64_t(a.T) * a.Hq * (p.np + p.ns);
     p.ml = (size_t(rows) * a.D * 4 + 255) / 256 * 256;
     p.total = p.ml + (size_t(rows) * 8 + 255) / 256 * 256;

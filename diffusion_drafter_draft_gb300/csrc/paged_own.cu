@@ -18,10 +18,11 @@
 // Blocks are numbered through all of a CTA's requests, so that the barriers' phases go on. Rows past the end may hold
 // anything: their scores are masked and their values zeroed. P is rounded to bf16, everything else is fp32. Every wait is
 // bounded; one that runs out records DARTREE_ETIMEOUT and ends the CTA's work.
-// 64 tokens behind 16384 shared rows and up to 512 of their own (134 MB, 20 us at the memory's rate): 55.5 us with the
-// shared rows in 64 CTAs and three pairs to each of the 176 others, 61.5 with the shared rows on 128 SMs, 65 with a CTA for
-// each request and head. A CTA of one pair keeps no chunk in memory and is compiled by itself (8 tokens behind 2048 rows
-// 12.3 us, 14 with the loops). Bound by the chain of a pair's blocks, sums and chunks, two CTAs to an SM.
+// 64 tokens behind 16384 shared rows and up to 512 of their own (134 MB, 20 us at the memory's rate): 51.3 us with the
+// shared rows in 64 CTAs (38 us) and three pairs to each of 171 others; 55.6 before the joins fetched the chunks' O ahead of
+// their weights, 61.5 with the shared rows on 128 SMs, 65 with a CTA for each request and head. A CTA of one pair keeps
+// no chunk in memory and is compiled by itself (51 tokens behind 3496 rows 17.6 us, 21 with the loops). Bound by the
+// chain of a pair's lookups, blocks (1.7 us each), sums and chunks, two CTAs to an SM.
 #include <cuda.h>
 
 #include <algorithm>
