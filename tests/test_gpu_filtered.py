@@ -303,3 +303,30 @@ def test_streams_and_graphs(dd):
     side = dd.sample(x, u, stream=s, **kw)
     s.synchronize()
     assert torch.equal(side, got)
+
+
+def test_a_row_of_minus_infinity_matches_no_slot(dd):
+    """A slot whose token is -1 is not what such a row draws."""
+    tree = dict(tok=torch.tensor([[5, -1, 2]], dtype=torch.int32, device="cuda"),
+                par=torch.tensor([[-1, 0, 0]], dtype=torch.int32, device="cuda"),
+                depth=torch.tensor([[0, 1, 1]], dtype=torch.int32, device="cuda"),
+                n_nodes=torch.tensor([3], dtype=torch.int32, device="cuda"))
+    x = torch.full((1, 3, 8), float("-inf"), device="cuda")
+    r = dd.verify_filtered(tree, x, dd.ROWS_PER_NODE, 4, torch.full((1, 3), 0.5, device="cuda"))
+    assert r["accepted_len"].item() == 0 and r["bonus"].item() == -1 and r["path"].tolist() == [[-1] * 4]
+
+
+def test_draws_on_two_streams_at_once(dd):
+    """Calls that run beside one another, each with its own settings, draw what they draw alone."""
+    xs = [torch.randn(24, 30011, device="cuda") * (1 + i) for i in range(3)]
+    us = [torch.rand(24, device="cuda") for _ in range(3)]
+    kw = [dict(top_p=0.9), dict(temperature=0.6, top_k=40), dict(temperature=1.4, top_p=0.99, min_p=0.001)]
+    alone = [dd.sample(x, u, **k) for x, u, k in zip(xs, us, kw)]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        got += [(i, dd.sample(xs[i], us[i], stream=streams[i], **kw[i])) for i in range(3)]
+    torch.cuda.synchronize()
+    for i, t in got:
+        assert torch.equal(t, alone[i])

@@ -226,3 +226,21 @@ def test_many_requests_to_a_cta_again_and_again(dd, D):
         assert dd.read_status(s.ws) == 0
         assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
     _check(x, s)
+
+
+def test_two_caches_on_two_streams_at_once(dd):
+    xs, ss = [], []
+    for i in range(2):
+        x = tp.Case(dd, new=[1] * 48, old=[700 + 11 * c for c in range(48)], Hq=8, Hkv=8, page=32, seed=80 + i, spare=3000).fill()
+        xs.append(x), ss.append(_groups(x, [0, 48], [700]))
+    alone = [x.cache.attention(x.q, shared=s) for x, s in zip(xs, ss)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        got += [(i, xs[i].cache.attention(xs[i].q, shared=ss[i], stream=streams[i])) for i in range(2)]
+    torch.cuda.synchronize()
+    for i, out in got:
+        assert torch.equal(out, alone[i])
+    for s in ss:
+        assert dd.read_status(s.ws) == 0
