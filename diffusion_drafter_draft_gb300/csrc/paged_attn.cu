@@ -880,9 +880,9 @@ struct PgSharedPlan {
 };
 
 // In us, fitted to sweeps like paged_plan's times. Shared rows: CTAs as there, and the partial results at 5 TB/s.
-// Own rows of few (paged_own.cu): 5, then for each round of two CTAs to an SM 3, a block 1.1 and the join's loads
-// 0.8 for every eight chunks; side by side with the shared rows' CTAs where both fit. Other own rows: as in
-// paged_plan, behind the shared rows' CTAs in the same launch; the join is a launch, 4.
+// Own rows of few (paged_own.cu): 5, a (request, head) pair 3, a block 1.1 and the join's loads 1.2 for every eight
+// chunks, in rounds of two CTAs to an SM; pairs of CTAs that find room beside the shared rows' cost their joins only. Other
+// own rows: as in paged_plan, behind the shared rows' CTAs in the same launch; the join is a launch, 4.
 constexpr int64_t PG_SHARED_BYTES = int64_t(512) << 20;  // of partial rows, as long as there is a choice
 
 static PgSharedPlan shared_plan(const PagedArgs& a, const dartree_paged_groups& s) {
