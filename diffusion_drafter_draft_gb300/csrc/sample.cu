@@ -1377,9 +1377,11 @@ __global__ void __launch_bounds__(SP_NT, 2) sample_kernel(const __grid_constant_
     __shared__ int found_s;
     const uint32_t S = cluster_nctarank(), cr = cluster_ctarank();
     const int r = int(blockIdx.x / S);
+    cluster_arrive_release();
     for (int i = threadIdx.x; i < 256 * 8; i += SP_NT) sh.table[i] = sp_table.t[i >> 3];
     griddep_launch_dependents();
     griddep_wait();
+    cluster_wait_acquire();                                // every CTA has started: its shared memory may be written
     const T* x = static_cast<const T*>(a.x);
     if constexpr (!TREE) {
         if (threadIdx.x == SP_NT - 1) sp_filter(a, r, a.u[r], sh);
