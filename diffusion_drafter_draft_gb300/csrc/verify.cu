@@ -238,6 +238,7 @@ __global__ void __launch_bounds__(WK_NT) walk_node_kernel(int L, int B, int V, i
     const int32_t* pr = par + size_t(r) * SL;
     const int lo = int(cr) * seg, hi = min(V, lo + seg);
     int cur = 0, acc = 0, bon = -1;
+    cluster_arrive_release();
     for (int step = 0; step <= L; ++step) {
         const T* row = target + (size_t(r) * SL + cur) * V;
         const bool vec_ok = (reinterpret_cast<uintptr_t>(row) % 16) == 0;
@@ -247,6 +248,7 @@ __global__ void __launch_bounds__(WK_NT) walk_node_kernel(int L, int B, int V, i
         if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = k;
         if (threadIdx.x == 0) found_s = 0x7fffffff;
         __syncthreads();
+        if (step == 0) cluster_wait_acquire();  // every CTA has started: its shared memory may be written
         if (threadIdx.x < 32) {
             uint64_t v = threadIdx.x < WK_NT / 32 ? red[threadIdx.x] : 0;
             v = warp_max_u64(v);
