@@ -416,6 +416,9 @@ struct Kept {                     // the last element kept
     int tok;
     __device__ __forceinline__ bool has(float v, int t) const { return v > x || (v == x && t <= tok); }
 };
+// Everything but -inf: what lies around the row reads as that, with tokens below 0 ahead of a row that does not start on
+// 16 bytes.
+constexpr Kept SP_ALL{-INFINITY, -0x7fffffff - 1};
 
 // What a row needs of the cluster. All functions are called by all threads of the cluster.
 template <typename T, bool HELD>
@@ -1316,7 +1319,7 @@ __device__ int sp_row(const T* row, int V, int seg, SpShared& sh, uint4* data, i
                 top = low = 0.f, reach = 0;
             }
             s.wg = sp_weigher<E::EXACT>(top, f, sh.table);
-            Kept kept{-INFINITY, -1};
+            Kept kept = SP_ALL;
             bool done = false, cut = f.p < 1.f;
             if (short_k) {
                 if (s.sl.only_inf || ord_f32(mine) >= reach)           // (the thread has some)

@@ -1,5 +1,5 @@
-"""Draws and walks of shapes that take the kernel's other ways: clusters of eight CTAs that walk several rows.
-Compared as in test_gpu_filtered."""
+"""Draws and walks of shapes that take the kernel's other ways: clusters of eight CTAs that walk several rows, fewer
+tokens than top-k asks for in rows that start anywhere. Compared as in test_gpu_filtered."""
 import numpy as np
 import pytest
 
@@ -66,3 +66,73 @@ def test_clusters_of_eight_walk_several_rows(dd, C, S, L, V, rows, dtype):
     for got in [dd.verify_filtered(dev, x, mode, L, un, **kw) for _ in range(50)]:
         for k in first:
             assert torch.equal(got[k], first[k]), k
+
+
+def _leave_narrow_borders(dd, V, dtype):
+    """Rows on every SM of which one token far above any other is kept: what a later call must not take for its own
+    border."""
+    x = torch.zeros(1200, V, dtype=DT[dtype], device="cuda")
+    x[:, 0] = 1000.0
+    assert (dd.sample(x, torch.full((1200,), 0.5, device="cuda"), top_p=0.01) == 0).all()
+    assert (dd.sample(x, torch.full((1200,), 0.5, device="cuda"), top_k=V - 1, top_p=0.01) == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("first", range(8))
+def test_fewer_tokens_than_top_k(dd, first, dtype):
+    """Masked rows at every offset from 16 bytes: with k of more than the finite logits all of these are kept, and
+    nothing else."""
+    rng = np.random.default_rng(20 + first)
+    V, R = 3001, 16                                            # (an odd pitch: each row has its own offset)
+    for finite in (1, 60, 296, 1100, 2400):
+        x = np.full((R, V), -np.inf)
+        for r in range(R):
+            x[r, rng.choice(V, finite, replace=False)] = rng.standard_normal(finite) * 2.5
+            if r % 4 == 3:                                     # NaN counts as -inf
+                x[r, np.isinf(x[r]) & (rng.random(V) < 0.5)] = np.nan
+        big = torch.full((R * V + first,), float("inf"), dtype=DT[dtype], device="cuda")
+        rows = big[first:].view(R, V)
+        rows.copy_(torch.from_numpy(x))
+        for kw in (dict(top_k=2500), dict(top_k=2999, temperature=0.7, top_p=0.9), dict(top_k=3000, min_p=0.02),
+                   dict(top_k=np.where(np.arange(R) % 2, 2400, 1025).astype(np.int32))):
+            for _ in range(3):
+                _leave_narrow_borders(dd, V, dtype)
+                tf._check(dd, rows, rng.random(R, dtype=np.float32).clip(0, 1 - 2.0 ** -24), dtype, **kw)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_infinities_under_a_large_top_k(dd, dtype):
+    """The tokens that reach +inf share the weight, whatever k asks for."""
+    rng = np.random.default_rng(30)
+    V, R = 3001, 16
+    x = rng.standard_normal((R, V)) * 2.5
+    at = [rng.choice(V, n, replace=False) for n in np.resize([1, 2, 3, 1200], R)]
+    for r in range(R):
+        x[r, at[r]] = np.inf
+    for kw in (dict(top_k=2500), dict(top_k=2500, top_p=0.5), dict(top_k=1100)):
+        _leave_narrow_borders(dd, V, dtype)
+        got = tf._check(dd, x, rng.random(R, dtype=np.float32).clip(0, 1 - 2.0 ** -24), dtype, **kw)
+        assert all(got[r] in at[r] for r in range(R))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [3001, 20001])
+def test_a_walk_from_a_full_row_into_masked_ones(dd, V, dtype):
+    """The rows of one walk share their CTAs: a border far above the next rows' logits stays with its row."""
+    rng = np.random.default_rng(V)
+    C, S, L = 6, 9, 8
+    t = tf._tree(rng, C, S, L, V, width=1)                     # chains
+    x = np.full((C, S, V), -np.inf)
+    for c in range(C):
+        x[c, 0] = 100.0 + rng.standard_normal(V)
+        for j in range(1, S):
+            x[c, j, rng.choice(V, 40, replace=False)] = rng.standard_normal(40)
+        for j in range(1, int(t["n_nodes"][c])):
+            p = int(t["par"][c, j])
+            x[c, p, t["tok"][c, j]] = 115.0 if p == 0 else 5.0
+    x = torch.from_numpy(x).to(DT[dtype]).cuda()
+    deepest = 0
+    for i in range(8):
+        u = rng.random((C, S), dtype=np.float32).clip(0, 1 - 2.0 ** -24)
+        deepest = max(deepest, int(_walk(dd, t, x, "node", L, u, top_k=2500, top_p=[1.0, 0.95][i % 2]).max()))
+    assert deepest >= 2
