@@ -813,7 +813,8 @@ class PagedCache:
       n_ctx             [C] int32, rows cached before the step's new tokens
       Hq, S             query heads; most new tokens of a request
       q_start           [C + 1] int32 first rows of q (T rows in all); None: S tokens of
-                        every request, or a tree's S slots
+                        every request (the first n of them, one after another, with
+                        tree=dict(n_nodes=n)), or a tree's S slots
       ws                a workspace to use (shared by calls that follow one another on
                         the device; the one of a larger batch will do; cleared, and ordered
                         between streams, by the caller); allocated when None
@@ -945,10 +946,13 @@ class PagedCache:
             return make(shape, dtype=dtype, device=self.device)
 
     def _tree(self, tree, key):
-        """The tree's n_nodes and its mask or pos, or None."""
+        """The tree's n_nodes and its mask or pos (lengths alone: neither), or None."""
         if tree is None:
             return None
         self._t.n_nodes = self._need(tree["n_nodes"], "tree['n_nodes']", torch.int32, self._shapes["C"])
+        if "mask" not in tree and "pos" not in tree:
+            self._t.mask = self._t.pos = None
+            return self._tp
         setattr(self._t, key, self._need(tree[key], f"tree[{key!r}]", torch.uint8 if key == "mask" else torch.int32,
                                          self._shapes[key]))
         return self._tp
@@ -1073,7 +1077,10 @@ class PagedCache:
     def reserve(self, n_new, free, n_free, out=None, stream=None):
         """Pages and rows for a step's new tokens (dartree_paged_reserve): request c wants n_new[c] tokens (0..S,
         int32 [C]) behind its n_ctx[c] rows. The pages it still needs come from the end of the stack free
-        (int32, n_free [1] of them) into the cache's table; a request that does not fit is granted nothing.
+        (int32, n_free [1] of them) into the cache's table; a request that does not fit is granted nothing, and has
+        no place for its tokens: the step's other calls get tree=dict(tree, n_nodes=granted), or
+        tree=dict(n_nodes=granted) where there is no tree (a cache with q_start needs neither), release n_ctx + granted,
+        and a refused request's n_ctx stays as it is when paths are committed.
         The cache's q_start, if it has one, is written. -> dict(granted [C], slot [T] int64, pos [T],
         request [T], n_free [1]); out: the same tensors, made before (n_free may be n_free itself, slot, pos
         and request None)."""

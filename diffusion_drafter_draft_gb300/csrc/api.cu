@@ -655,7 +655,7 @@ int check_paged_cache(const dartree_paged_cache* m, const dartree_tree* tree, bo
     a->q_start = m->q_start;
     if (tree) {
         if (!tree->n_nodes) return DARTREE_EINVAL;
-        a->n_nodes = tree->n_nodes, a->mask = tree->mask, a->pos = tree->pos;
+        a->n_nodes = tree->n_nodes, a->mask = tree->mask, a->pos = tree->pos;   // (neither of the two: a run of tokens)
     }
     return DARTREE_OK;
 }
@@ -687,7 +687,7 @@ int dartree_paged_append(const dartree_paged_params* p, const dartree_paged_toke
     if ((x->gq || x->gk) && !(x->eps > 0.f && isfinite(x->eps))) return DARTREE_EINVAL;
     if (a.C == 0 || a.T == 0) return DARTREE_OK;
     if (int e = check_paged_cache(cache, tree, true, &a)) return e;
-    if (tree && !tree->pos) return DARTREE_EINVAL;
+    if (tree && !tree->pos && tree->mask) return DARTREE_EINVAL;
     const int64_t vec = a.dtype == DARTREE_BF16 ? 8 : 4;
     if (!al16(x->q) || !al16(x->k) || !al16(x->v) || !al16(q_out) || (x->gq && !al16(x->gq)) ||
         (x->gk && !al16(x->gk)) || x->ldq % vec != 0 || x->ldk % vec != 0 || x->ldv % vec != 0 ||
@@ -718,7 +718,7 @@ static int check_paged_scores(const dartree_paged_params* p, const dartree_tree*
         return DARTREE_OK;
     }
     if (int e = check_paged_cache(cache, tree, true, a)) return e;
-    if ((tree && !tree->mask) || !al16(q)) return DARTREE_EINVAL;
+    if ((tree && !tree->mask && tree->pos) || !al16(q)) return DARTREE_EINVAL;
     return DARTREE_OK;
 }
 

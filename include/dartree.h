@@ -344,7 +344,9 @@ DARTREE_API int dartree_tree_attention(const dartree_attn_params* p, const void*
  *                 [q_start[0], q_start[C]) are not used and not written
  *   tree          (q_start NULL only) the new tokens are the S slots of a verification
  *                 tree; slots from tree->n_nodes[c] on are not stored, and their output
- *                 rows (lse too) are zero
+ *                 rows (lse too) are zero. With both pos and mask NULL it is no tree but
+ *                 lengths: the first n_nodes[c] <= S rows of each request are its new
+ *                 tokens, one after another, the others like slots without a node
  * A new token sees all n_ctx cached rows and, of the new ones, those up to its own
  * (causal), or the slots tree->mask [C, S, S] marks.
  * Checked on the device, with DARTREE_EINTERNAL in the status word of ws: lengths below
@@ -541,6 +543,12 @@ DARTREE_API int dartree_paged_commit_weights(const dartree_paged_params* p, cons
  * (the i-th page that the step takes is free_pages[n_free - 1 - i]). Requests are served in their
  * order; one whose pages, tokens (T rows of q with q_start) or row of the block table do not
  * suffice is granted nothing, and those behind it are served from what is left.
+ * A request that was granted nothing has no rows for its tokens: its entries of the block table behind its cached
+ * rows are whatever lay there, pages that are another request's by now among them. So what the step's other calls
+ * are given is `granted`, not n_new: as tree->n_nodes of dartree_paged_append, the attention and dartree_paged_weights
+ * (with pos and mask, or without both where there is no tree; with q_start the request has no rows of q as it is), and
+ * n_ctx + granted as dartree_paged_release's n_held. dartree_paged_commit and dartree_verify* take a root's row of
+ * every request: what they give for a refused one is not used (its n_ctx stays).
  *   table       [C, max_pages] entries of the new pages written (the cache's; others not touched)
  *   n_ctx       [C] rows cached
  *   n_new       [C] tokens wanted, 0..S (tree->n_nodes, say)
