@@ -157,17 +157,16 @@ __device__ __forceinline__ void st_dsmem_u32(uint32_t addr, uint32_t v) {
 
 // The weight of x in units of 2^-43: with t = (m - x) 256 log2(e) / T, K = -round(t), rho = -t - K,
 //   w = 2^(K div 256) 2^(K mod 256 / 256) (1 + rho L + (rho L)^2 / 2 + (rho L)^3 / 6),   L = ln 2 / 256, |rho L| < 2^-9.5
-// The difference (fp32; of bf16 values it is exact but for tiny ones), t and the table are pairs of floats, so
-// what is left is the rounding of rho L and of its product with the table, 2^-34 of the weight, different for
-// every x: no bias. A weight is then rounded twice to integers of 2^-22 and, what remains, of 2^-43, by adding
-// 3 and 1.5 * 2^-20: the sums' low bits are the integers. Two elements at a time (fma.rn.f32x2): 19 issue slots
-// an element for bf16, 22 for fp32. The table has a copy for every eighth lane, so that a look-up costs three accesses
-// of the shared memory's banks (one copy of 1024 entries: six, and 25 instead of 20 slots' time an element).
+// The difference, t and the table are pairs of floats, so what is left is the rounding of rho L and of its product with
+// the table, 2^-34 of the weight, different for every x: no bias. (bf16 values, too: the difference of a large maximum
+// and a value near zero, or the other way round, is no float.) A weight is then rounded twice to integers of 2^-22 and,
+// what remains, of 2^-43, by adding 3 and 1.5 * 2^-20: the sums' low bits are the integers. Two elements at a time
+// (fma.rn.f32x2): 22 issue slots an element. The table has a copy for every eighth lane, so that a look-up costs three
+// accesses of the shared memory's banks (one copy of 1024 entries: six, and 25 instead of 20 slots' time an element).
 // Below xlo, where the weight is none, x counts as xlo (t of at least 62 * 256). Rows in which xlo cannot lie between
 // two floats, or differences overflow, take the same steps one element at a time (`slow`).
 constexpr uint32_t SP_C1 = 0x40400000u;   // 3.0
 constexpr uint32_t SP_C2 = 0x35c00000u;   // 1.5 * 2^-20
-template <bool EXACT>             // differences of two values are
 struct Weigher {
     float m, ch, cl, xlo;
     bool slow;
@@ -180,8 +179,7 @@ struct Weigher {
     // integers of 2^-22 and of 2^-43 of d = m - x, off by e
     __device__ __forceinline__ void core1(float d, float e, uint32_t& i1, uint32_t& i2) const {
         const float th = __fmul_rn(d, -ch);
-        float tl = __fmaf_rn(d, cl, __fmaf_rn(d, ch, th));
-        if (!EXACT) tl = __fmaf_rn(e, ch, tl);
+        const float tl = __fmaf_rn(e, ch, __fmaf_rn(d, cl, __fmaf_rn(d, ch, th)));
         const float y = __fadd_rn(th, 12582912.0f);
         const float rho = __fadd_rn(__fadd_rn(th, __fsub_rn(12582912.0f, y)), -tl);
         const float em = __fmul_rn(rho, __fmaf_rn(rho, __fmaf_rn(rho, L3, L2), L));
@@ -201,7 +199,7 @@ struct Weigher {
         if (slow && !(d * ch < 15872.0f)) return 0;
         if (!slow) x = fmaxf(x, xlo), d = __fsub_rn(m, x);
         const float bb = __fsub_rn(d, m);
-        const float e = EXACT ? 0.f : __fsub_rn(__fsub_rn(m, __fsub_rn(d, bb)), __fadd_rn(x, bb));
+        const float e = __fsub_rn(__fsub_rn(m, __fsub_rn(d, bb)), __fadd_rn(x, bb));
         uint32_t i1, i2;
         core1(d, e, i1, i2);
         return whole(i1, i2);
@@ -213,11 +211,8 @@ struct Weigher {
         const uint64_t X = pair(x0, x1), MG = pair(12582912.0f, 12582912.0f), C1 = pair(SP_C1, SP_C1);
         const uint64_t d = fma2(X, N1, M);
         const uint64_t th = mul2(d, NCH);
-        uint64_t tl = fma2(d, CL, fma2(d, CH, th));
-        if (!EXACT) {
-            const uint64_t bb = fma2(M, N1, d), e1 = fma2(fma2(bb, N1, d), N1, M);
-            tl = fma2(fma2(add2(X, bb), N1, e1), CH, tl);
-        }
+        const uint64_t bb = fma2(M, N1, d), e1 = fma2(fma2(bb, N1, d), N1, M);
+        const uint64_t tl = fma2(fma2(add2(X, bb), N1, e1), CH, fma2(d, CL, fma2(d, CH, th)));
         const uint64_t y = add2(th, MG);
         const uint64_t rho = fma2(tl, N1, add2(th, fma2(y, N1, MG)));
         const uint64_t em = mul2(rho, fma2(rho, fma2(rho, pair(L3, L3), pair(L2, L2)), pair(L, L)));
@@ -277,11 +272,10 @@ struct Weigher {
     }
 };
 // Of row maximum m under f.
-template <bool EXACT>
-__device__ __forceinline__ Weigher<EXACT> sp_weigher(float m, const Filter& f, const float2* table) {
+__device__ __forceinline__ Weigher sp_weigher(float m, const Filter& f, const float2* table) {
     const float below = __uint_as_float(m > 0.f ? __float_as_uint(m) - 1u : m < 0.f ? __float_as_uint(m) + 1u : 0x80000001u);
     const float reach = 15872.0f / f.ch;                   // 62 * 256
-    Weigher<EXACT> w{m, f.ch, f.cl, fminf(m - reach, below), false, table + (threadIdx.x & 7)};
+    Weigher w{m, f.ch, f.cl, fminf(m - reach, below), false, table + (threadIdx.x & 7)};
     w.slow = !(fabsf(m) < 1e30f && reach < 1e30f && reach > 1e-30f && (m - below) * f.ch < 15872.0f);
     return w;
 }
@@ -289,7 +283,6 @@ __device__ __forceinline__ Weigher<EXACT> sp_weigher(float m, const Filter& f, c
 template <typename T> struct SpElem;
 template <> struct SpElem<float> {
     static constexpr int VEC = 4;
-    static constexpr bool EXACT = false;   // differences of values
     static __device__ __forceinline__ void widen(const uint4& v, float (&x)[4]) {
         x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
     }
@@ -305,7 +298,6 @@ template <> struct SpElem<float> {
 };
 template <> struct SpElem<bf16_t> {
     static constexpr int VEC = 8;
-    static constexpr bool EXACT = true;
     static __device__ __forceinline__ void widen(const uint4& v, float (&x)[8]) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -428,7 +420,7 @@ struct Sampler {
     SpShared& sh;
     Slice<T, HELD> sl;
     uint32_t S, cr;               // CTAs, this one
-    Weigher<E::EXACT> wg;
+    Weigher wg;
 
     template <typename F>
     __device__ __forceinline__ void each(F f) const {          // f(x, token), this thread's elements
@@ -717,10 +709,10 @@ struct Sampler {
                 for (int e = 0; e < VEC; ++e) sum += x[e] > -INFINITY ? w[e] : 0;
             } else {
                 wg.template add<VEC>(x, i1, i2);
-                if (!HELD && ++n == SP_FLUSH / VEC) sum += Weigher<E::EXACT>::whole(i1, i2), i1 = i2 = 0, n = 0;
+                if (!HELD && ++n == SP_FLUSH / VEC) sum += Weigher::whole(i1, i2), i1 = i2 = 0, n = 0;
             }
         });
-        return sum + Weigher<E::EXACT>::whole(i1, i2);
+        return sum + Weigher::whole(i1, i2);
     }
 
     // The stretch of sums[S][SP_WARPS] that holds the goal-th unit (u of the whole, when u is not null), and the units
@@ -940,12 +932,12 @@ struct Sampler {
                 take(sl.value(sl.first + i * VEC + e), sl.first + i * VEC + e);
             }
             if (!HELD && ++held == SP_FLUSH / VEC) {
-                t_sum += Weigher<E::EXACT>::whole(i1, i2), a_sum += Weigher<E::EXACT>::whole(a1, a2);
+                t_sum += Weigher::whole(i1, i2), a_sum += Weigher::whole(a1, a2);
                 i1 = i2 = a1 = a2 = 0, held = 0;
             }
         });
-        const uint64_t total = sp_warp_sum(t_sum + Weigher<E::EXACT>::whole(i1, i2));
-        const uint64_t above = sp_warp_sum(a_sum + Weigher<E::EXACT>::whole(a1, a2));
+        const uint64_t total = sp_warp_sum(t_sum + Weigher::whole(i1, i2));
+        const uint64_t above = sp_warp_sum(a_sum + Weigher::whole(a1, a2));
         if (lane == 0) {
             st_dsmem_u64(dsmem_addr(&sh.sums[cr][wid], 0), total);
             st_dsmem_u64(dsmem_addr(&sh.above[cr][wid], 0), above);
@@ -1300,7 +1292,7 @@ __device__ int sp_row(const T* row, int V, int seg, SpShared& sh, uint4* data, i
     int tok = -1;
     if (top > -INFINITY) {
         Sampler<T, HELD> s{sh, Slice<T, HELD>{HELD ? data : mem.v, row, nv, lo - shift, lo, hi, false}, S, cr,
-                           Weigher<E::EXACT>{}};
+                           Weigher{}};
         if (f.greedy) {                                    // the maximum's lowest token
             uint32_t best = 0xffffffffu;
             if (mine == top) s.each([&](float x, int t) { if (x == top) best = min(best, uint32_t(t)); });
@@ -1318,7 +1310,7 @@ __device__ int sp_row(const T* row, int V, int seg, SpShared& sh, uint4* data, i
                 s.sl.only_inf = true;
                 top = low = 0.f, reach = 0;
             }
-            s.wg = sp_weigher<E::EXACT>(top, f, sh.table);
+            s.wg = sp_weigher(top, f, sh.table);
             Kept kept = SP_ALL;
             bool done = false, cut = f.p < 1.f;
             if (short_k) {

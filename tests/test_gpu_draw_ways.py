@@ -1,5 +1,6 @@
 """Draws and walks of shapes that take the kernel's other ways: clusters of eight CTAs that walk several rows, fewer
-tokens than top-k asks for in rows that start anywhere. Compared as in test_gpu_filtered."""
+tokens than top-k asks for in rows that start anywhere, values whose difference is no float. Compared as in
+test_gpu_filtered."""
 import numpy as np
 import pytest
 
@@ -136,3 +137,28 @@ def test_a_walk_from_a_full_row_into_masked_ones(dd, V, dtype):
         u = rng.random((C, S), dtype=np.float32).clip(0, 1 - 2.0 ** -24)
         deepest = max(deepest, int(_walk(dd, t, x, "node", L, u, top_k=2500, top_p=[1.0, 0.95][i % 2]).max()))
     assert deepest >= 2
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("m,lo,hi,T", [(20.0, -9.1e-7, 9.1e-7, 10.0), (100.0, -3e-6, 3e-6, 50.0), (-1e-5, -6.0, -9.0, 4.0),
+                                       (-3e-6, -3.5, -1.75, 1.0)])
+def test_differences_that_are_no_floats(dd, m, lo, hi, T, dtype):
+    """A maximum and values so far apart in magnitude that fp32 rounds their difference: numbers u between the border of
+    two runs of such values and where weights of rounded differences would put it."""
+    V = 512
+    x = torch.full((V,), lo, dtype=torch.float64)
+    tried = 0
+    for n in (3, 4, 6, 8, 11, 16, 23, 32, 45, 64, 100, 200):
+        x[:n], x[n:], x[V // 2] = hi, lo, m
+        h = x.to(DT[dtype]).double().numpy()
+        top = h.max()
+        exact, rounded = (np.cumsum(np.exp(-d / T)) for d in (top - h, (top - h).astype(np.float32).astype(np.float64)))
+        a, b = exact[n - 1] / exact[-1], rounded[n - 1] / rounded[-1]
+        margin = 2 * V * 2.0 ** -42
+        u = np.float32(0.5 * (a + b))
+        if min(abs(u - a), abs(u - b)) < 2 * margin or not min(a, b) < u < max(a, b):
+            continue                                           # (no float lies between)
+        tried += 1
+        tf._check(dd, x[None].to(DT[dtype]).cuda(), np.array([u]), dtype, temperature=T)
+        tf._check(dd, x[None].to(DT[dtype]).cuda(), np.array([u]), dtype, temperature=T, top_p=float(np.float32(0.9999999)))
+    assert tried >= 3
