@@ -153,10 +153,7 @@ __global__ void __launch_bounds__(128 + 128 * NT, NT == 1 ? 2 : 1)
         r = PagedRequest{u.q0, u.n, u.keys, u.keys};
     } else {
         r = paged_request(a, c, bad);
-        if (SH) {
-            kb = paged_shared_rows(x, c);
-            bad |= kb > r.n_old;
-        }
+        if (SH) kb = paged_shared_rows(x, c, r.n_old, bad);
         bad = bad && tp == 0;
     }
     if (bad && threadIdx.x == 0 && g == 0) set_status(a.status, DARTREE_EINTERNAL);

@@ -42,8 +42,9 @@ __device__ __forceinline__ bool paged_in_group(const PgArgs& x, int c) {
     return c >= x.s.start[0] && c < x.s.start[x.s.G];
 }
 
-// Rows that request c shares with its group, in whole pages (0: no group). By a whole warp, the same for all lanes.
-__device__ __forceinline__ int paged_shared_rows(const PgArgs& x, int c) {
+// Rows that request c shares with its group, in whole pages (0: no group); `bad` is set where the group's are past the
+// request's `n_old` cached ones. By a whole warp, the same for all lanes.
+__device__ __forceinline__ int paged_shared_rows(const PgArgs& x, int c, int n_old, bool& bad) {
     const int lane = threadIdx.x & 31;
     int n = 0, rows = 0;                                  // starts up to c; the last one's rows
     for (int j = 0; j <= x.s.G; j += 32) {                // (starts and rows at once: one round of loads for 31 groups)
@@ -55,6 +56,7 @@ __device__ __forceinline__ int paged_shared_rows(const PgArgs& x, int c) {
         if (b != 0xffffffffu) break;
     }
     if (n == 0 || n > x.s.G) return 0;
+    bad |= rows > n_old;
     const int64_t cap = int64_t(x.a.max_pages) << x.a.log2_page;
     return int(min(int64_t(max(rows, 0)), cap)) & ~(x.a.page - 1);
 }

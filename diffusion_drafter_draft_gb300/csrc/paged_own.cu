@@ -116,9 +116,8 @@ __global__ void __launch_bounds__(PO_NT, 2)
     auto item_of = [&](int it) -> Item {
         Item t;
         t.c = it / a.Hkv, t.g = it - t.c * a.Hkv;
-        t.kb = paged_shared_rows(x, t.c);
         t.r = paged_request(a, t.c, t.bad);
-        t.bad |= t.kb > t.r.n_old;
+        t.kb = paged_shared_rows(x, t.c, t.r.n_old, t.bad);
         t.nblk = t.r.n_new > 0 ? (max(t.r.n_keys - t.kb, 0) + PF_BM - 1) / PF_BM : 0;
         return t;
     };
