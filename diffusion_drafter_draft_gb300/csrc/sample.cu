@@ -94,9 +94,9 @@ struct Filter {
     uint64_t cut;                 // weights below it cannot be reached by p of the whole
     bool greedy;
 };
-// x in [0, 1) times 2^bits, rounded down (or up): doubles are slow here.
+// x in [0, 1) times 2^bits, rounded down (or up): doubles are slow here. (-0 is 0.)
 __device__ __forceinline__ uint64_t sp_fixed(float x, int bits, bool up) {
-    const uint32_t b = __float_as_uint(x);
+    const uint32_t b = __float_as_uint(x) & 0x7fffffffu;
     const int e = int(b >> 23);
     uint64_t m = e ? (b & 0x7fffffu) | 0x800000u : b & 0x7fffffu;      // x = m 2^(e - 150)
     const int s = (e ? e : 1) - 150 + bits;

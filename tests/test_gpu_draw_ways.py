@@ -162,3 +162,17 @@ def test_differences_that_are_no_floats(dd, m, lo, hi, T, dtype):
         tf._check(dd, x[None].to(DT[dtype]).cuda(), np.array([u]), dtype, temperature=T)
         tf._check(dd, x[None].to(DT[dtype]).cuda(), np.array([u]), dtype, temperature=T, top_p=float(np.float32(0.9999999)))
     assert tried >= 3
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_minus_zero_is_zero(dd, dtype):
+    """u and settings of -0, as numbers and as tensors, are settings: they draw what 0 draws."""
+    rng = np.random.default_rng(40)
+    R = 6
+    x = rng.standard_normal((R, 3001))
+    z, f = np.full(R, -0.0, np.float32), rng.random(R, dtype=np.float32).clip(0, 1 - 2.0 ** -24)
+    for kw in (dict(), dict(top_p=0.9), dict(top_k=50), dict(top_k=2000), dict(min_p=0.05)):
+        assert (tf._check(dd, x, z, dtype, **kw) == tf._check(dd, x, -z, dtype, **kw)).all()
+    for key in ("temperature", "top_p", "min_p"):
+        for value in (-0.0, z):
+            tf._check(dd, x, f, dtype, **{key: value})
