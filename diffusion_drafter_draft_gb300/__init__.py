@@ -522,8 +522,9 @@ def verify_filtered(tree, target, rows: int, L: int, u, temperature=1.0, top_k=0
     for k in ("tok", "par", "depth"):
         _need(tree[k], f"tree[{k!r}]", torch.int32, (C, S))
     _need(tree["n_nodes"], "tree['n_nodes']", torch.int32, (C,))
-    _same_device(dev, u=u, out=out["path"] if out else None, ws=ws,
-                 **{k: tree[k] for k in ("tok", "par", "depth", "n_nodes")})
+    _same_device(dev, u=u, ws=ws, **{k: tree[k] for k in ("tok", "par", "depth", "n_nodes")})
+    if out is not None:
+        _same_device(dev, **{k: out[k] for k in ("accepted_len", "path", "bonus")})
     with torch.cuda.device(dev):
         with torch.cuda.stream(stream):
             if out is None:
