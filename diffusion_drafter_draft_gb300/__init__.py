@@ -481,6 +481,12 @@ def _same_device(device, **tensors) -> None:
             raise ValueError(f"{name} must be on {device}, got {t.device}")
 
 
+def _small(name, *sizes) -> None:
+    """Sizes beyond the entry point's int are refused (a ctypes int would keep their low 32 bits)."""
+    if max(sizes) >= 2 ** 31:
+        raise DartreeError(EUNSUPPORTED, name)
+
+
 def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None, ws=None, stream=None):
     """A token for each row of logits [rows, V] (rows may lie further apart) under temperature, top-k, top-p and
     min-p, from one uniform number u [rows] (float32 in [0, 1)) a row (dartree_sample) -> int32 [rows]; -1 for a
@@ -488,6 +494,7 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None, 
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2 or not logits.is_cuda:
         raise ValueError("logits must be a CUDA tensor [rows, V]")
     rows, V = logits.shape
+    _small("dartree_sample", rows, V)
     ld = logits.stride(0) if rows > 1 else V
     if logits.stride(1) != 1 and V > 1:
         raise ValueError("the logits of a row must be contiguous")
@@ -516,6 +523,7 @@ def verify_filtered(tree, target, rows: int, L: int, u, temperature=1.0, top_k=0
     C, S = tree["tok"].shape
     V = target.shape[-1]
     n = L if rows == ROWS_PER_POSITION else S
+    _small("dartree_verify_filtered", C, L, S, V)
     _need(target, "target", None, (C, n, V))
     _need(u, "u", torch.float32, (C, n))
     dev = target.device
