@@ -222,7 +222,9 @@ def _prepare_attention(case, seed):
     if own:
         import diffusion_drafter_draft_gb300 as dd
         s["cache"] = dd.PagedCache(s["k"], s["v"], s["table"], s["n_ctx"], Hq, S, T=s["T"], q_start=s["q_start"])
-        s["shared"] = s["cache"].shared(s["start"], s["rows"], most_rows=case["shared"], most_rest=case["rest"] + page)
+        # (behind the shared pages: what a prefix has in its last page, the rest and the new tokens)
+        s["shared"] = s["cache"].shared(s["start"], s["rows"], most_rows=case["shared"],
+                                        most_rest=case["rest"] + S + page - 1)
     return s
 
 
