@@ -9,7 +9,7 @@
 //
 // A token hangs on the last digits of these sums: a sum over 150 thousand fp32 weights, off by
 // 1e-7 of itself, lands on a neighbour wherever weights are smaller than that. So weights are
-// integers, 2^43 for the largest, off by about half a unit and 2^-33 of themselves at random (sp_weigh
+// integers, 2^43 for the largest, off by about half a unit and 2^-34 of themselves at random (Weigher
 // below), and sums are exact 64-bit integers, the same in any order and for any split of the row.
 //
 // One cluster per row; each CTA keeps its slice in shared memory, so the logits are read once.
@@ -294,7 +294,6 @@ template <> struct SpElem<float> {
                           __float_as_uint(clean(x[3])));
     }
     static __device__ __forceinline__ float get(const float* p) { return clean(*p); }
-    static __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 };
 template <> struct SpElem<bf16_t> {
     static constexpr int VEC = 8;
@@ -316,7 +315,6 @@ template <> struct SpElem<bf16_t> {
         return make_uint4(clean2(v.x), clean2(v.y), clean2(v.z), clean2(v.w));
     }
     static __device__ __forceinline__ float get(const bf16_t* p) { return fmaxf(to_float(*p), -INFINITY); }
-    static __device__ __forceinline__ void put(bf16_t* p, float x) { *p = bf16_t{uint16_t(__float_as_uint(x) >> 16)}; }
 };
 
 // A CTA's slice [lo, hi) of a row as `nv` vectors of 16 bytes, element e of vector v being token first + v * VEC + e
