@@ -88,7 +88,8 @@ struct SampleArgs {
 struct Filter {
     float T, p, least;
     int k;
-    float ch, cl;                 // 256 log2(e) / T as a pair
+    float up;                     // 2^64 for a T below 2^-64, 2^-64 for one above 2^64 (the next would lose bits), else 1
+    float ch, cl;                 // 256 log2(e) / (T up) as a pair
     uint64_t u, share;            // u and (below 1) p times 2^64
     uint64_t wmin;                // least weight that min-p keeps
     uint64_t cut;                 // weights below it cannot be reached by p of the whole
@@ -164,11 +165,12 @@ __device__ __forceinline__ void st_dsmem_u32(uint32_t addr, uint32_t v) {
 // (fma.rn.f32x2): 22 issue slots an element. The table has a copy for every eighth lane, so that a look-up costs three
 // accesses of the shared memory's banks (one copy of 1024 entries: six, and 25 instead of 20 slots' time an element).
 // Below xlo, where the weight is none, x counts as xlo (t of at least 62 * 256). Rows in which xlo cannot lie between
-// two floats, or differences overflow, take the same steps one element at a time (`slow`).
+// two floats, or differences overflow, and temperatures beyond 2^-64 .. 2^64, with which differences are scaled, take the
+// same steps one element at a time (`slow`).
 constexpr uint32_t SP_C1 = 0x40400000u;   // 3.0
 constexpr uint32_t SP_C2 = 0x35c00000u;   // 1.5 * 2^-20
 struct Weigher {
-    float m, ch, cl, xlo;
+    float m, ch, cl, xlo, up;
     bool slow;
     const float2* table;
     static constexpr float L = 2.7076061740622863e-3f, L2 = 3.6655656e-6f, L3 = 3.3083027e-9f;   // ln 2 / 256, L^2/2, L^3/6
@@ -196,12 +198,12 @@ struct Weigher {
     __device__ __forceinline__ uint64_t one(float x) const {
         if (x == m) return uint64_t(1) << SP_Q;
         float d = __fsub_rn(m, x);
-        if (slow && !(d * ch < 15872.0f)) return 0;
+        if (slow && !(d * up * ch < 15872.0f)) return 0;
         if (!slow) x = fmaxf(x, xlo), d = __fsub_rn(m, x);
         const float bb = __fsub_rn(d, m);
         const float e = __fsub_rn(__fsub_rn(m, __fsub_rn(d, bb)), __fadd_rn(x, bb));
         uint32_t i1, i2;
-        core1(d, e, i1, i2);
+        core1(d * up, e * up, i1, i2);
         return whole(i1, i2);
     }
     __device__ __noinline__ uint64_t one_call(float x) const { return one(x); }   // (rare places)
@@ -275,8 +277,8 @@ struct Weigher {
 __device__ __forceinline__ Weigher sp_weigher(float m, const Filter& f, const float2* table) {
     const float below = __uint_as_float(m > 0.f ? __float_as_uint(m) - 1u : m < 0.f ? __float_as_uint(m) + 1u : 0x80000001u);
     const float reach = 15872.0f / f.ch;                   // 62 * 256
-    Weigher w{m, f.ch, f.cl, fminf(m - reach, below), false, table + (threadIdx.x & 7)};
-    w.slow = !(fabsf(m) < 1e30f && reach < 1e30f && reach > 1e-30f && (m - below) * f.ch < 15872.0f);
+    Weigher w{m, f.ch, f.cl, fminf(m - reach, below), f.up, false, table + (threadIdx.x & 7)};
+    w.slow = !(f.up == 1.f && fabsf(m) < 1e30f && reach < 1e30f && (m - below) * f.ch < 15872.0f);
     return w;
 }
 
@@ -661,7 +663,8 @@ struct Sampler {
     __device__ Take take_of(const Kept& kept, const Filter& f) const {
         Take t{kept, kept.x, kept.x};
         if (f.wmin) {
-            const float mid = wg.m + f.T * logf(f.least), slack = 1e-4f * f.T + 4e-7f * fabsf(wg.m);
+            // (a few steps of the smallest floats, where the products are none)
+            const float mid = wg.m + f.T * logf(f.least), slack = 1e-4f * f.T + 4e-7f * fabsf(wg.m) + 1e-44f;
             t.sure = fmaxf(t.sure, mid + slack), t.never = fmaxf(t.never, mid - slack);
         }
         return t;
@@ -1354,9 +1357,11 @@ __device__ __forceinline__ void sp_filter(const SampleArgs& a, int r, float u, S
     f.greedy = f.T == 0.f || f.k == 1 || f.p == 0.f;
     // 256 / ln 2 (a pair) by T: the quotient, and the remainder's
     constexpr float KH = 369.329925537109375f, KL = 4.9304653e-6f;
-    const float T = f.T > 0.f ? f.T : 1.f;
-    f.ch = fminf(__fdiv_rn(KH, T), 1e37f);
-    f.cl = f.ch < 1e37f ? __fdiv_rn(__fmaf_rn(-f.ch, T, KH) + KL, T) : 0.f;
+    constexpr float BIG = 18446744073709551616.0f;         // 2^64
+    f.up = f.T < 1.0f / BIG ? BIG : f.T > BIG ? 1.0f / BIG : 1.0f;
+    const float T = f.T > 0.f ? f.T * f.up : 1.f;
+    f.ch = __fdiv_rn(KH, T);
+    f.cl = __fdiv_rn(__fmaf_rn(-f.ch, T, KH) + KL, T);
     f.u = sp_fixed(u, 64, false), f.share = f.p < 1.f ? sp_fixed(f.p, 64, true) : 0;
     f.wmin = f.least < 1.f ? sp_fixed(f.least, SP_Q, true) : uint64_t(1) << SP_Q;
     f.cut = sp_fixed(0.99f * (1.0f - f.p) / float(a.V), SP_Q, false);

@@ -176,3 +176,17 @@ def test_minus_zero_is_zero(dd, dtype):
     for key in ("temperature", "top_p", "min_p"):
         for value in (-0.0, z):
             tf._check(dd, x, f, dtype, **{key: value})
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1.4e-45, 3e-42, 1e-39, 2e-36, 1e-30, 5e-20, 6e-20, 1e-10, 1e18, 2e19, 1e30, 2e37])
+def test_logits_of_the_temperatures_size(dd, T, dtype):
+    """Temperatures from the smallest float to the largest ones, logits a few of them apart."""
+    T = float(np.float32(T))
+    rng = np.random.default_rng(50)
+    quantum = max(T, 2.0 ** -133) if dtype == "bf16" else T    # (the smallest bf16)
+    x = np.stack([rng.integers(0, 8, 3001) * quantum, -rng.integers(0, 60, 3001) * quantum * 0.5,
+                  np.where(rng.random(3001) < 0.01, 9 * quantum, 0.0), rng.standard_normal(3001) * 3 * quantum])
+    for kw in (dict(), dict(top_p=0.9), dict(top_k=40), dict(top_k=2000, top_p=0.97), dict(min_p=0.3), dict(top_p=0.8, min_p=0.01)):
+        for _ in range(4):
+            tf._check(dd, x, rng.random(4, dtype=np.float32).clip(0, 1 - 2.0 ** -24), dtype, temperature=T, **kw)
