@@ -248,8 +248,9 @@ typedef struct {
 /* A token for each row of logits under `f`, from one uniform number u in [0, 1) a row: the lowest token at
  * which the sum of the kept w_0 .. w_v passes u times their whole sum. -inf is never drawn, nor is
  * NaN (counted as -inf); where the maximum is +inf, the tokens that reach it share the weight; a row
- * of -inf alone gives -1. Sums are exact sums of weights rounded to 2^-43 of the largest:
- * a row's token does not depend on the batch it is in.
+ * of -inf alone gives -1. Sums are exact sums of weights rounded to 2^-43 of the largest (and
+ * off by about 2^-34 of themselves before that), and top-p and min-p go by these weights, too: what lies nearer to
+ * a border than that may fall on either side of it. A row's token does not depend on the batch it is in.
  *   logits  [rows, V], consecutive rows ld >= V elements apart, aligned to their type
  *   f       one request to a row
  *   u       [rows]
@@ -451,9 +452,9 @@ DARTREE_API int dartree_paged_attention(const dartree_paged_params* p, const voi
  *               batch is expected to have at most, 0: as many as the block table holds. They size the
  *               workspace and decide how the work is split, not the results; where sharing does not pay by
  *               them, the call is dartree_paged_attention.
- * Checked on the device, with DARTREE_EINTERNAL in the status word and unspecified results: start not
- * ascending or outside 0..C, rows below zero, past the table or past n_ctx, besides what dartree_paged_attention
- * checks. Other arguments and errors as there; the workspace is dartree_paged_shared_workspace_bytes
+ * Checked on the device where rows are shared (the plain call reads no group), with DARTREE_EINTERNAL in the
+ * status word and unspecified results: start not ascending or outside 0..C, rows below zero, past the table or
+ * past n_ctx, besides what dartree_paged_attention checks. Other arguments and errors as there; the workspace is dartree_paged_shared_workspace_bytes
  * (that of these sizes; nothing is promised for smaller batches). */
 typedef struct {
     int G;                  /* groups, 0..C */
