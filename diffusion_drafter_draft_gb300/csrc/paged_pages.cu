@@ -12,8 +12,8 @@
 // Where the requests of a turn do not all fit, one warp goes through them, 32 at a time: those
 // that want more than is left can never fit and drop out, the others are granted up to the
 // first whose prefix does not fit; a few rounds a group.
-// 64 trees of 65 slots 4.8 us in a graph (9.7 with the host's time of calls one after another), 512 requests of up to
-// 128 tokens, a quarter refused, 13.3 (12.9), 64 releases 3.2 (8.0).
+// 64 trees of 65 slots 5.4 us in a graph (10.6 with the host's time of calls one after another), 512 requests of up to
+// 128 tokens, a quarter refused, 13.6 (13.5), 64 releases 3.5 (8.5).
 #include "paged.cuh"
 
 namespace dartree {
