@@ -16,7 +16,8 @@
 //   warp 4      producer: keys and values through a ring of ST stages; q when the scores before are done
 //   warp 5      issues S^T, a block ahead of the softmax, into one of two buffers
 // Blocks are numbered through all of a CTA's requests, so that the barriers' phases go on. Rows past the end may hold
-// anything: their scores are masked and their values zeroed. P is rounded to bf16, everything else is fp32. Every wait is
+// anything: their scores are masked and their values zeroed. P is rounded to bf16 as in paged_attn.cu and for its reason
+// (outputs 2.3e-3 from 64 bits, relative, where one rounding to bf16 is 1.7e-3); everything else is fp32. Every wait is
 // bounded; one that runs out records DARTREE_ETIMEOUT and ends the CTA's work.
 // 64 tokens behind 16384 shared rows and up to 512 of their own (134 MB, 20 us at the memory's rate): 51.3 us with the
 // shared rows in 64 CTAs (38 us) and three pairs to each of 171 others; 55.6 before the joins fetched the chunks' O ahead of
